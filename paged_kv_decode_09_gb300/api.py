@@ -1,4 +1,5 @@
-"""ctypes binding of libpkv.so (C ABI in include/pkv.h).
+"""ctypes binding of libpkv.so (C ABI in include/pkv.h, include/pkv_chunk.h and
+include/pkv_alloc.h).
 
 Argument marshalling only: every function checks tensor dtypes, shapes and
 devices, passes raw device pointers and the current torch CUDA stream to the
@@ -42,7 +43,7 @@ def library_path() -> str:
     return _LIB_PATH
 
 
-_vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_vp, _i, _sz, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
 _SIGS = {
     "kv_pool_bytes": ([_i, _i, _i, _i, _i, _i], _sz),
     "kv_pool_create": ([ctypes.POINTER(_vp), _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp], _i),
@@ -84,6 +85,15 @@ _SIGS = {
                                    _vp, _sz, _i, _vp], _i),
     "pkv_decode_step_mq": ([_vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, ctypes.c_float,
                             _vp, _vp, _sz, _i, _vp], _i),
+    "kv_rope_append": ([_vp, _i, _vp, _ll, _vp, _ll, _vp, _ll, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _i,
+                        _vp, _i, _vp, _i, _vp, _i, _i, _vp], _i),
+    "paged_chunk_workspace_bytes": ([_vp, _i, _i], _sz),
+    "paged_chunk_default_chunks": ([_vp, _i, ctypes.POINTER(_i)], _i),
+    "paged_chunk_attention": ([_vp, _i, _vp, _ll, _i, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp,
+                               _sz, _i, _vp], _i),
+    "paged_attention_mass": ([_vp, _i, _vp, _ll, _i, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _i, _vp,
+                              _vp, _i, _vp], _i),
+    "kv_evict": ([_vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp], _i),
     "pkv_status_string": ([_i], ctypes.c_char_p),
     "pkv_last_error_message": ([], ctypes.c_char_p),
 }
@@ -411,6 +421,196 @@ def paged_decode_combine(seq_lens, n_q_heads: int, n_kv_heads: int, bt_stride: i
                                       workspace.numel(),
                                       _ptr(out), _stream(stream)), "paged_decode_combine")
     return out
+
+
+# ------------------------------------------------------------- long prompts ----
+_KIND = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+
+
+class _Scores(ctypes.Structure):  # pkv_scores
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", _vp),
+                ("prefix_lens", _vp)]
+
+
+def _scores(scale, softcap, slopes, prefix_lens, n_q, rows, device):
+    if slopes is not None:
+        _need(slopes, torch.float32, "slopes", (n_q,), device)
+    if prefix_lens is not None:
+        _need(prefix_lens, torch.int32, "prefix_lens", (rows,), device)
+    return _Scores(float(scale), float(softcap), _ptr(slopes), _ptr(prefix_lens))
+
+
+def _chunk_rows(cu_seqlens, block_table, seq_lens, device):
+    rows, stride = _rows(block_table, seq_lens, device)
+    _need(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), device)
+    return rows, stride
+
+
+def _token_array(t, name, tokens, heads, dtype, device):
+    """Checks a token array [tokens][heads][128] whose tokens may be strided; its stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 3 or t.shape[2] != HEAD_DIM or (tokens is not None and t.shape[0] != tokens) or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{tokens}][{heads}][{HEAD_DIM}]")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != HEAD_DIM)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+
+
+def _on(pool):
+    """The pool's device as the current one: launches go to the current device."""
+    return torch.cuda.device(pool.device)
+
+
+def kv_rope_append(pool: KVPool, layer: int, q, k, v, positions, inv_freq, sections, cu_seqlens, block_table,
+                   seq_lens, q_out=None, interleaved: bool = False, stream=None):
+    """Rotate a ragged chunk's queries and keys and store its keys and values (kv_rope_append in
+    pkv_chunk.h).  q [tokens][n_q][128] (None: keys and values only), k and v [tokens][n_kv][128] of one
+    type (f16, bf16, f32), tokens strided at will; positions int32 [axes][tokens]; inv_freq fp32 [rot / 2];
+    sections: pairs of each axis.  Returns q_out (the type of q unless given; it may be q)."""
+    rows, stride = _chunk_rows(cu_seqlens, block_table, seq_lens, pool.device)
+    if not isinstance(k, torch.Tensor) or k.dtype not in _KIND:
+        raise TypeError("k must be a float16, bfloat16 or float32 tensor")
+    tokens = k.shape[0]
+    ks = _token_array(k, "k", tokens, pool.n_kv, k.dtype, pool.device)
+    vs = _token_array(v, "v", tokens, pool.n_kv, k.dtype, pool.device)
+    n_q = qs = 0
+    kind_out = _KIND[k.dtype]
+    if q is not None:
+        qs = _token_array(q, "q", tokens, None, k.dtype, pool.device)
+        n_q = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(tokens, n_q, HEAD_DIM, dtype=q.dtype, device=pool.device)
+        if q_out.dtype not in _KIND:
+            raise TypeError(f"q_out must be float16, bfloat16 or float32, got {q_out.dtype}")
+        _need(q_out, q_out.dtype, "q_out", (tokens, n_q, HEAD_DIM), pool.device)
+        kind_out = _KIND[q_out.dtype]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    sections = [int(x) for x in sections]
+    _need(inv_freq, torch.float32, "inv_freq", device=pool.device)
+    _need(positions, torch.int32, "positions", (len(sections), tokens), pool.device)
+    sec = (ctypes.c_int * max(len(sections), 1))(*sections)
+    with _on(pool):
+        _check(lib().kv_rope_append(pool.handle, layer, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _KIND[k.dtype],
+                                    _ptr(q_out), kind_out, _ptr(positions), len(sections), sec, _ptr(inv_freq),
+                                    2 * inv_freq.numel(), int(interleaved), _ptr(cu_seqlens), tokens,
+                                    _ptr(block_table), stride, _ptr(seq_lens), rows, n_q, _stream(stream)),
+               "kv_rope_append")
+    return q_out
+
+
+class WorkspaceChunk:
+    """Device scratch for paged_chunk_attention: partial states of split segments.  One per stream of
+    calls that may overlap."""
+
+    def __init__(self, pool: KVPool, n_q_heads: int, num_chunks: int = 0):
+        if not num_chunks:
+            c = ctypes.c_int(0)
+            with _on(pool):
+                _check(lib().paged_chunk_default_chunks(pool.handle, n_q_heads, ctypes.byref(c)),
+                       "paged_chunk_default_chunks")
+            num_chunks = c.value
+        self.num_chunks = num_chunks
+        self.nbytes = lib().paged_chunk_workspace_bytes(pool.handle, n_q_heads, num_chunks)
+        if self.nbytes == 0:
+            raise PkvError(1, "paged_chunk_workspace_bytes", "invalid sizes")
+        self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=pool.device)
+
+
+def _q_type(pool):
+    return torch.bfloat16 if pool.dtype == BF16 else torch.float16
+
+
+def paged_chunk_attention(pool: KVPool, layer: int, q, cu_seqlens, block_table, seq_lens, scale: float, *,
+                          softcap: float = 0.0, slopes=None, prefix_lens=None, out=None, lse=None,
+                          workspace: WorkspaceChunk | None = None, stream=None):
+    """Attention of a ragged chunk over the paged cache (paged_chunk_attention in pkv_chunk.h): q
+    [tokens][n_q][128] in bf16 for bf16 pools and f16 for f16 and q8_0 pools.  Returns out, like q; `lse`
+    (fp32 [tokens][n_q]) receives the log of the softmax denominators."""
+    rows, stride = _chunk_rows(cu_seqlens, block_table, seq_lens, pool.device)
+    qs = _token_array(q, "q", None, None, _q_type(pool), pool.device)
+    tokens, n_q = q.shape[:2]
+    if out is None:
+        out = torch.empty(tokens, n_q, HEAD_DIM, dtype=q.dtype, device=pool.device)
+    _need(out, q.dtype, "out", (tokens, n_q, HEAD_DIM), pool.device)
+    if lse is not None:
+        _need(lse, torch.float32, "lse", (tokens, n_q), pool.device)
+    sc = _scores(scale, softcap, slopes, prefix_lens, n_q, rows, pool.device)
+    if workspace is None:
+        workspace = WorkspaceChunk(pool, n_q)
+    with _on(pool):
+        _check(lib().paged_chunk_attention(pool.handle, layer, _ptr(q), qs, _KIND[q.dtype], _ptr(cu_seqlens),
+                                           tokens, _ptr(block_table), stride, _ptr(seq_lens), rows, n_q,
+                                           ctypes.byref(sc), _ptr(out), _ptr(lse), _ptr(workspace.tensor),
+                                           workspace.nbytes, workspace.num_chunks, _stream(stream)),
+               "paged_chunk_attention")
+    return out
+
+
+def paged_attention_mass(pool: KVPool, layer: int, q, lse, cu_seqlens, block_table, seq_lens, scale: float, *,
+                         softcap: float = 0.0, slopes=None, prefix_lens=None, last_queries: int = 0,
+                         mass_in=None, mass_out=None, stream=None):
+    """Add the chunk's attention weights to each cached token's (paged_attention_mass in pkv_chunk.h):
+    mass_in and mass_out fp32 [rows][n_kv][stride], which may be the same tensor.  Returns mass_out."""
+    rows, stride = _chunk_rows(cu_seqlens, block_table, seq_lens, pool.device)
+    qs = _token_array(q, "q", None, None, _q_type(pool), pool.device)
+    tokens, n_q = q.shape[:2]
+    _need(lse, torch.float32, "lse", (tokens, n_q), pool.device)
+    if mass_out is None:
+        if mass_in is None:
+            raise ValueError("mass_in or mass_out is needed")
+        mass_out = mass_in
+    _need(mass_out, torch.float32, "mass_out", device=pool.device)
+    if mass_out.dim() != 3 or mass_out.shape[:2] != (rows, pool.n_kv):
+        raise ValueError("mass_out must be [rows][n_kv][stride]")
+    if mass_in is not None:
+        _need(mass_in, torch.float32, "mass_in", mass_out.shape, pool.device)
+    sc = _scores(scale, softcap, slopes, prefix_lens, n_q, rows, pool.device)
+    with _on(pool):
+        _check(lib().paged_attention_mass(pool.handle, layer, _ptr(q), qs, _KIND[q.dtype], _ptr(lse),
+                                          _ptr(cu_seqlens), tokens, _ptr(block_table), stride, _ptr(seq_lens),
+                                          rows, n_q, ctypes.byref(sc), last_queries, _ptr(mass_in),
+                                          _ptr(mass_out), mass_out.shape[2], _stream(stream)),
+               "paged_attention_mass")
+    return mass_out
+
+
+def kv_evict(pool: KVPool, layer: int, mass, block_table, seq_lens, keep_lens, dst_block_table, *, first: int = 0,
+             recent: int = 0, keep_idx=None, new_lens=None, dst_mass=None, stream=None):
+    """Shorten rows to keep_lens tokens per KV head by their attention weight (kv_evict in pkv_chunk.h);
+    the kept K and V go to the pages of dst_block_table.  keep_idx int32 [rows][n_kv][stride] (made here
+    unless given, as wide as the new pages hold).  Returns (keep_idx, new_lens)."""
+    rows, stride = _rows(block_table, seq_lens, pool.device)
+    _need(mass, torch.float32, "mass", device=pool.device)
+    if mass.dim() != 3 or mass.shape[:2] != (rows, pool.n_kv):
+        raise ValueError("mass must be [rows][n_kv][stride]")
+    _need(keep_lens, torch.int32, "keep_lens", (rows,), pool.device)
+    _need(dst_block_table, torch.int32, "dst_block_table", device=pool.device)
+    if dst_block_table.dim() != 2 or dst_block_table.shape[0] != rows:
+        raise ValueError("dst_block_table must be [rows][stride]")
+    if keep_idx is None:
+        keep_idx = torch.full((rows, pool.n_kv, PAGE * dst_block_table.shape[1]), -1, dtype=torch.int32,
+                              device=pool.device)
+    _need(keep_idx, torch.int32, "keep_idx", device=pool.device)
+    if keep_idx.dim() != 3 or keep_idx.shape[:2] != (rows, pool.n_kv):
+        raise ValueError("keep_idx must be [rows][n_kv][stride]")
+    if new_lens is None:
+        new_lens = torch.empty_like(seq_lens)
+    _need(new_lens, torch.int32, "new_lens", (rows,), pool.device)
+    if dst_mass is not None:
+        _need(dst_mass, torch.float32, "dst_mass", keep_idx.shape, pool.device)
+    with _on(pool):
+        _check(lib().kv_evict(pool.handle, layer, _ptr(mass), mass.shape[2], _ptr(block_table), stride,
+                              _ptr(seq_lens), rows, _ptr(keep_lens), first, recent, _ptr(dst_block_table),
+                              dst_block_table.shape[1], _ptr(keep_idx), keep_idx.shape[2], _ptr(dst_mass),
+                              _ptr(new_lens), _stream(stream)), "kv_evict")
+    return keep_idx, new_lens
 
 
 class PageAllocator:

@@ -10,6 +10,7 @@
 #include <mutex>
 #include <new>
 
+#include "chunk_internal.h"
 #include "pkv.h"
 #include "pkv_internal.h"
 
@@ -341,6 +342,23 @@ pkv_status check_attention_args(const pkv_pool* pool, int layer, const float* q,
                          num_chunks);
 }
 pkv_status record_error(pkv_status s, const char* msg) { return fail(s, "%s", msg); }
+pkv_status pool_layer_view(const pkv_pool* pool, int layer, PoolView* view) {
+  const pkv_status s = check_pool_layer(pool, layer);
+  if (s) return s;
+  view->k_data = pool->k_data + layer * pool->layer_data_bytes;
+  view->v_data = pool->v_data + layer * pool->layer_data_bytes;
+  view->k_scales = pool->k_scales ? pool->k_scales + layer * pool->layer_scale_bytes : nullptr;
+  view->v_scales = pool->v_scales ? pool->v_scales + layer * pool->layer_scale_bytes : nullptr;
+  view->num_pages = pool->num_pages;
+  view->n_kv = pool->n_kv;
+  view->dtype = pool->dtype;
+  view->window = pool->window[layer];
+  view->status = pool->status;
+  return PKV_OK;
+}
+pkv_status pool_layer_maps(const pkv_pool* pool, int layer, const TileMaps** maps) {
+  return layer_maps(pool, layer, maps);
+}
 }  // namespace pkv
 
 extern "C" {
