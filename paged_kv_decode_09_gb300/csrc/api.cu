@@ -354,6 +354,7 @@ pkv_status pool_layer_view(const pkv_pool* pool, int layer, PoolView* view) {
   view->dtype = pool->dtype;
   view->window = pool->window[layer];
   view->status = pool->status;
+  view->test_stall_ns = pool->test_stall_ns;
   return PKV_OK;
 }
 pkv_status pool_layer_maps(const pkv_pool* pool, int layer, const TileMaps** maps) {

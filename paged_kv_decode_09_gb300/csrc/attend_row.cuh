@@ -36,12 +36,13 @@ __device__ __forceinline__ void load_kv8(const uint8_t* data, const uint8_t* sca
 
 // The state of a row over the tokens [t0, t1) of row i (all attended): running
 // maximum m and sum l in base 2, and dims 4 lane .. + 3 of the unnormalised
-// output.  q points at the row's 128 dims as fp32 (shared memory).  The whole
-// warp must call it.
+// output.  q points at the row's 128 dims (f16 or bf16).  The whole warp must
+// call it.
 template <int DT>
 __device__ __forceinline__ void attend_row(const PoolView& pool, const ChunkRows& rows, const ScoreArgs& sc, int i,
-                                           int h, float slope, int P, const float* q, int t0, int t1, float& m,
+                                           int h, float slope, int P, const uint8_t* q, int t0, int t1, float& m,
                                            float& l, float (&acc)[4]) {
+  constexpr int kIo = DT == PKV_KV_BF16 ? PKV_KV_BF16 : PKV_KV_F16;
   const int lane = threadIdx.x & 31;
   const int32_t* bt = rows.block_table + static_cast<long long>(i) * rows.bt_stride;
   m = -INFINITY;
@@ -62,10 +63,11 @@ __device__ __forceinline__ void attend_row(const PoolView& pool, const ChunkRows
       float dot = 0.0f;
 #pragma unroll 4
       for (int vec = 0; vec < kD / 8; ++vec) {
-        float x[8];
+        float x[8], y[8];
         load_kv8<DT>(pool.k_data, pool.k_scales, r, vec, x);
+        load8(q, 8 * vec, kIo, y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dot = fmaf(x[e], q[8 * vec + e], dot);
+        for (int e = 0; e < 8; ++e) dot = fmaf(x[e], y[e], dot);
       }
       s = score2(dot, sc.scale, sc.softcap, slope, abs(P - t));
     }

@@ -1,75 +1,965 @@
-// chunk_attention.cu — paged_chunk_attention: a warp per (token, query head),
-// straight from the pages (attend_row).
+// chunk_attention.cu — paged_chunk_attention on the fifth-generation tensor
+// cores (tcgen05, accumulators in tensor memory): f16 and bf16 caches; q8_0
+// caches by a warp per (token, query head) for now.
+//
+// For one (row, KV head), the (query, query head) pairs are rows of a matrix
+// product: a tile is 256 of them, 256 / G queries, as two halves m of 128.
+// Over the tile's blocks of 128 cached tokens,
+//     S_m = Q_m K^T             128 x 128, both from shared memory
+//     P_m = 2^(y - max)         y the base-2 score, one thread per row
+//     O_m += P_m V              128 x 128, P_m from tensor memory
+// with one pass over K and V and the running maximum and sum of the softmax
+// in the row's thread.  The maximum is raised, and O rescaled, only when a
+// block exceeds it by more than 8 (a factor of 256, which f16 and bf16 hold).
+// P_m overwrites S_m in tensor memory as 16-bit pairs: S_0, S_1, O_0 and O_1
+// take all 512 columns.  The halves alternate on the tensor cores: while one
+// is in its softmax, the other's products run.
+//
+// Warps: 0-3 and 4-7 the softmax of half 0 and 1, 8 walks the work and copies
+// Q, 9 issues the products, 10 copies K and V pages (one tensor copy each)
+// into a ring of five 32 KiB slots, 11 mends V blocks that hold tokens no
+// query of the tile attends to.  Hand-overs by shared-memory barriers:
+//   dfull, dempty[x]  descriptor x of a piece (a tile's blocks in this range)
+//   qfull[m], qempty  Q_m landed; the piece's last scores are computed
+//   full, empty[s]    K or V block in ring slot s
+//   land[s]           a V block that warp 11 passes on to full[s]
+//   sfull[m]          S_m computed (and every product issued before it)
+//   pready[m]         P_m written, S_m read
+//   ofull[m]          O_m of the piece complete
+// Every wait is bounded; a warp that gives up sets the abort flag, which ends
+// the other waits, and its copies and products are awaited before the CTA ends.
+//
+// The work of the batch is a line of (KV head, tile, block) units, cut into
+// equal ranges, one per CTA (chunk_plan.cuh).  A tile that crosses a boundary
+// leaves partial states (m, l, O) in the workspace, which the second kernel
+// merges.
+//
+// A token that some rows of a tile attend to and others do not gets weight 0
+// in the latter, but 0 times a value that is not finite is not 0.  Warp 11
+// looks for such values in the blocks that are masked for part of the tile;
+// where it finds one, rows that end up not finite are computed again from the
+// tokens they attend to alone (attend_row).
+#include <atomic>
+#include <cmath>
 #include <cstdint>
+
+#include <cudaTypedefs.h>
 
 #include "attend_row.cuh"
 #include "chunk_device.cuh"
+#include "chunk_plan.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
+constexpr int kAttnThreads = kPlanThreads;
+constexpr int kSlots = 5;
+constexpr uint32_t kHalf = 32768;                    // bytes of Q_m, and of a ring slot
+constexpr uint32_t kRing = 2 * kHalf;                // the ring, behind Q
+constexpr uint32_t kTail = kRing + kSlots * kHalf;   // barriers and descriptors
+constexpr int kDescs = 4;
+constexpr int kSplitSnap = 2;   // blocks: see chunk_plan
+constexpr uint32_t kTmemS = 0, kTmemO = 256;         // S_m at 128 m, O_m at 256 + 128 m
+
+// barriers
+enum : int {
+  kBFull = 0,
+  kBEmpty = kBFull + kSlots,
+  kBLand = kBEmpty + kSlots,
+  kBS = kBLand + kSlots,
+  kBP = kBS + 2,
+  kBO = kBP + 2,
+  kBQ = kBO + 2,
+  kBQEmpty = kBQ + 2,
+  kBDesc = kBQEmpty + 1,
+  kBDescEmpty = kBDesc + kDescs,
+  kBDrain = kBDescEmpty + kDescs,
+  kBStall,
+  kNumBars,
+};
+constexpr int kDescReaders = 11;  // 8 softmax warps, products, copies, mending
+
+// A piece: blocks kb .. kb + nb - 1 of one tile for KV head h.
+struct Piece {
+  int i, h, tok, nq, P0, L, F, kb, nb, t_lo, t_hi;
+  int full_lo, full_hi;  // [full_lo, full_hi): tokens every query of the tile attends to
+  int slot;              // partial slot, -1: the whole tile
+  int last;              // no piece: the end
+  int pad;
+};
+static_assert(sizeof(Piece) == 64, "");
+
+struct Tail {
+  uint64_t bars[kNumBars];
+  Piece piece[kDescs];
+  int bad[kDescs];  // a masked V block of the piece holds a value that is not finite
+  volatile int ctl[2];
+  uint32_t tmem;
+  Place bounds[2];
+  PlanScratch scratch;
+};
+constexpr size_t kSmemBytes = 1024 + kTail + sizeof(Tail);
+static_assert(kSmemBytes <= 232448, "");
+
+// ------------------------------------------------------------ workspace ----
+// Records of the boundaries (Rec), then two partial slots per chunk: slot 2k
+// for the piece at the start of range k, 2k + 1 for the one at its end.  A
+// slot: (m, l) of its 256 rows, then O as [32 groups of 4 dims][256 rows].
+struct Rec {
+  int inside;  // the boundary cuts a tile
+  int h, tile, tok, nq, pad[3];
+};
+constexpr size_t kSlotMl = kTileRows * 8;
+constexpr size_t kSlotFull = kSlotMl + static_cast<size_t>(kTileRows) * kD * 4;
+__host__ __device__ inline size_t rec_bytes(int chunks) {
+  return (static_cast<size_t>(chunks + 1) * sizeof(Rec) + 255) & ~size_t(255);
+}
+__device__ __forceinline__ float2* slot_ml(const ChunkAttnArgs& a, int slot) {
+  return reinterpret_cast<float2*>(a.workspace + rec_bytes(a.chunks) + slot * kSlotFull);
+}
+__device__ __forceinline__ float4* slot_acc(const ChunkAttnArgs& a, int slot) {
+  return reinterpret_cast<float4*>(a.workspace + rec_bytes(a.chunks) + slot * kSlotFull + kSlotMl);
+}
+
+template <int DT>
+struct Io {
+  static constexpr int kType = DT == PKV_KV_BF16 ? PKV_KV_BF16 : PKV_KV_F16;
+  [[maybe_unused]] static constexpr uint32_t kFormat = DT == PKV_KV_BF16 ? 1u : 0u;
+  // P is scaled by 2^kShift: f16 weights far below the maximum stay normal
+  // (the largest, 2^(8 + 7), is still below f16's 65504); bf16 has the range.
+  [[maybe_unused]] static constexpr float kShift = DT == PKV_KV_BF16 ? 0.0f : 7.0f;
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    if constexpr (kType == PKV_KV_BF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+      return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(x, y);
+      return *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+};
+
+// ---------------------------------------------------- a row, once more ----
+// Row r of a piece computed by the whole warp from the tokens it attends to.
+template <int DT>
+__device__ __noinline__ void redo_row(const ChunkAttnArgs& a, const Piece& p, int r) {
+  const int lane = threadIdx.x & 31;
+  const int G = a.n_q / a.pool.n_kv;
+  const int j = r / G, g = p.h * G + r % G, P = p.P0 + j;
+  const int t0 = max(seen_from(P, a.pool.window), p.kb * kBlockTok);
+  const int t1 = min(seen_to(P, p.L, p.F), (p.kb + p.nb) * kBlockTok);
+  const float slope = a.sc.slopes ? __ldg(a.sc.slopes + g) : 0.0f;
+  float m, l, acc[4];
+  attend_row<DT>(a.pool, a.rows, a.sc, p.i, p.h, slope, P,
+                 a.q + ((p.tok + j) * a.q_stride + static_cast<long long>(g) * kD) * 2, t0, t1, m, l, acc);
+  if (p.slot >= 0) {
+    slot_acc(a, p.slot)[lane * kTileRows + r] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (lane == 0) slot_ml(a, p.slot)[r] = make_float2(m, l);
+  } else {
+    const float inv = 1.0f / l;
+    const long long to = (static_cast<long long>(p.tok + j) * a.n_q + g) * kD + 4 * lane;
+    *reinterpret_cast<uint2*>(a.out + to * 2) =
+        make_uint2(Io<DT>::pack(acc[0] * inv, acc[1] * inv), Io<DT>::pack(acc[2] * inv, acc[3] * inv));
+  }
+}
+
+// Zeros and an lse of -inf for the queries of rows that are skipped (one warp).
+__device__ __forceinline__ void fill_skipped(const ChunkAttnArgs& a) {
+  const int lane = threadIdx.x & 31;
+  for (int i = blockIdx.x; i < a.rows.num_rows; i += gridDim.x) {
+    const RowInfo r = row_info(a.rows, i, lane == 0 ? a.pool.status : nullptr);
+    if (r.L >= 0 || r.n == 0) continue;
+    uint4* out = reinterpret_cast<uint4*>(a.out + static_cast<long long>(r.start) * a.n_q * kD * 2);
+    const long long rows = static_cast<long long>(r.n) * a.n_q;
+    for (long long e = lane; e < rows * (kD / 8); e += 32) out[e] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse)
+      for (long long e = lane; e < rows; e += 32) a.lse[static_cast<long long>(r.start) * a.n_q + e] = -INFINITY;
+  }
+}
+
+// GEN: scores with a cap, a bias, or a scale that is not positive.
+template <int DT, bool GEN>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    chunk_attention_kernel(const __grid_constant__ ChunkAttnArgs a, const __grid_constant__ TileMaps maps,
+                           const __grid_constant__ CUtensorMap qmap) {
+  using F = Io<DT>;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  Tail& tail = *reinterpret_cast<Tail*>(smem + kTail);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t bars = smem_addr(tail.bars);
+  auto bar = [&](int b) { return bars + 8u * static_cast<uint32_t>(b); };
+  volatile int* ctl = tail.ctl;
+  const int G = a.n_q / a.pool.n_kv, QT = kTileRows / G;
+
+  if (tid == 0) {
+    prefetch_tensormap(&maps.kp);
+    prefetch_tensormap(&maps.vp);
+    prefetch_tensormap(&qmap);
+    tail.ctl[0] = 0;
+    for (int b = 0; b < kNumBars; ++b) {
+      int count = 1;
+      if (b >= kBP && b < kBP + 2) count = 4;
+      if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders;
+      mbar_init(bar(b), count);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tail.tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc::fence_before();
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int T = chunk_plan(a.rows, a.pool.n_kv, QT, a.pool.window, a.sc.prefix_lens, a.chunks, kSplitSnap,
+                           reinterpret_cast<int*>(smem + kRing), &tail.scratch, tail.bounds);
+  tc::fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tail.tmem);
+  const Place begin = tail.bounds[0], end = tail.bounds[1];
+  // the ring is written next by the async proxy, after the plan's plain accesses
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  // test hook: every warp gives up here, before any copy
+  const bool stalled = test_stall(bar(kBStall), a.pool.test_stall_ns, ctl, a.pool.status);
+
+  auto wait = [&](int b, uint32_t parity) { return tc::warp_wait(bar(b), parity & 1u, ctl, a.pool.status); };
+  auto pages_of = [&](const Piece& p, int b, int& lo, int& hi) {  // pages of a block that are read
+    const int first = (p.kb + b) * (kBlockTok / kPage);
+    lo = max(first, p.t_lo / kPage);
+    hi = min(first + kBlockTok / kPage, (p.t_hi + kPage - 1) / kPage);
+  };
+  // V blocks that warp 11 sees: with tokens outside [t_lo, t_hi) in their
+  // pages (zeroed), or masked for part of the tile (searched)
+  auto mended = [&](const Piece& p, int b) {
+    const int t0 = (p.kb + b) * kBlockTok;
+    return t0 < p.full_lo || t0 + kBlockTok > p.full_hi;
+  };
+
+  if (stalled) {
+    // nothing to do
+  } else if (warp == 8) {
+    // ------------------------------------------------- pieces and queries ----
+    // 32 rows at a time, a row per lane
+    int base = -1;
+    RowInfo mine{0, 0, -1};
+    int mineF = 0;
+    auto row_at = [&](int i, RowInfo& r, int& Fi) {
+      if (base < 0 || i < base || i >= base + 32) {
+        base = i;
+        mine = RowInfo{0, 0, -1};
+        mineF = 0;
+        if (base + lane < a.rows.num_rows) {
+          mine = row_info(a.rows, base + lane, nullptr);
+          if (a.sc.prefix_lens) mineF = __ldg(a.sc.prefix_lens + base + lane);
+        }
+      }
+      r.start = __shfl_sync(kFull, mine.start, i - base);
+      r.n = __shfl_sync(kFull, mine.n, i - base);
+      r.L = __shfl_sync(kFull, mine.L, i - base);
+      Fi = __shfl_sync(kFull, mineF, i - base);
+    };
+    Place c = begin;
+    int p = 0;
+    bool ok = true;
+    uint32_t q1 = 0;  // pieces with both halves so far
+    while (before(c, end)) {
+      RowInfo r;
+      int Fi;
+      row_at(c.i, r, Fi);
+      const TileGeom g = tile_geom(r, c.t, QT, a.pool.window, Fi);
+      const bool ends_here = c.h == end.h && c.tile == end.tile;
+      const int b1 = ends_here ? end.off : g.nb;
+      const int x = p % kDescs;
+      const int tok = r.start + c.t * QT;
+      if (p >= kDescs && !(ok = wait(kBDescEmpty + x, p / kDescs - 1))) break;
+      if (lane == 0) {
+        Piece& d = tail.piece[x];
+        d.i = c.i;
+        d.h = c.h;
+        d.tok = tok;
+        d.nq = g.nq;
+        d.P0 = g.P0;
+        d.L = r.L;
+        d.F = Fi;
+        d.kb = g.kb + c.off;
+        d.nb = b1 - c.off;
+        d.t_lo = g.t_lo;
+        d.t_hi = g.t_hi;
+        d.full_lo = seen_from(g.P0 + g.nq - 1, a.pool.window);
+        d.full_hi = seen_to(g.P0, r.L, Fi);
+        d.slot = c.off > 0 ? 2 * static_cast<int>(blockIdx.x) : b1 < g.nb ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
+        d.last = 0;
+        tail.bad[x] = 0;
+        mbar_arrive(bar(kBDesc + x));
+      }
+      __syncwarp();
+      const bool two = g.nq * G > kTileRows / 2;
+      if (p > 0 && !(ok = wait(kBQEmpty, p - 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(kBQ), kHalf);
+        tc::load_rows(sbase, &qmap, c.h * G, tok, bar(kBQ));
+        if (two) {
+          mbar_arrive_expect_tx(bar(kBQ + 1), kHalf);
+          tc::load_rows(sbase + kHalf, &qmap, c.h * G, tok + QT / 2, bar(kBQ + 1));
+        }
+      }
+      __syncwarp();
+      q1 += two ? 1 : 0;
+      ++p;
+      if (ends_here) break;
+      // the next tile
+      c.off = 0;
+      ++c.t;
+      if (++c.tile == T) {
+        c.tile = 0;
+        ++c.h;
+        c.i = 0;
+        c.t = 0;
+        row_at(0, r, Fi);
+      }
+      while (c.h < a.pool.n_kv && c.t >= tiles_of(r, QT)) {
+        ++c.i;
+        c.t = 0;
+        row_at(c.i, r, Fi);
+      }
+    }
+    if (ok) {
+      const int x = p % kDescs;
+      if (p < kDescs || wait(kBDescEmpty + x, p / kDescs - 1)) {
+        if (lane == 0) {
+          tail.piece[x].last = 1;
+          mbar_arrive(bar(kBDesc + x));
+        }
+        __syncwarp();
+      }
+    }
+    // the last copies land before the CTA ends
+    const int zero = 0;
+    if (lane == 0 && p > 0) {
+      mbar_wait_bounded(bar(kBQ), (p - 1) & 1, &zero);
+      if (q1 > 0) mbar_wait_bounded(bar(kBQ + 1), (q1 - 1) & 1, &zero);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------ K and V pages ----
+    int gs = 0;              // slots filled
+    uint32_t landed = 0;     // parity of each slot's land barrier
+    uint32_t my_bar = 0, my_par = 0;  // lane s: the last copy's barrier of slot s
+    bool ok = true;
+    for (int p = 0; ok; ++p) {
+      const int x = p % kDescs;
+      if (!wait(kBDesc + x, p / kDescs)) break;
+      const Piece d = tail.piece[x];
+      if (d.last) break;
+      const int32_t* bt = a.rows.block_table + static_cast<long long>(d.i) * a.rows.bt_stride;
+      int lo, hi;
+      pages_of(d, 0, lo, hi);
+      auto entry = [&](int b) {
+        int l0, h0;
+        pages_of(d, b, l0, h0);
+        return lane < h0 - l0 ? __ldg(bt + l0 + lane) : 0;
+      };
+      int next = entry(0);
+      for (int b = 0; b < d.nb; ++b) {
+        int pg = next;
+        pages_of(d, b, lo, hi);
+        if (b + 1 < d.nb) next = entry(b + 1);
+        const int n = hi - lo;
+        if (lane < n && (pg < 0 || pg >= a.pool.num_pages)) {
+          record_status(a.pool.status, PKV_DEV_BAD_PAGE);
+          pg = 0;
+        }
+        const uint32_t in_slot = (lo & 7) * 4096u + lane * 4096u;
+        const bool mend = mended(d, b);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int s = (gs + v) % kSlots;
+          if (gs + v >= kSlots && !wait(kBEmpty + s, (gs + v) / kSlots - 1)) {
+            ok = false;
+            break;
+          }
+          const int to = v == 1 && mend ? kBLand + s : kBFull + s;
+          const uint32_t par = v == 1 && mend ? (landed >> s) & 1u : static_cast<uint32_t>((gs + v) / kSlots) & 1u;
+          if (v == 1 && mend) landed ^= 1u << s;
+          if (lane == s) {
+            my_bar = bar(to);
+            my_par = par;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(to), static_cast<uint32_t>(n) * 4096u);
+          __syncwarp();
+          if (lane < n)
+            tc::load_tile(sbase + kRing + s * kHalf + in_slot, v ? &maps.vp : &maps.kp, pg * a.pool.n_kv + d.h,
+                          bar(to));
+        }
+        if (!ok) break;
+        gs += 2;
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
+    }
+    const int zero = 0;
+    if (my_bar) mbar_wait_bounded(my_bar, my_par, &zero);
+    __syncwarp();
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ mending ----
+    int gs = 0;
+    uint32_t landed = 0;
+    bool ok = true;
+    for (int p = 0; ok; ++p) {
+      const int x = p % kDescs;
+      if (!wait(kBDesc + x, p / kDescs)) break;
+      const Piece d = tail.piece[x];
+      if (d.last) break;
+      for (int b = 0; b < d.nb; ++b, gs += 2) {
+        if (!mended(d, b)) continue;
+        const int s = (gs + 1) % kSlots;
+        if (!wait(kBLand + s, (landed >> s) & 1u)) {
+          ok = false;
+          break;
+        }
+        landed ^= 1u << s;
+        uint8_t* v = smem + kRing + s * kHalf;
+        const int t0 = (d.kb + b) * kBlockTok;
+        int lo, hi;
+        pages_of(d, b, lo, hi);
+        // tokens of the pages read that no query of the tile attends to
+        for (int t = lo * kPage + lane; t < hi * kPage; t += 32) {
+          if (t >= d.t_lo && t < d.t_hi) continue;
+          const int u = t - t0;  // token of the block: page u / 16, group (u / 8) % 2
+          uint4* row = reinterpret_cast<uint4*>(v + (u >> 3) * 2048 + (u & 7) * 128);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            row[e] = make_uint4(0u, 0u, 0u, 0u);
+            row[64 + e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        __syncwarp();
+        // 0 * x is NaN for the others
+        uint32_t bits = 0;
+        const uint4* w = reinterpret_cast<const uint4*>(v + (lo & 7) * 4096);
+        const int n16 = (hi - lo) * 256;
+        if constexpr (DT == PKV_KV_BF16) {
+          __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
+          const __nv_bfloat162 z = acc;
+#pragma unroll 8
+          for (int e = lane; e < n16; e += 32) {
+            const uint4 q = w[e];
+            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&q.x), z, acc);
+            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&q.y), z, acc);
+            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&q.z), z, acc);
+            acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&q.w), z, acc);
+          }
+          bits = *reinterpret_cast<const uint32_t*>(&acc);
+        } else {
+          __half2 acc = __floats2half2_rn(0.f, 0.f);
+          const __half2 z = acc;
+#pragma unroll 8
+          for (int e = lane; e < n16; e += 32) {
+            const uint4 q = w[e];
+            acc = __hfma2(*reinterpret_cast<const __half2*>(&q.x), z, acc);
+            acc = __hfma2(*reinterpret_cast<const __half2*>(&q.y), z, acc);
+            acc = __hfma2(*reinterpret_cast<const __half2*>(&q.z), z, acc);
+            acc = __hfma2(*reinterpret_cast<const __half2*>(&q.w), z, acc);
+          }
+          bits = *reinterpret_cast<const uint32_t*>(&acc);
+        }
+        if (__any_sync(kFull, (bits & 0x7FFF7FFFu) != 0u) && lane == 0) *(volatile int*)&tail.bad[x] = 1;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the zeroed rows
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBFull + s));
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
+    }
+    fill_skipped(a);
+  } else if (warp == 9) {
+    // ----------------------------------------------------------- products ----
+    const bool leader = tc::elect_one();
+    const uint32_t id_s = tc::idesc(128, 128, false, false, F::kFormat);
+    const uint32_t id_o = tc::idesc(128, 128, false, true, F::kFormat);
+    // scores S_m of the K block in slot s
+    auto issue_s = [&](int m, int s) {
+      const uint64_t qd = tc::desc(sbase + m * kHalf, 16, 1024), kd = tc::desc(sbase + kRing + s * kHalf, 16, 2048);
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_ss(tmem + kTmemS + 128 * m, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                     kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0);
+        tc::commit(bar(kBS + m));
+      }
+      __syncwarp();
+    };
+    // the block whose values product is due
+    struct {
+      int s, lo, n;          // V slot, first page in it, pages
+      bool first, last, two;
+    } v{0, 0, 0, false, false, false};
+    bool due = false;
+    uint32_t np[2] = {0, 0};  // P blocks consumed per half
+    auto issue_o = [&](int m) {
+      const uint64_t vd = tc::desc(sbase + kRing + v.s * kHalf + v.lo * 4096, 1024, 2048);
+      if (leader) {
+        for (int kk = 0; kk < v.n; ++kk)
+          tc::mma_ts(tmem + kTmemO + 128 * m, tmem + kTmemS + 128 * m + 8 * (v.lo + kk), vd + kk * (4096 >> 4), id_o,
+                     !v.first || kk > 0);
+        if (v.last) tc::commit(bar(kBO + m));
+      }
+      __syncwarp();
+    };
+    int gs = 0;
+    bool ok = true, any = false;
+    auto half0 = [&]() {  // O_0 of the due block
+      if (!due) return true;
+      if (!wait(kBP, np[0]) || !wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kSlots)) return false;
+      ++np[0];
+      tc::fence_after();
+      issue_o(0);
+      return true;
+    };
+    auto half1 = [&]() {
+      if (!due) return true;
+      if (v.two) {
+        if (!wait(kBP + 1, np[1])) return false;
+        ++np[1];
+        tc::fence_after();
+        issue_o(1);
+      }
+      if (leader) tc::commit(bar(kBEmpty + v.s));
+      __syncwarp();
+      due = false;
+      return true;
+    };
+    uint32_t q1 = 0;
+    for (int p = 0; ok; ++p) {
+      const int x = p % kDescs;
+      if (!wait(kBDesc + x, p / kDescs)) { ok = false; break; }
+      const Piece d = tail.piece[x];
+      if (d.last) break;
+      const bool two = d.nq * G > kTileRows / 2;
+      any = true;
+      for (int b = 0; b < d.nb && ok; ++b) {
+        // gs: the slot of this block's K; gs - 1 that of the due block's V
+        const int s = gs % kSlots;
+        ok = half0();
+        if (!ok) break;
+        if (b == 0 && !(ok = wait(kBQ, p))) break;
+        if (!(ok = wait(kBFull + s, gs / kSlots))) break;
+        tc::fence_after();
+        issue_s(0, s);
+        ok = half1();
+        if (!ok) break;
+        if (two) {
+          if (b == 0 && !(ok = wait(kBQ + 1, q1))) break;
+          tc::fence_after();
+          issue_s(1, s);
+        }
+        if (leader) {
+          tc::commit(bar(kBEmpty + s));
+          if (b + 1 == d.nb) tc::commit(bar(kBQEmpty));
+        }
+        __syncwarp();
+        int lo, hi;
+        pages_of(d, b, lo, hi);
+        v.s = (gs + 1) % kSlots;
+        v.lo = lo & 7;
+        v.n = hi - lo;
+        v.first = b == 0;
+        v.last = b + 1 == d.nb;
+        v.two = two;
+        due = true;
+        gs += 2;
+      }
+      if (!ok) break;
+      q1 += two ? 1 : 0;
+      if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
+      __syncwarp();
+    }
+    if (ok) ok = half0() && half1();
+    // every product issued completes before the tensor memory is freed
+    if (any) {
+      const int zero = 0;
+      if (leader) tc::commit(bar(kBDrain));
+      __syncwarp();
+      if (lane == 0) mbar_wait_bounded(bar(kBDrain), 0, &zero);
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax ----
+    const int m = warp >> 2, quarter = warp & 3;
+    const int r = 128 * m + 32 * quarter + lane;  // row of the tile
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t tS = tmem + lanes + kTmemS + 128 * m, tO = tmem + lanes + kTmemO + 128 * m;
+    const int jq = r / G;
+    uint32_t blocks = 0, pieces = 0;
+    bool ok = true;
+    const float c1 = a.sc.scale * kLog2e;
+    const float inv_cap = a.sc.softcap > 0.0f ? a.sc.scale / a.sc.softcap : 0.0f, cap2 = a.sc.softcap * kLog2e;
+    for (int p = 0; ok; ++p) {
+      const int x = p % kDescs;
+      if (!wait(kBDesc + x, p / kDescs)) break;
+      const Piece d = tail.piece[x];
+      if (d.last) break;
+      const bool two = d.nq * G > kTileRows / 2;
+      if (m == 0 || two) {
+        const bool valid = jq < d.nq;
+        const bool any = __any_sync(kFull, valid);
+        const int P = d.P0 + jq, g = d.h * G + r % G;
+        const int lo = valid ? seen_from(P, a.pool.window) : 0;
+        const int hi = valid ? seen_to(P, d.L, d.F) : 0x7FFFFFFF;
+        float slope2 = 0.0f;
+        if constexpr (GEN) slope2 = a.sc.slopes ? __ldg(a.sc.slopes + g) * kLog2e : 0.0f;
+        float mx = -INFINITY;  // the maximum in force, base 2
+        float sub = 0.0f;      // what is taken off the scores: mx - shift (0 before a first score)
+        float2 l2 = make_float2(0.0f, 0.0f);
+        for (int b = 0; b < d.nb; ++b, ++blocks) {
+          const int t0 = (d.kb + b) * kBlockTok;
+          const bool fast = __all_sync(kFull, t0 >= lo && t0 + kBlockTok <= hi);
+          if (!(ok = wait(kBS + m, blocks))) break;
+          tc::fence_after();
+          if (any) {
+            float s[128];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tc::ld32(tS + 32 * e, s + 32 * e);
+            tc::wait_ld();
+            if constexpr (GEN) {
+              const float dist0 = static_cast<float>(P - t0);
+#pragma unroll
+              for (int e = 0; e < 128; ++e) {
+                float y;
+                if (a.sc.softcap > 0.0f) {
+                  // tanh z = 1 - 2 / (1 + e^2z)
+                  y = cap2 - __fdividef(2.0f * cap2, 1.0f + tc::ex2(s[e] * (2.0f * kLog2e * inv_cap)));
+                } else {
+                  y = s[e] * c1;
+                }
+                s[e] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(e)), y);
+              }
+            }
+            if (!fast) {
+              const int from = lo - t0, to = hi - t0;
+#pragma unroll
+              for (int e = 0; e < 128; ++e) s[e] = e >= from && e < to ? s[e] : -INFINITY;
+            }
+            float b0 = s[0], b1 = s[1], b2 = s[2], b3 = s[3];
+#pragma unroll
+            for (int e = 4; e < 128; e += 4) {
+              b0 = fmaxf(b0, s[e]);
+              b1 = fmaxf(b1, s[e + 1]);
+              b2 = fmaxf(b2, s[e + 2]);
+              b3 = fmaxf(b3, s[e + 3]);
+            }
+            float bm = fmaxf(fmaxf(b0, b1), fmaxf(b2, b3));
+            if constexpr (!GEN) bm *= c1;
+            const bool raise = bm > mx + 8.0f;  // also from -inf
+            if (__any_sync(kFull, raise)) {
+              float al = 1.0f;
+              if (raise) {
+                al = tc::ex2(mx - bm);
+                mx = bm;
+                sub = bm - F::kShift;
+                l2.x *= al;
+                l2.y *= al;
+              }
+              if (b > 0) {
+                // the values products so far are complete: S was issued after them
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                  float o[32];
+                  tc::ld32(tO + 32 * e, o);
+                  tc::wait_ld();
+#pragma unroll
+                  for (int u = 0; u < 32; ++u) o[u] *= al;
+                  tc::st32(tO + 32 * e, o);
+                }
+              }
+            }
+            const float2 mul = make_float2(GEN ? 1.0f : c1, GEN ? 1.0f : c1), off = make_float2(-sub, -sub);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[16];
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                const float2 y = tc::fma2(make_float2(s[32 * e + 2 * u], s[32 * e + 2 * u + 1]), mul, off);
+                const float2 pr = make_float2(tc::ex2(y.x), tc::ex2(y.y));
+                l2 = tc::add2(l2, pr);
+                w[u] = F::pack(pr.x, pr.y);
+              }
+              tc::st16(tS + 16 * e, w);
+            }
+            tc::wait_st();
+          }
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBP + m));
+        }
+        if (!ok || !(ok = wait(kBO + m, pieces))) break;
+        ++pieces;
+        tc::fence_after();
+        if (any) {
+          const float l = l2.x + l2.y;
+          const float inv = d.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+          const long long row = static_cast<long long>(d.tok + jq) * a.n_q + g;
+          float watch = 0.0f;  // NaN once a value is not finite
+#pragma unroll 1
+          for (int e = 0; e < 4; ++e) {
+            float o[32];
+            tc::ld32(tO + 32 * e, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              o[u] *= inv;
+              watch = fmaf(o[u], 0.0f, watch);
+            }
+            if (valid) {
+              if (d.slot >= 0) {
+                float4* acc = slot_acc(a, d.slot) + r;
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                  acc[(8 * e + u) * kTileRows] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+              } else {
+                uint4* to = reinterpret_cast<uint4*>(a.out + (row * kD + 32 * e) * 2);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  to[u] = make_uint4(F::pack(o[8 * u], o[8 * u + 1]), F::pack(o[8 * u + 2], o[8 * u + 3]),
+                                     F::pack(o[8 * u + 4], o[8 * u + 5]), F::pack(o[8 * u + 6], o[8 * u + 7]));
+              }
+            }
+          }
+          tc::fence_before();  // O read before the next piece's first values product
+          if (valid) {
+            if (d.slot >= 0)
+              slot_ml(a, d.slot)[r] = make_float2(l > 0.0f ? sub : -INFINITY, l);
+            else if (a.lse)
+              a.lse[row] = (sub + log2f(l)) * kLn2;
+          }
+          if (*(volatile int*)&tail.bad[x]) {
+            unsigned again = __ballot_sync(kFull, valid && watch != 0.0f);
+            __syncwarp();  // this warp's stores above come first
+            while (again) {
+              const int u = __ffs(again) - 1;
+              again &= again - 1;
+              redo_row<DT>(a, d, 128 * m + 32 * quarter + u);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
+    }
+  }
+
+  // the boundary at this range's start, for the merge
+  if (tid == 0) {
+    Rec* rec = reinterpret_cast<Rec*>(a.workspace) + blockIdx.x;
+    Rec x{};
+    x.inside = begin.h < a.pool.n_kv && begin.off > 0;
+    if (x.inside) {
+      const RowInfo r = row_info(a.rows, begin.i, nullptr);
+      const TileGeom g = tile_geom(r, begin.t, QT, a.pool.window, 0);
+      x.h = begin.h;
+      x.tile = begin.tile;
+      x.tok = r.start + begin.t * QT;
+      x.nq = g.nq;
+    }
+    *rec = x;
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc::fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- merge ----
+// CTA (k, y): if boundary k is the first to cut its tile, the tile's rows
+// 32 y .. from its pieces: the end of range k - 1 and the starts of the ranges
+// whose boundaries cut it.
+constexpr int kMergeThreads = 256;
+template <int DT>
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkAttnArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const Rec* rec = reinterpret_cast<const Rec*>(a.workspace);
+  const int k0 = blockIdx.x + 1;
+  const Rec me = rec[k0];
+  if (!me.inside) return;
+  const Rec prev = rec[k0 - 1];
+  if (prev.inside && prev.h == me.h && prev.tile == me.tile) return;
+  const int G = a.n_q / a.pool.n_kv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = 32 * blockIdx.y + lane;
+  if (32 * static_cast<int>(blockIdx.y) >= me.nq * G) return;
+  int k1 = k0;
+  while (k1 + 1 < a.chunks) {
+    const Rec n = rec[k1 + 1];
+    if (!n.inside || n.h != me.h || n.tile != me.tile) break;
+    ++k1;
+  }
+  if (r >= me.nq * G) return;
+  // pieces: slot 2 (k0 - 1) + 1, then 2 k for k0 .. k1
+  auto slot_of = [&](int k) { return k < k0 ? 2 * k + 1 : 2 * k; };
+  float M = -INFINITY;
+  for (int k = k0 - 1; k <= k1; ++k) {
+    const float2 ml = slot_ml(a, slot_of(k))[r];
+    if (ml.y > 0.0f || ml.y != ml.y) M = fmaxf(M, ml.x);
+  }
+  float Lsum = 0.0f;
+  float4 acc[4];  // dims 16 warp ..
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = k0 - 1; k <= k1; ++k) {
+    const int s = slot_of(k);
+    const float2 ml = slot_ml(a, s)[r];
+    if (ml.y == 0.0f) continue;  // no token of the row in the piece
+    const float w = tc::ex2(ml.x - M);
+    Lsum += w * ml.y;
+    const float4* src = slot_acc(a, s) + r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 v = src[(4 * warp + e) * kTileRows];
+      acc[e].x = fmaf(w, v.x, acc[e].x);
+      acc[e].y = fmaf(w, v.y, acc[e].y);
+      acc[e].z = fmaf(w, v.z, acc[e].z);
+      acc[e].w = fmaf(w, v.w, acc[e].w);
+    }
+  }
+  const float inv = 1.0f / Lsum;
+  const long long row = static_cast<long long>(me.tok + r / G) * a.n_q + me.h * G + r % G;
+  uint4* to = reinterpret_cast<uint4*>(a.out + (row * kD + 16 * warp) * 2);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float4 p = acc[2 * e], q = acc[2 * e + 1];
+    to[e] = make_uint4(Io<DT>::pack(p.x * inv, p.y * inv), Io<DT>::pack(p.z * inv, p.w * inv),
+                       Io<DT>::pack(q.x * inv, q.y * inv), Io<DT>::pack(q.z * inv, q.w * inv));
+  }
+  if (a.lse && warp == 0) a.lse[row] = (M + log2f(Lsum)) * kLn2;
+}
+
+// ------------------------------------------------------------------ q8_0 ----
 constexpr int kRowWarps = 8;
 
 template <int DT>
 __global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(const __grid_constant__ ChunkAttnArgs a) {
-  __shared__ float qs[kRowWarps][kD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0) report_rows(a.rows, a.pool.status);
   const long long item = static_cast<long long>(blockIdx.x) * kRowWarps + warp;
   const int tok = static_cast<int>(item / a.n_q), g = static_cast<int>(item % a.n_q);
   if (tok >= a.rows.total_tokens) return;
-  constexpr int kIo = DT == PKV_KV_BF16 ? PKV_KV_BF16 : PKV_KV_F16;
   const int i = row_of_token(a.rows, tok);
   if (i < 0) return;
   const RowInfo r = row_info(a.rows, i, nullptr);
   if (r.n == 0) return;
   float m = -INFINITY, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (r.L >= 0) {
-    if (lane < kD / 8) {
-      float x[8];
-      load8(a.q, tok * a.q_stride + g * kD + 8 * lane, kIo, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) qs[warp][8 * lane + e] = x[e];
-    }
-    __syncwarp();
     const int P = r.L - r.n + tok - r.start;
     const int F = a.sc.prefix_lens ? __ldg(a.sc.prefix_lens + i) : 0;
     const float slope = a.sc.slopes ? __ldg(a.sc.slopes + g) : 0.0f;
-    attend_row<DT>(a.pool, a.rows, a.sc, i, g / (a.n_q / a.pool.n_kv), slope, P, qs[warp],
-                   seen_from(P, a.pool.window), seen_to(P, r.L, F), m, l, acc);
+    attend_row<DT>(a.pool, a.rows, a.sc, i, g / (a.n_q / a.pool.n_kv), slope, P,
+                   a.q + (tok * a.q_stride + static_cast<long long>(g) * kD) * 2, seen_from(P, a.pool.window),
+                   seen_to(P, r.L, F), m, l, acc);
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   const long long to = (static_cast<long long>(tok) * a.n_q + g) * kD + 4 * lane;
-  uint32_t w[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    if constexpr (kIo == PKV_KV_BF16) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-      w[e] = *reinterpret_cast<const uint32_t*>(&x);
-    } else {
-      const __half2 x = __floats2half2_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-      w[e] = *reinterpret_cast<const uint32_t*>(&x);
-    }
-  }
-  *reinterpret_cast<uint2*>(a.out + to * 2) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(a.out + to * 2) =
+      make_uint2(Io<DT>::pack(acc[0] * inv, acc[1] * inv), Io<DT>::pack(acc[2] * inv, acc[3] * inv));
   if (a.lse && lane == 0)
     a.lse[static_cast<long long>(tok) * a.n_q + g] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
+// ------------------------------------------------------------- launchers ----
+template <int DT, bool GEN>
+cudaError_t launch_attention_t(const ChunkAttnArgs& a, const TileMaps& maps, const CUtensorMap& qmap, cudaStream_t st) {
+  static std::atomic<int> granted[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !granted[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(chunk_attention_kernel<DT, GEN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemBytes));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) granted[dev].store(1, std::memory_order_relaxed);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.chunks);
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, chunk_attention_kernel<DT, GEN>, a, maps, qmap);
+  if (e != cudaSuccess) return e;
+  if (a.chunks > 1) {
+    cfg.gridDim = dim3(a.chunks - 1, kTileRows / 32);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, chunk_merge_kernel<DT>, a);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-size_t chunk_attention_workspace(int n_q, int n_kv, int chunks) { return 256; }
+size_t chunk_attention_workspace(int n_q, int n_kv, int chunks) {
+  (void)n_q;
+  (void)n_kv;
+  return rec_bytes(chunks) + 2 * static_cast<size_t>(chunks) * kSlotFull;
+}
 
-cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, const TileMaps&, cudaStream_t st) {
-  const long long items = static_cast<long long>(a.rows.total_tokens) * a.n_q;
-  const dim3 grid(static_cast<unsigned>((items + kRowWarps - 1) / kRowWarps));
-  if (a.pool.dtype == PKV_KV_F16)
-    chunk_rows_kernel<PKV_KV_F16><<<grid, kRowWarps * 32, 0, st>>>(a);
-  else if (a.pool.dtype == PKV_KV_BF16)
-    chunk_rows_kernel<PKV_KV_BF16><<<grid, kRowWarps * 32, 0, st>>>(a);
-  else
+cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, const TileMaps& maps, cudaStream_t st) {
+  if (a.pool.dtype == PKV_KV_Q8_0) {
+    const long long items = static_cast<long long>(a.rows.total_tokens) * a.n_q;
+    const dim3 grid(static_cast<unsigned>((items + kRowWarps - 1) / kRowWarps));
     chunk_rows_kernel<PKV_KV_Q8_0><<<grid, kRowWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+    return cudaGetLastError();
+  }
+  CUtensorMap qmap;
+  cudaError_t e = encode_query_map(&qmap, a.pool.dtype == PKV_KV_BF16, a.q, a.q_stride, a.n_q, a.n_q / a.pool.n_kv,
+                                   a.rows.total_tokens, 128 / (a.n_q / a.pool.n_kv));
+  if (e != cudaSuccess) return e;
+  const bool gen = a.sc.softcap > 0.0f || a.sc.slopes != nullptr || !(a.sc.scale > 0.0f);
+  if (a.pool.dtype == PKV_KV_F16)
+    return gen ? launch_attention_t<PKV_KV_F16, true>(a, maps, qmap, st)
+               : launch_attention_t<PKV_KV_F16, false>(a, maps, qmap, st);
+  return gen ? launch_attention_t<PKV_KV_BF16, true>(a, maps, qmap, st)
+             : launch_attention_t<PKV_KV_BF16, false>(a, maps, qmap, st);
+}
+
+// The queries as a 4-D tensor {64 dims, heads, tokens, 2 halves of the dims},
+// box {64, G, queries, 2}: a copy lands [half][query, head][64 dims] under the
+// 128-byte swizzle, the K-major layout of a product's first operand.  Tokens
+// behind the last read as zeros.
+cudaError_t encode_query_map(CUtensorMap* m, bool bf16, const void* q, long long stride, int heads, int group,
+                             int tokens, int queries) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {64u, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens), 2u};
+  const cuuint64_t strides[3] = {kD * 2, static_cast<cuuint64_t>(stride) * 2, 128u};
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(queries), 2u};
+  const cuuint32_t estride[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                        const_cast<void*>(q), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace pkv

@@ -24,6 +24,7 @@ struct PoolView {
   int dtype;
   int window;
   int32_t* status;
+  unsigned long long test_stall_ns;  // test hook (kv_pool_set_test_stall); 0: off
 };
 pkv_status pool_layer_view(const pkv_pool* pool, int layer, PoolView* view);
 pkv_status pool_layer_maps(const pkv_pool* pool, int layer, const TileMaps** maps);
@@ -97,6 +98,10 @@ struct ChunkAttnArgs {
 };
 size_t chunk_attention_workspace(int n_q, int n_kv, int chunks);
 cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, const TileMaps& maps, cudaStream_t stream);
+
+// Tensor map of a call's queries (chunk_attention.cu).
+cudaError_t encode_query_map(CUtensorMap* m, bool bf16, const void* q, long long stride, int heads, int group,
+                             int tokens, int queries);
 
 struct MassArgs {
   PoolView pool;

@@ -265,3 +265,13 @@ def test_mass_skips_queries_without_a_finite_lse():
     finite = lse.masked_fill(~torch.isfinite(lse), math.inf)  # exp(s - inf) = 0
     want, tol = R.mass(c, q, finite, SCALE, torch.zeros_like(got))
     assert ((got.double() - want).abs() <= tol).all()
+
+
+def test_bounded_waits():
+    """The test hook stalls every wait: the call gives up, says so, and the next one is whole again."""
+    c = R.Chunk(api.F16, 2, 4, [(65, 500), (1, 900)], seed=6)
+    c.pool.set_test_stall(2_000_000)
+    run(c)
+    assert c.pool.read_status() & api.DEV_TIMEOUT
+    c.pool.set_test_stall(0)
+    check(c, *run(c))
