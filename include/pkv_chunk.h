@@ -137,14 +137,22 @@ pkv_status paged_chunk_attention(const pkv_pool *pool, int layer, const void *q,
  *                      skipped); entries from L_i on are left as they are;
  *                      mass_in may be mass_out
  *   q, lse, q_dtype    as in paged_chunk_attention
- * Skipped rows are left as they are.  A query whose lse is not finite adds
- * nothing.  Sums run in a fixed order: equal calls give equal bits. */
+ * Skipped rows are left as they are, all rows where total_tokens is 0.  A
+ * query whose lse is not finite adds nothing.  Sums run in a fixed order: equal
+ * calls give equal bits.
+ *   workspace, num_chunks  as in paged_chunk_attention, of
+ *              paged_attention_mass_workspace_bytes(num_chunks) bytes (the
+ *              default chunks are those of paged_chunk_default_chunks)
+ * Two launches: the sums, and the merge of the tiles that were split. */
+size_t paged_attention_mass_workspace_bytes(int num_chunks);
+
 pkv_status paged_attention_mass(const pkv_pool *pool, int layer, const void *q, long long q_stride,
                                 pkv_kv_dtype q_dtype, const float *lse, const int32_t *cu_seqlens,
                                 int total_tokens, const int32_t *block_table, int bt_stride,
                                 const int32_t *seq_lens, int num_rows, int n_q_heads,
                                 const pkv_scores *scores, int last_queries, const float *mass_in,
-                                float *mass_out, int mass_stride, void *stream);
+                                float *mass_out, int mass_stride, void *workspace,
+                                size_t workspace_bytes, int num_chunks, void *stream);
 
 /* kv_evict — shorten rows to their budget, per KV head, by attention weight.
  * Row i keeps B_i = min(L_i, keep_lens[i]) tokens of each KV head h: the last

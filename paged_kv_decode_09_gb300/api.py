@@ -91,8 +91,9 @@ _SIGS = {
     "paged_chunk_default_chunks": ([_vp, _i, ctypes.POINTER(_i)], _i),
     "paged_chunk_attention": ([_vp, _i, _vp, _ll, _i, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp,
                                _sz, _i, _vp], _i),
+    "paged_attention_mass_workspace_bytes": ([_i], _sz),
     "paged_attention_mass": ([_vp, _i, _vp, _ll, _i, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _i, _vp,
-                              _vp, _i, _vp], _i),
+                              _vp, _i, _vp, _sz, _i, _vp], _i),
     "kv_evict": ([_vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp], _i),
     "pkv_status_string": ([_i], ctypes.c_char_p),
     "pkv_last_error_message": ([], ctypes.c_char_p),
@@ -505,21 +506,34 @@ def kv_rope_append(pool: KVPool, layer: int, q, k, v, positions, inv_freq, secti
     return q_out
 
 
+def _default_chunks_chunk(pool, n_q_heads):
+    c = ctypes.c_int(0)
+    with _on(pool):
+        _check(lib().paged_chunk_default_chunks(pool.handle, n_q_heads, ctypes.byref(c)),
+               "paged_chunk_default_chunks")
+    return c.value
+
+
 class WorkspaceChunk:
     """Device scratch for paged_chunk_attention: partial states of split segments.  One per stream of
     calls that may overlap."""
 
     def __init__(self, pool: KVPool, n_q_heads: int, num_chunks: int = 0):
-        if not num_chunks:
-            c = ctypes.c_int(0)
-            with _on(pool):
-                _check(lib().paged_chunk_default_chunks(pool.handle, n_q_heads, ctypes.byref(c)),
-                       "paged_chunk_default_chunks")
-            num_chunks = c.value
-        self.num_chunks = num_chunks
-        self.nbytes = lib().paged_chunk_workspace_bytes(pool.handle, n_q_heads, num_chunks)
+        self.num_chunks = num_chunks or _default_chunks_chunk(pool, n_q_heads)
+        self.nbytes = lib().paged_chunk_workspace_bytes(pool.handle, n_q_heads, self.num_chunks)
         if self.nbytes == 0:
             raise PkvError(1, "paged_chunk_workspace_bytes", "invalid sizes")
+        self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=pool.device)
+
+
+class WorkspaceMass:
+    """Device scratch for paged_attention_mass, as WorkspaceChunk."""
+
+    def __init__(self, pool: KVPool, n_q_heads: int, num_chunks: int = 0):
+        self.num_chunks = num_chunks or _default_chunks_chunk(pool, n_q_heads)
+        self.nbytes = lib().paged_attention_mass_workspace_bytes(self.num_chunks)
+        if self.nbytes == 0:
+            raise PkvError(1, "paged_attention_mass_workspace_bytes", "invalid sizes")
         self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=pool.device)
 
 
@@ -555,7 +569,7 @@ def paged_chunk_attention(pool: KVPool, layer: int, q, cu_seqlens, block_table, 
 
 def paged_attention_mass(pool: KVPool, layer: int, q, lse, cu_seqlens, block_table, seq_lens, scale: float, *,
                          softcap: float = 0.0, slopes=None, prefix_lens=None, last_queries: int = 0,
-                         mass_in=None, mass_out=None, stream=None):
+                         mass_in=None, mass_out=None, workspace: WorkspaceMass | None = None, stream=None):
     """Add the chunk's attention weights to each cached token's (paged_attention_mass in pkv_chunk.h):
     mass_in and mass_out fp32 [rows][n_kv][stride], which may be the same tensor.  Returns mass_out."""
     rows, stride = _chunk_rows(cu_seqlens, block_table, seq_lens, pool.device)
@@ -572,11 +586,14 @@ def paged_attention_mass(pool: KVPool, layer: int, q, lse, cu_seqlens, block_tab
     if mass_in is not None:
         _need(mass_in, torch.float32, "mass_in", mass_out.shape, pool.device)
     sc = _scores(scale, softcap, slopes, prefix_lens, n_q, rows, pool.device)
+    if workspace is None:
+        workspace = WorkspaceMass(pool, n_q)
     with _on(pool):
         _check(lib().paged_attention_mass(pool.handle, layer, _ptr(q), qs, _KIND[q.dtype], _ptr(lse),
                                           _ptr(cu_seqlens), tokens, _ptr(block_table), stride, _ptr(seq_lens),
                                           rows, n_q, ctypes.byref(sc), last_queries, _ptr(mass_in),
-                                          _ptr(mass_out), mass_out.shape[2], _stream(stream)),
+                                          _ptr(mass_out), mass_out.shape[2], _ptr(workspace.tensor),
+                                          workspace.nbytes, workspace.num_chunks, _stream(stream)),
                "paged_attention_mass")
     return mass_out
 

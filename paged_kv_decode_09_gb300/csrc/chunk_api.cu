@@ -178,6 +178,10 @@ size_t paged_chunk_workspace_bytes(const pkv_pool* pool, int n_q_heads, int num_
   return pkv::chunk_attention_workspace(n_q_heads, n_kv, num_chunks);
 }
 
+size_t paged_attention_mass_workspace_bytes(int num_chunks) {
+  return num_chunks < 1 || num_chunks > kMaxChunks ? 0 : pkv::attention_mass_workspace(num_chunks);
+}
+
 pkv_status paged_chunk_default_chunks(const pkv_pool* pool, int n_q_heads, int* chunks) {
   if (!pool || !chunks) return fail(PKV_ERR_INVALID_ARG, "null pool or output pointer");
   const pkv_status s = check_group(n_q_heads, pkv::pool_kv_heads(pool));
@@ -230,7 +234,8 @@ pkv_status paged_attention_mass(const pkv_pool* pool, int layer, const void* q, 
                                 int total_tokens, const int32_t* block_table, int bt_stride,
                                 const int32_t* seq_lens, int num_rows, int n_q_heads,
                                 const pkv_scores* scores, int last_queries, const float* mass_in,
-                                float* mass_out, int mass_stride, void* stream) {
+                                float* mass_out, int mass_stride, void* workspace,
+                                size_t workspace_bytes, int num_chunks, void* stream) {
   pkv::MassArgs a;
   pkv_status s = pkv::pool_layer_view(pool, layer, &a.pool);
   if (s) return s;
@@ -240,12 +245,11 @@ pkv_status paged_attention_mass(const pkv_pool* pool, int layer, const void* q, 
   if ((s = check_scores(scores))) return s;
   if (last_queries < 0) return fail(PKV_ERR_INVALID_ARG, "last_queries < 0");
   if (mass_stride < 1) return fail(PKV_ERR_INVALID_ARG, "mass_stride < 1");
-  if (a.pool.n_kv > 65535) return fail(PKV_ERR_UNSUPPORTED, "n_kv_heads %d > 65535", a.pool.n_kv);
-  if (num_rows == 0) return PKV_OK;
-  if (total_tokens > 0) {
-    if ((s = check_tokens("q", q, q_stride, n_q_heads, q_dtype))) return s;
-    if (!lse) return fail(PKV_ERR_INVALID_ARG, "null lse");
-  }
+  if (num_chunks < 0) return fail(PKV_ERR_INVALID_ARG, "num_chunks < 0");
+  if (num_chunks > kMaxChunks) return fail(PKV_ERR_UNSUPPORTED, "num_chunks > %d", kMaxChunks);
+  if (num_rows == 0 || total_tokens == 0) return PKV_OK;
+  if ((s = check_tokens("q", q, q_stride, n_q_heads, q_dtype))) return s;
+  if (!lse) return fail(PKV_ERR_INVALID_ARG, "null lse");
   if (!mass_out) return fail(PKV_ERR_INVALID_ARG, "null mass_out");
   if (!aligned(lse, 4) || !aligned(mass_in, 4) || !aligned(mass_out, 4))
     return fail(PKV_ERR_INVALID_ARG, "lse / mass not 4-byte aligned");
@@ -259,6 +263,13 @@ pkv_status paged_attention_mass(const pkv_pool* pool, int layer, const void* q, 
   a.mass_in = mass_in;
   a.mass_out = mass_out;
   a.mass_stride = mass_stride;
+  if (num_chunks == 0 && (s = default_chunks(&num_chunks))) return s;
+  const size_t need = pkv::attention_mass_workspace(num_chunks);
+  if (!workspace || workspace_bytes < need)
+    return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  if (!aligned(workspace, 256)) return fail(PKV_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  a.workspace = static_cast<uint8_t*>(workspace);
+  a.chunks = num_chunks;
   const pkv::TileMaps* maps = nullptr;
   if ((s = pkv::pool_layer_maps(pool, layer, &maps))) return s;
   const cudaError_t e = pkv::launch_attention_mass(a, *maps, as_stream(stream));

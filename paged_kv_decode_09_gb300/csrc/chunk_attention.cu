@@ -54,6 +54,8 @@ namespace pkv {
 namespace {
 
 constexpr int kAttnThreads = kPlanThreads;
+constexpr int kTileRows = 256;   // (query, query head) rows of a tile: 256 / G queries
+constexpr int kBlockTok = 128;   // cached tokens of a block
 constexpr int kSlots = 5;
 constexpr uint32_t kHalf = 32768;                    // bytes of Q_m, and of a ring slot
 constexpr uint32_t kRing = 2 * kHalf;                // the ring, behind Q
@@ -101,6 +103,32 @@ struct Tail {
 };
 constexpr size_t kSmemBytes = 1024 + kTail + sizeof(Tail);
 static_assert(kSmemBytes <= 232448, "");
+
+// A tile: queries t * QT .. of a row, and the blocks they attend to.
+struct TileGeom {
+  int nq;    // queries
+  int P0;    // position of the first
+  int t_lo;  // tokens [t_lo, t_hi) that some query of the tile attends to
+  int t_hi;
+  int kb;    // first block
+  int nb;    // blocks
+};
+struct QueryTiles {
+  int QT, W;
+  __device__ __forceinline__ int tiles(const RowInfo& r) const { return r.L >= 0 ? (r.n + QT - 1) / QT : 0; }
+  __device__ __forceinline__ TileGeom tile(const RowInfo& r, int F, int t) const {
+    TileGeom g;
+    const int j0 = t * QT;
+    g.nq = min(QT, r.n - j0);
+    g.P0 = r.L - r.n + j0;
+    g.t_lo = seen_from(g.P0, W);
+    g.t_hi = seen_to(g.P0 + g.nq - 1, r.L, F);
+    g.kb = g.t_lo / kBlockTok;
+    g.nb = (g.t_hi + kBlockTok - 1) / kBlockTok - g.kb;
+    return g;
+  }
+  __device__ __forceinline__ int blocks(const RowInfo& r, int F, int t) const { return tile(r, F, t).nb; }
+};
 
 // ------------------------------------------------------------ workspace ----
 // Records of the boundaries (Rec), then two partial slots per chunk: slot 2k
@@ -216,7 +244,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  const int T = chunk_plan(a.rows, a.pool.n_kv, QT, a.pool.window, a.sc.prefix_lens, a.chunks, kSplitSnap,
+  const QueryTiles geo{QT, a.pool.window};
+  const int T = chunk_plan(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, kSplitSnap,
                            reinterpret_cast<int*>(smem + kRing), &tail.scratch, tail.bounds);
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tail.tmem);
@@ -244,36 +273,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // nothing to do
   } else if (warp == 8) {
     // ------------------------------------------------- pieces and queries ----
-    // 32 rows at a time, a row per lane
-    int base = -1;
-    RowInfo mine{0, 0, -1};
-    int mineF = 0;
-    auto row_at = [&](int i, RowInfo& r, int& Fi) {
-      if (base < 0 || i < base || i >= base + 32) {
-        base = i;
-        mine = RowInfo{0, 0, -1};
-        mineF = 0;
-        if (base + lane < a.rows.num_rows) {
-          mine = row_info(a.rows, base + lane, nullptr);
-          if (a.sc.prefix_lens) mineF = __ldg(a.sc.prefix_lens + base + lane);
-        }
-      }
-      r.start = __shfl_sync(kFull, mine.start, i - base);
-      r.n = __shfl_sync(kFull, mine.n, i - base);
-      r.L = __shfl_sync(kFull, mine.L, i - base);
-      Fi = __shfl_sync(kFull, mineF, i - base);
-    };
-    Place c = begin;
+    Walk<QueryTiles> w(a.rows, geo, a.sc.prefix_lens, T, begin, end);
     int p = 0;
     bool ok = true;
     uint32_t q1 = 0;  // pieces with both halves so far
-    while (before(c, end)) {
-      RowInfo r;
-      int Fi;
-      row_at(c.i, r, Fi);
-      const TileGeom g = tile_geom(r, c.t, QT, a.pool.window, Fi);
-      const bool ends_here = c.h == end.h && c.tile == end.tile;
-      const int b1 = ends_here ? end.off : g.nb;
+    while (w.more()) {
+      const Place& c = w.at;
+      const RowInfo& r = w.r;
+      const TileGeom g = geo.tile(r, w.F, c.t);
+      const int b1 = w.ends_here() ? end.off : g.nb;
       const int x = p % kDescs;
       const int tok = r.start + c.t * QT;
       if (p >= kDescs && !(ok = wait(kBDescEmpty + x, p / kDescs - 1))) break;
@@ -285,13 +293,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         d.nq = g.nq;
         d.P0 = g.P0;
         d.L = r.L;
-        d.F = Fi;
+        d.F = w.F;
         d.kb = g.kb + c.off;
         d.nb = b1 - c.off;
         d.t_lo = g.t_lo;
         d.t_hi = g.t_hi;
         d.full_lo = seen_from(g.P0 + g.nq - 1, a.pool.window);
-        d.full_hi = seen_to(g.P0, r.L, Fi);
+        d.full_hi = seen_to(g.P0, r.L, w.F);
         d.slot = c.off > 0 ? 2 * static_cast<int>(blockIdx.x) : b1 < g.nb ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
         d.last = 0;
         tail.bad[x] = 0;
@@ -311,22 +319,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       __syncwarp();
       q1 += two ? 1 : 0;
       ++p;
-      if (ends_here) break;
-      // the next tile
-      c.off = 0;
-      ++c.t;
-      if (++c.tile == T) {
-        c.tile = 0;
-        ++c.h;
-        c.i = 0;
-        c.t = 0;
-        row_at(0, r, Fi);
-      }
-      while (c.h < a.pool.n_kv && c.t >= tiles_of(r, QT)) {
-        ++c.i;
-        c.t = 0;
-        row_at(c.i, r, Fi);
-      }
+      if (w.ends_here()) break;
+      w.next();
     }
     if (ok) {
       const int x = p % kDescs;
@@ -762,7 +756,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     x.inside = begin.h < a.pool.n_kv && begin.off > 0;
     if (x.inside) {
       const RowInfo r = row_info(a.rows, begin.i, nullptr);
-      const TileGeom g = tile_geom(r, begin.t, QT, a.pool.window, 0);
+      const TileGeom g = geo.tile(r, 0, begin.t);
       x.h = begin.h;
       x.tile = begin.tile;
       x.tok = r.start + begin.t * QT;

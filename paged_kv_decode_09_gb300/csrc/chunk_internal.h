@@ -115,7 +115,10 @@ struct MassArgs {
   const float* mass_in;
   float* mass_out;
   int mass_stride;
+  uint8_t* workspace;
+  int chunks;
 };
+size_t attention_mass_workspace(int chunks);
 cudaError_t launch_attention_mass(const MassArgs& a, const TileMaps& maps, cudaStream_t stream);
 
 }  // namespace pkv

@@ -1,6 +1,6 @@
-// chunk_plan.cuh — how a ragged chunk's attention is cut into work: tiles of
-// queries, blocks of 128 cached tokens, and contiguous ranges of (KV head,
-// tile, block) units, one range per CTA.
+// chunk_plan.cuh — how the work on a ragged chunk is cut: every row has tiles
+// (of its queries, or of its cached tokens), every tile blocks, and the batch
+// is a line of (KV head, tile, block) units of which each CTA takes a range.
 #pragma once
 
 #include <cstdint>
@@ -9,32 +9,13 @@
 
 namespace pkv {
 
-constexpr int kTileRows = 256;   // (query, query head) rows of a tile: 256 / G queries
-constexpr int kBlockTok = 128;   // cached tokens of a block
-constexpr int kPlanThreads = 384;
+constexpr int kPlanThreads = 384;  // the first threads of a CTA make its plan
 constexpr int kPlanWarps = kPlanThreads / 32;
 
-// A tile: queries tile * QT .. of a row, and the blocks they attend to.
-struct TileGeom {
-  int nq;    // queries
-  int P0;    // position of the first
-  int t_lo;  // tokens [t_lo, t_hi) that some query of the tile attends to
-  int t_hi;
-  int kb;    // first block
-  int nb;    // blocks
-};
-__device__ __forceinline__ TileGeom tile_geom(const RowInfo& r, int t, int QT, int W, int F) {
-  TileGeom g;
-  const int j0 = t * QT;
-  g.nq = min(QT, r.n - j0);
-  g.P0 = r.L - r.n + j0;
-  g.t_lo = seen_from(g.P0, W);
-  g.t_hi = seen_to(g.P0 + g.nq - 1, r.L, F);
-  g.kb = g.t_lo / kBlockTok;
-  g.nb = (g.t_hi + kBlockTok - 1) / kBlockTok - g.kb;
-  return g;
-}
-__device__ __forceinline__ int tiles_of(const RowInfo& r, int QT) { return r.L >= 0 ? (r.n + QT - 1) / QT : 0; }
+// What a kernel tells the plan (Geo below):
+//   int tiles(const RowInfo&)                    tiles of a row
+//   int blocks(const RowInfo&, int F, int t)     blocks of its tile t, at least 1
+//   F is prefix_lens[i], or 0 without.
 
 // A place in the work: block `off` of tile `tile` (counted over the batch;
 // tile t of row i) for KV head h.  The end of all work is {n_kv, 0, .., 0}.
@@ -45,8 +26,9 @@ __device__ __forceinline__ bool before(const Place& a, const Place& b) {
   return a.h != b.h ? a.h < b.h : a.tile != b.tile ? a.tile < b.tile : a.off < b.off;
 }
 
-// Exclusive prefix sum over the CTA's threads and the total; `tmp` holds
-// kPlanWarps + 1 values.  Ends with a barrier.
+// Exclusive prefix sum over the first kPlanThreads threads and its total (any
+// further threads call it too, with 0); `tmp` holds kPlanWarps values.  Ends
+// with a barrier.
 template <typename T>
 __device__ __forceinline__ T cta_scan(T x, T* tmp, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -56,7 +38,7 @@ __device__ __forceinline__ T cta_scan(T x, T* tmp, T& total) {
     const T u = __shfl_up_sync(kFull, v, o);
     if (lane >= o) v += u;
   }
-  if (lane == 31) tmp[warp] = v;
+  if (lane == 31 && warp < kPlanWarps) tmp[warp] = v;
   __syncthreads();
   T pre = 0, sum = 0;
 #pragma unroll
@@ -69,30 +51,39 @@ __device__ __forceinline__ T cta_scan(T x, T* tmp, T& total) {
   return pre + v - x;
 }
 
-// The plan of the call, made by every CTA (kPlanThreads threads, all of them
-// call it; `scratch` holds num_rows + 1 ints and may be reused afterwards).
+// The plan of the call, made by every CTA (all its threads, kPlanThreads or
+// more, call it; `tile_start` holds num_rows + 1 ints and may be reused afterwards).
 // The U units of the batch are cut into C = min(chunks, U) ranges, range k from
 // floor(k U / C); a boundary closer than `snap` blocks to an end of its tile
 // moves there, since a split tile costs a partial state and its merge.  Writes
 // the boundaries blockIdx.x and blockIdx.x + 1 to bounds[0], bounds[1], and
-// returns the number of tiles.  A thread shares out the tiles in contiguous
-// runs, so that its work is the same whatever the rows' lengths.
+// returns the number of tiles.  The threads share out the tiles in contiguous
+// runs, so that their work is the same whatever the rows' lengths.
 struct PlanScratch {
-  long long wide[kPlanWarps + 1];
-  int narrow[kPlanWarps + 1];
+  long long wide[kPlanWarps];
+  int narrow[kPlanWarps];
 };
-__device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, int QT, int W, const int32_t* prefix_lens,
+__device__ __forceinline__ int row_of_tile(const int* tile_start, int rows, int x) {
+  int lo = 0, hi = rows;  // the last row that starts at or before tile x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tile_start[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+template <typename Geo>
+__device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, const Geo& geo, const int32_t* prefix_lens,
                                           int chunks, int snap, int* tile_start, PlanScratch* tmp, Place* bounds) {
   const int tid = threadIdx.x;
   const int per = (rows.num_rows + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(tid * per, rows.num_rows), r1 = min(r0 + per, rows.num_rows);
   int mine = 0;
-  for (int i = r0; i < r1; ++i) mine += tiles_of(row_info(rows, i, nullptr), QT);
+  for (int i = r0; i < r1; ++i) mine += geo.tiles(row_info(rows, i, nullptr));
   int T;
   int pre = cta_scan(mine, tmp->narrow, T);
   for (int i = r0; i < r1; ++i) {
     tile_start[i] = pre;
-    pre += tiles_of(row_info(rows, i, nullptr), QT);
+    pre += geo.tiles(row_info(rows, i, nullptr));
   }
   if (tid == 0) tile_start[rows.num_rows] = T;
   if (tid < 2) bounds[tid] = Place{n_kv, 0, 0, 0, 0};
@@ -100,20 +91,11 @@ __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, int Q
   // this thread's run of tiles
   const int run = (T + kPlanThreads - 1) / kPlanThreads;
   const int a = min(tid * run, T), b = min(a + run, T);
-  int i0 = 0;
-  if (a < b) {  // the last row that starts at or before tile a
-    int lo = 0, hi = rows.num_rows;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tile_start[mid] <= a) lo = mid; else hi = mid;
-    }
-    i0 = lo;
-  }
+  const int i0 = a < b ? row_of_tile(tile_start, rows.num_rows, a) : 0;
   long long cost = 0;
   {
-    int i = i0;
+    int i = i0, seen = -1, F = 0;
     RowInfo r{0, 0, 0};
-    int F = 0, seen = -1;
     for (int x = a; x < b; ++x) {
       while (x >= tile_start[i + 1]) ++i;
       if (i != seen) {
@@ -121,7 +103,7 @@ __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, int Q
         F = prefix_lens ? __ldg(prefix_lens + i) : 0;
         seen = i;
       }
-      cost += tile_geom(r, x - tile_start[i], QT, W, F).nb;
+      cost += geo.blocks(r, F, x - tile_start[i]);
     }
   }
   long long U1;
@@ -140,9 +122,8 @@ __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, int Q
     int i = i0;
     for (int x = a; x < b; ++x) {
       while (x >= tile_start[i + 1]) ++i;
-      const RowInfo r = row_info(rows, i, nullptr);
       const int F = prefix_lens ? __ldg(prefix_lens + i) : 0;
-      const int nb = tile_geom(r, x - tile_start[i], QT, W, F).nb;
+      const int nb = geo.blocks(row_info(rows, i, nullptr), F, x - tile_start[i]);
       if (rem < at + nb) {
         Place p{h, x, i, x - tile_start[i], static_cast<int>(rem - at)};
         if (p.off < snap) {
@@ -153,14 +134,8 @@ __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, int Q
             p.tile = 0;
             ++p.h;
           }
-          // its row: the last that starts at or before it
-          int lo = 0, hi = rows.num_rows;
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (tile_start[mid] <= p.tile) lo = mid; else hi = mid;
-          }
-          p.i = lo;
-          p.t = p.tile - tile_start[lo];
+          p.i = row_of_tile(tile_start, rows.num_rows, p.tile);
+          p.t = p.tile - tile_start[p.i];
         }
         bounds[e] = p;
         break;
@@ -171,5 +146,63 @@ __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, int Q
   __syncthreads();
   return T;
 }
+
+// Walks the tiles of a range (one warp, all lanes): the rows are read 32 at a
+// time, one per lane.
+template <typename Geo>
+struct Walk {
+  const ChunkRows& rows;
+  const Geo& geo;
+  const int32_t* prefix_lens;
+  int T;
+  Place at, end;
+  RowInfo r;  // the row of `at`
+  int F;
+  int base;
+  RowInfo mine;
+  int mineF;
+  __device__ __forceinline__ Walk(const ChunkRows& rows_, const Geo& geo_, const int32_t* prefix, int T_,
+                                  const Place& begin, const Place& end_)
+      : rows(rows_), geo(geo_), prefix_lens(prefix), T(T_), at(begin), end(end_), base(-1) {
+    if (more()) load(at.i);
+  }
+  __device__ __forceinline__ void load(int i) {
+    if (base < 0 || i < base || i >= base + 32) {
+      base = i;
+      mine = RowInfo{0, 0, -1};
+      mineF = 0;
+      const int lane = threadIdx.x & 31;
+      if (base + lane < rows.num_rows) {
+        mine = row_info(rows, base + lane, nullptr);
+        if (prefix_lens) mineF = __ldg(prefix_lens + base + lane);
+      }
+    }
+    r.start = __shfl_sync(kFull, mine.start, i - base);
+    r.n = __shfl_sync(kFull, mine.n, i - base);
+    r.L = __shfl_sync(kFull, mine.L, i - base);
+    F = __shfl_sync(kFull, mineF, i - base);
+  }
+  __device__ __forceinline__ bool more() const { return before(at, end); }
+  // the range ends within this tile, or at its start
+  __device__ __forceinline__ bool ends_here() const { return at.h == end.h && at.tile == end.tile; }
+  // to the next tile; `end` is not in the tile just left
+  __device__ __forceinline__ void next() {
+    at.off = 0;
+    ++at.t;
+    if (++at.tile == T) {
+      at.tile = 0;
+      ++at.h;
+      at.i = 0;
+      at.t = 0;
+      if (!more()) return;
+      load(0);
+    }
+    while (at.t >= geo.tiles(r)) {
+      ++at.i;
+      at.t = 0;
+      load(at.i);
+    }
+  }
+};
 
 }  // namespace pkv

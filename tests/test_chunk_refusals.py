@@ -114,12 +114,14 @@ def test_workspace_bytes(lib, pools):
     assert f(pools[api.F16], 32, 8) > 0
     assert f(None, 32, 8) == 0 and f(pools[api.F16], 30, 8) == 0 and f(pools[api.F16], 24, 8) == 0
     assert f(pools[api.F16], 32, 0) == 0 and f(pools[api.F16], 32, 4097) == 0
+    g = lib.paged_attention_mass_workspace_bytes
+    assert g(8) > 0 and g(0) == 0 and g(4097) == 0
 
 
 def mass(pools, kv=api.F16, sc=SCORES):
     return dict(pool=pools[kv], layer=0, q=FAKE, qs=4096, t=api.F16, lse=FAKE, cu=FAKE, tokens=5, bt=FAKE, stride=4,
                 lens=FAKE, rows=2, n_q=32, sc=ctypes.byref(sc), last=0, mass_in=None, mass_out=FAKE, mass_stride=64,
-                stream=None)
+                ws=FAKE, ws_bytes=1 << 40, chunks=8, stream=None)
 
 
 @pytest.mark.parametrize("changes,status", [
@@ -127,7 +129,8 @@ def mass(pools, kv=api.F16, sc=SCORES):
     (dict(t=api.BF16), UNSUPPORTED), (dict(n_q=24), UNSUPPORTED), (dict(qs=4100), INVALID),
     (dict(mass_out=None), INVALID), (dict(mass_in=ctypes.c_void_p((1 << 20) + 1)), INVALID),
     (dict(mass_stride=0), INVALID), (dict(last=-1), INVALID), (dict(sc=None), INVALID), (dict(cu=None), INVALID),
-    (dict(rows=2049), UNSUPPORTED),
+    (dict(rows=2049), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws_bytes=64), WORKSPACE),
+    (dict(ws=ctypes.c_void_p((1 << 20) + 16)), INVALID), (dict(chunks=-1), INVALID), (dict(chunks=4097), UNSUPPORTED),
 ])
 def test_mass(lib, pools, changes, status):
     refused(lib, "paged_attention_mass", mass(pools), changes, status)

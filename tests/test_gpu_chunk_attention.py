@@ -220,6 +220,40 @@ def test_mass(kv, group, last):
     assert c.pool.read_status() == 0
 
 
+@pytest.mark.parametrize("chunks", [1, 2, 7, 152, 400])
+@pytest.mark.parametrize("kv", [api.F16, api.Q8_0])
+def test_mass_splits(kv, chunks):
+    c = R.Chunk(kv, 2, 4, [(90, 1500), (1, 2600), (700, 900), (1, 5)], seed=9)
+    q, _, lse = run(c)
+    ws = api.WorkspaceMass(c.pool, c.n_q, chunks)
+    ws.tensor.fill_(255)  # NaN: no initialisation is needed
+    before = torch.rand(4, 2, 2600, device=c.device)
+    got = api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, mass_in=before,
+                                   mass_out=torch.empty_like(before), workspace=ws)
+    want, tol = R.mass(c, q, lse, SCALE, before)
+    for i, (_, L) in enumerate(c.rows):
+        assert ((got[i, :, :L].double() - want[i, :, :L]).abs() <= tol[i, :, :L]).all(), i
+    assert c.pool.read_status() == 0
+
+
+def test_mass_ignores_what_is_not_a_query():
+    """Tokens behind the last row, another row's queries and a query without an lse may hold anything."""
+    c = R.Chunk(api.F16, 2, 4, [(5, 90), (40, 300)], seed=2, behind=20)
+    q, _, lse = run(c)
+    want, tol = R.mass(c, q, lse, SCALE, torch.zeros(2, 2, 300, device=c.device))
+    q[45:], lse[45:] = math.nan, math.nan
+    got = torch.zeros(2, 2, 300, device=c.device)
+    api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, mass_out=got)
+    for i, (_, L) in enumerate(c.rows):
+        assert ((got[i, :, :L].double() - want[i, :, :L]).abs() <= tol[i, :, :L]).all(), i
+    q[5:45], lse[7, 3] = math.nan, math.nan  # row 1's queries: NaN
+    lse[5:45] = math.nan
+    got = torch.zeros(2, 2, 300, device=c.device)
+    api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, mass_out=got)
+    assert ((got[0, :, :90].double() - want[0, :, :90]).abs() <= tol[0, :, :90]).all()
+    assert (got[1] == 0).all()
+
+
 @pytest.mark.parametrize("kw", [dict(softcap=20.0), dict(bias=True), dict(prefix=True), dict(window=50),
                                 dict(softcap=20.0, bias=True, prefix=True, window=77)])
 def test_mass_scores(kw):
@@ -271,7 +305,15 @@ def test_bounded_waits():
     """The test hook stalls every wait: the call gives up, says so, and the next one is whole again."""
     c = R.Chunk(api.F16, 2, 4, [(65, 500), (1, 900)], seed=6)
     c.pool.set_test_stall(2_000_000)
-    run(c)
+    q, _, lse = run(c)
+    assert c.pool.read_status() & api.DEV_TIMEOUT
+    mass = torch.zeros(2, 2, 900, device=c.device)
+    api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, mass_out=mass)
     assert c.pool.read_status() & api.DEV_TIMEOUT
     c.pool.set_test_stall(0)
-    check(c, *run(c))
+    q, out, lse = run(c, q)
+    check(c, q, out, lse)
+    api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, mass_out=mass)
+    want, tol = R.mass(c, q, lse, SCALE, torch.zeros_like(mass))
+    for i, (_, L) in enumerate(c.rows):
+        assert ((mass[i, :, :L].double() - want[i, :, :L]).abs() <= tol[i, :, :L]).all()
