@@ -38,6 +38,8 @@ constexpr int kMassTok = 256;                        // tokens of a tile
 constexpr uint32_t kBuf = 32768;                     // 128 tokens or 128 query rows
 constexpr int kKBufs = 4;                            // K buffers (q8_0: two of hi and lo)
 constexpr int kQSlots = 2;
+constexpr int kLseSlots = 4;
+constexpr int kTileCost = 1;  // units of a tile besides its blocks (chunk_plan)
 constexpr uint32_t kQRing = kKBufs * kBuf;
 constexpr uint32_t kMassTail = kQRing + kQSlots * kBuf;
 constexpr int kDescs = 4;
@@ -47,7 +49,9 @@ enum : int {
   kBKEmpty = kBKFull + kKBufs,
   kBQFull = kBKEmpty + kKBufs,
   kBQEmpty = kBQFull + kQSlots,
-  kBS = kBQEmpty + kQSlots,  // [half][buffer]
+  kBLse = kBQEmpty + kQSlots,
+  kBLseEmpty = kBLse + kLseSlots,
+  kBS = kBLseEmpty + kLseSlots,  // [half][buffer]
   kBSFree = kBS + 4,
   kBDesc = kBSFree + 4,
   kBDescEmpty = kBDesc + kDescs,
@@ -71,8 +75,8 @@ static_assert(sizeof(Piece) == 64, "");
 struct Tail {
   uint64_t bars[kNumBars];
   Piece piece[kDescs];
-  float lse2[kQSlots][128];  // lse of the block's rows in base 2, +inf: not counted
-  int odd[kQSlots];          // the block has a row that is not counted
+  float lse2[kLseSlots][128];  // lse of a block's rows in base 2, +inf: not counted
+  int odd[kLseSlots];          // the block has a row that is not counted
   volatile int ctl[2];
   uint32_t tmem;
   Place bounds[2];
@@ -83,8 +87,7 @@ constexpr size_t kSmemBytes = 1024 + kMassTail + sizeof(Tail);
 static_assert(kSmemBytes <= 232448, "");
 
 // Tokens t * 256 .. of a row, and the blocks of the queries that attend to
-// any of them (at least one unit: a tile without any still has its weights
-// carried over).
+// any of them (a tile without any still has its weights carried over).
 struct TokenTiles {
   int QT, W, last, stride;
   __device__ __forceinline__ int tiles(const RowInfo& r) const {
@@ -106,8 +109,9 @@ struct TokenTiles {
   __device__ __forceinline__ int blocks(const RowInfo& r, int F, int t) const {
     int b0, b1;
     range(r, F, t, b0, b1);
-    return max(1, b1 - b0);
+    return b1 - b0;
   }
+  __device__ __forceinline__ int lead() const { return kTileCost; }
 };
 
 struct Rec {
@@ -149,8 +153,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
     for (int b = 0; b < kNumBars; ++b) {
       int count = 1;
       if (b < kBKEmpty && kQ8) count = 4;
-      if (b >= kBQFull && b < kBQEmpty) count = 2;
-      if (b >= kBQEmpty && b < kBS) count = 9;
+      if (b >= kBLseEmpty && b < kBS) count = 8;
       if (b >= kBSFree && b < kBDesc) count = 4;
       if (b >= kBDescEmpty && b < kBDrain) count = kReaders;
       mbar_init(bar(b), count);
@@ -187,8 +190,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
       const RowInfo& r = w.r;
       int b0, b1;
       geo.range(r, w.F, w.at.t, b0, b1);
-      const int units = max(1, b1 - b0);
-      const int stop = w.ends_here() ? end.off : units;
+      const int from = w.from(), to = w.to(b1 - b0);
       const int x = p % kDescs;
       if (p >= kDescs && !(ok = wait(kBDescEmpty + x, p / kDescs - 1))) break;
       if (lane == 0) {
@@ -203,10 +205,10 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
         d.L = r.L;
         d.n = r.n;
         d.F = w.F;
-        d.b0 = b0 + w.at.off;
-        d.nb = b1 > b0 ? stop - w.at.off : 0;
-        d.slot = w.at.off > 0 ? 2 * static_cast<int>(blockIdx.x)
-                 : stop < units ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
+        d.b0 = b0 + from;
+        d.nb = to - from;
+        d.slot = from > 0 ? 2 * static_cast<int>(blockIdx.x)
+                 : to < b1 - b0 ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
         d.last = 0;
         mbar_arrive(bar(kBDesc + x));
       }
@@ -358,11 +360,16 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
           odd = odd || !fine;
           v[e] = fine ? v[e] * kLog2e : INFINITY;
         }
-        *reinterpret_cast<float4*>(&tail.lse2[s][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+        const int ls = gq % kLseSlots;
+        if (gq >= kLseSlots && !(ok = wait(kBLseEmpty + ls, gq / kLseSlots - 1))) {
+          ++gq;  // its copy is in flight
+          break;
+        }
+        *reinterpret_cast<float4*>(&tail.lse2[ls][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
         const bool any = __any_sync(kFull, odd);
-        if (lane == 0) tail.odd[s] = any;
+        if (lane == 0) tail.odd[ls] = any;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBQFull + s));
+        if (lane == 0) mbar_arrive(bar(kBLse + ls));
       }
       if (!ok) break;
       __syncwarp();
@@ -462,10 +469,10 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
       }
       float sum = 0.0f, lost = 0.0f;  // the sum over blocks and its rounding error so far
       for (int b = 0; b < d.nb; ++b, ++gq) {
-        const int s = gq % kQSlots;
+        const int s = gq % kLseSlots;
         // the block's lse staged (a half without tokens takes part in the
         // slots' hand-overs all the same)
-        if (!(ok = wait(kBQFull + s, gq / kQSlots))) break;
+        if (!(ok = wait(kBLse + s, gq / kLseSlots))) break;
         if (mine) {
           if (!(ok = wait(kBS + 2 * m + (used & 1), used >> 1))) break;
           tc::fence_after();
@@ -476,16 +483,8 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
           float2 acc[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float v[32];
-            tc::ld32(tS + 32 * q, v);
-            tc::wait_ld();
-            if (q == 3) {
-              tc::fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(kBSFree + 2 * m + (used & 1)));
-            }
+          // the weights of columns 32 q ..: y = c1 s - lse2
+          auto weigh = [&](float (&v)[32], int q) {
             if constexpr (GEN) {
               const int dist0 = past + j - t;
 #pragma unroll
@@ -499,9 +498,10 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
               }
             }
             const float2 mul = make_float2(GEN ? 1.0f : c1, GEN ? 1.0f : c1);
+            const float4* lse4 = reinterpret_cast<const float4*>(&tail.lse2[s][32 * q]);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 l = *reinterpret_cast<const float4*>(&tail.lse2[s][32 * q + e]);
+              const float4 l = lse4[e >> 2];
               float2 y0 = tc::fma2(make_float2(v[e], v[e + 1]), mul, make_float2(-l.x, -l.y));
               float2 y1 = tc::fma2(make_float2(v[e + 2], v[e + 3]), mul, make_float2(-l.z, -l.w));
               if (!fast) {
@@ -514,7 +514,24 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
               acc[(e >> 1) & 3] = tc::add2(acc[(e >> 1) & 3], make_float2(tc::ex2(y0.x), tc::ex2(y0.y)));
               acc[((e >> 1) + 1) & 3] = tc::add2(acc[((e >> 1) + 1) & 3], make_float2(tc::ex2(y1.x), tc::ex2(y1.y)));
             }
-          }
+          };
+          // one load from tensor memory ahead of the arithmetic
+          float v0[32], v1[32];
+          tc::ld32(tS, v0);
+          tc::wait_ld();
+          tc::ld32(tS + 32, v1);
+          weigh(v0, 0);
+          tc::wait_ld();
+          tc::ld32(tS + 64, v0);
+          weigh(v1, 1);
+          tc::wait_ld();
+          tc::ld32(tS + 96, v1);
+          weigh(v0, 2);
+          tc::wait_ld();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBSFree + 2 * m + (used & 1)));
+          weigh(v1, 3);
           ++used;
           const float2 a2 = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
           // compensated: a tile may see hundreds of blocks
@@ -523,7 +540,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
           sum = z;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBQEmpty + s));
+        if (lane == 0) mbar_arrive(bar(kBLseEmpty + s));
       }
       if (!ok) break;
       if (mine && t < d.L) {

@@ -1,11 +1,10 @@
 // chunk_attention.cu — paged_chunk_attention on the fifth-generation tensor
-// cores (tcgen05, accumulators in tensor memory): f16 and bf16 caches; q8_0
-// caches by a warp per (token, query head) for now.
+// cores (tcgen05, accumulators in tensor memory).
 //
 // For one (row, KV head), the (query, query head) pairs are rows of a matrix
 // product: a tile is 256 of them, 256 / G queries, as two halves m of 128.
-// Over the tile's blocks of 128 cached tokens,
-//     S_m = Q_m K^T             128 x 128, both from shared memory
+// Over the tile's blocks of N cached tokens (128; q8_0: 64),
+//     S_m = Q_m K^T             128 x N, both from shared memory
 //     P_m = 2^(y - max)         y the base-2 score, one thread per row
 //     O_m += P_m V              128 x 128, P_m from tensor memory
 // with one pass over K and V and the running maximum and sum of the softmax
@@ -13,18 +12,22 @@
 // block exceeds it by more than 8 (a factor of 256, which f16 and bf16 hold).
 // P_m overwrites S_m in tensor memory as 16-bit pairs: S_0, S_1, O_0 and O_1
 // take all 512 columns.  The halves alternate on the tensor cores: while one
-// is in its softmax, the other's products run.
+// is in its softmax, the other's products run.  P_m is handed over in two
+// parts, so that the first part's products overlap the second's exponentials.
+// q8_0 keys and values enter as two f16 parts, hi and lo (q8_tiles.cuh), two
+// products each.
 //
 // Warps: 0-3 and 4-7 the softmax of half 0 and 1, 8 walks the work and copies
 // Q, 9 issues the products, 10 copies K and V pages (one tensor copy each)
 // into a ring of five 32 KiB slots, 11 mends V blocks that hold tokens no
-// query of the tile attends to.  Hand-overs by shared-memory barriers:
+// query of the tile attends to; with q8_0, 12-15 fill the ring instead of 10
+// and 11.  Hand-overs by shared-memory barriers:
 //   dfull, dempty[x]  descriptor x of a piece (a tile's blocks in this range)
 //   qfull[m], qempty  Q_m landed; the piece's last scores are computed
 //   full, empty[s]    K or V block in ring slot s
 //   land[s]           a V block that warp 11 passes on to full[s]
 //   sfull[m]          S_m computed (and every product issued before it)
-//   pready[m]         P_m written, S_m read
+//   pready[m][part]   part of P_m written (all of S_m read with the last)
 //   ofull[m]          O_m of the piece complete
 // Every wait is bounded; a warp that gives up sets the abort flag, which ends
 // the other waits, and its copies and products are awaited before the CTA ends.
@@ -48,20 +51,34 @@
 #include "attend_row.cuh"
 #include "chunk_device.cuh"
 #include "chunk_plan.cuh"
+#include "q8_tiles.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kAttnThreads = kPlanThreads;
 constexpr int kTileRows = 256;   // (query, query head) rows of a tile: 256 / G queries
-constexpr int kBlockTok = 128;   // cached tokens of a block
+template <int DT>
+constexpr int kBlockTok = DT == PKV_KV_Q8_0 ? 64 : 128;  // cached tokens of a block
+template <int DT>
+constexpr int kAttnThreads = DT == PKV_KV_Q8_0 ? 512 : kPlanThreads;
+#ifndef PKV_CHUNK_TILE_COST
+#define PKV_CHUNK_TILE_COST 2
+#endif
+#ifndef PKV_CHUNK_SNAP
+#define PKV_CHUNK_SNAP 2
+#endif
+// What a tile costs besides its blocks, and how far from a tile's end a
+// boundary moves there, in blocks (chunk_plan).
+template <int DT>
+constexpr int kTileCost = PKV_CHUNK_TILE_COST * (128 / kBlockTok<DT>);
+template <int DT>
+constexpr int kSplitSnap = PKV_CHUNK_SNAP * (128 / kBlockTok<DT>);
 constexpr int kSlots = 5;
 constexpr uint32_t kHalf = 32768;                    // bytes of Q_m, and of a ring slot
 constexpr uint32_t kRing = 2 * kHalf;                // the ring, behind Q
 constexpr uint32_t kTail = kRing + kSlots * kHalf;   // barriers and descriptors
 constexpr int kDescs = 4;
-constexpr int kSplitSnap = 2;   // blocks: see chunk_plan
 constexpr uint32_t kTmemS = 0, kTmemO = 256;         // S_m at 128 m, O_m at 256 + 128 m
 
 // barriers
@@ -70,8 +87,8 @@ enum : int {
   kBEmpty = kBFull + kSlots,
   kBLand = kBEmpty + kSlots,
   kBS = kBLand + kSlots,
-  kBP = kBS + 2,
-  kBO = kBP + 2,
+  kBP = kBS + 2,  // [half][part]
+  kBO = kBP + 4,
   kBQ = kBO + 2,
   kBQEmpty = kBQ + 2,
   kBDesc = kBQEmpty + 1,
@@ -80,7 +97,8 @@ enum : int {
   kBStall,
   kNumBars,
 };
-constexpr int kDescReaders = 11;  // 8 softmax warps, products, copies, mending
+template <int DT>
+constexpr int kDescReaders = DT == PKV_KV_Q8_0 ? 13 : 11;  // softmax, products, copies and mending (4 warps)
 
 // A piece: blocks kb .. kb + nb - 1 of one tile for KV head h.
 struct Piece {
@@ -113,6 +131,7 @@ struct TileGeom {
   int kb;    // first block
   int nb;    // blocks
 };
+template <int DT>
 struct QueryTiles {
   int QT, W;
   __device__ __forceinline__ int tiles(const RowInfo& r) const { return r.L >= 0 ? (r.n + QT - 1) / QT : 0; }
@@ -123,11 +142,12 @@ struct QueryTiles {
     g.P0 = r.L - r.n + j0;
     g.t_lo = seen_from(g.P0, W);
     g.t_hi = seen_to(g.P0 + g.nq - 1, r.L, F);
-    g.kb = g.t_lo / kBlockTok;
-    g.nb = (g.t_hi + kBlockTok - 1) / kBlockTok - g.kb;
+    g.kb = g.t_lo / kBlockTok<DT>;
+    g.nb = (g.t_hi + kBlockTok<DT> - 1) / kBlockTok<DT> - g.kb;
     return g;
   }
   __device__ __forceinline__ int blocks(const RowInfo& r, int F, int t) const { return tile(r, F, t).nb; }
+  __device__ __forceinline__ int lead() const { return kTileCost<DT>; }
 };
 
 // ------------------------------------------------------------ workspace ----
@@ -175,8 +195,8 @@ __device__ __noinline__ void redo_row(const ChunkAttnArgs& a, const Piece& p, in
   const int lane = threadIdx.x & 31;
   const int G = a.n_q / a.pool.n_kv;
   const int j = r / G, g = p.h * G + r % G, P = p.P0 + j;
-  const int t0 = max(seen_from(P, a.pool.window), p.kb * kBlockTok);
-  const int t1 = min(seen_to(P, p.L, p.F), (p.kb + p.nb) * kBlockTok);
+  const int t0 = max(seen_from(P, a.pool.window), p.kb * kBlockTok<DT>);
+  const int t1 = min(seen_to(P, p.L, p.F), (p.kb + p.nb) * kBlockTok<DT>);
   const float slope = a.sc.slopes ? __ldg(a.sc.slopes + g) : 0.0f;
   float m, l, acc[4];
   attend_row<DT>(a.pool, a.rows, a.sc, p.i, p.h, slope, P,
@@ -208,10 +228,14 @@ __device__ __forceinline__ void fill_skipped(const ChunkAttnArgs& a) {
 
 // GEN: scores with a cap, a bias, or a scale that is not positive.
 template <int DT, bool GEN>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkAttnArgs a, const __grid_constant__ TileMaps maps,
                            const __grid_constant__ CUtensorMap qmap) {
   using F = Io<DT>;
+  constexpr bool kQ8 = DT == PKV_KV_Q8_0;
+  constexpr int N = kBlockTok<DT>;                   // tokens of a block
+  constexpr int kPages = N / kPage;                  // its pages
+  constexpr uint32_t kPart = N * kD * 2;             // bytes of one part of it
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   Tail& tail = *reinterpret_cast<Tail*>(smem + kTail);
@@ -229,8 +253,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tail.ctl[0] = 0;
     for (int b = 0; b < kNumBars; ++b) {
       int count = 1;
-      if (b >= kBP && b < kBP + 2) count = 4;
-      if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders;
+      if (b < kBEmpty && kQ8) count = 4;
+      if (b >= kBP && b < kBO) count = 4;
+      if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT>;
       mbar_init(bar(b), count);
     }
     fence_mbar_init();
@@ -244,8 +269,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  const QueryTiles geo{QT, a.pool.window};
-  const int T = chunk_plan(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, kSplitSnap,
+  const QueryTiles<DT> geo{QT, a.pool.window};
+  const int T = chunk_plan(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, kSplitSnap<DT>,
                            reinterpret_cast<int*>(smem + kRing), &tail.scratch, tail.bounds);
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tail.tmem);
@@ -258,22 +283,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   auto wait = [&](int b, uint32_t parity) { return tc::warp_wait(bar(b), parity & 1u, ctl, a.pool.status); };
   auto pages_of = [&](const Piece& p, int b, int& lo, int& hi) {  // pages of a block that are read
-    const int first = (p.kb + b) * (kBlockTok / kPage);
+    const int first = (p.kb + b) * kPages;
     lo = max(first, p.t_lo / kPage);
-    hi = min(first + kBlockTok / kPage, (p.t_hi + kPage - 1) / kPage);
+    hi = min(first + kPages, (p.t_hi + kPage - 1) / kPage);
   };
   // V blocks that warp 11 sees: with tokens outside [t_lo, t_hi) in their
   // pages (zeroed), or masked for part of the tile (searched)
   auto mended = [&](const Piece& p, int b) {
-    const int t0 = (p.kb + b) * kBlockTok;
-    return t0 < p.full_lo || t0 + kBlockTok > p.full_hi;
+    const int t0 = (p.kb + b) * N;
+    return t0 < p.full_lo || t0 + N > p.full_hi;
   };
 
+  if (warp >= 8) {
+  if constexpr (!kQ8) tc::fewer_registers<88>();  // 2 x 208 + 88 = 3 x 168, what the launch has
   if (stalled) {
-    // nothing to do
+    // test hook: every warp gave up
   } else if (warp == 8) {
     // ------------------------------------------------- pieces and queries ----
-    Walk<QueryTiles> w(a.rows, geo, a.sc.prefix_lens, T, begin, end);
+    Walk<QueryTiles<DT>> w(a.rows, geo, a.sc.prefix_lens, T, begin, end);
     int p = 0;
     bool ok = true;
     uint32_t q1 = 0;  // pieces with both halves so far
@@ -281,7 +308,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const Place& c = w.at;
       const RowInfo& r = w.r;
       const TileGeom g = geo.tile(r, w.F, c.t);
-      const int b1 = w.ends_here() ? end.off : g.nb;
+      const int b0 = w.from(), b1 = w.to(g.nb);
       const int x = p % kDescs;
       const int tok = r.start + c.t * QT;
       if (p >= kDescs && !(ok = wait(kBDescEmpty + x, p / kDescs - 1))) break;
@@ -294,13 +321,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         d.P0 = g.P0;
         d.L = r.L;
         d.F = w.F;
-        d.kb = g.kb + c.off;
-        d.nb = b1 - c.off;
+        d.kb = g.kb + b0;
+        d.nb = b1 - b0;
         d.t_lo = g.t_lo;
         d.t_hi = g.t_hi;
         d.full_lo = seen_from(g.P0 + g.nq - 1, a.pool.window);
         d.full_hi = seen_to(g.P0, r.L, w.F);
-        d.slot = c.off > 0 ? 2 * static_cast<int>(blockIdx.x) : b1 < g.nb ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
+        d.slot = b0 > 0 ? 2 * static_cast<int>(blockIdx.x) : b1 < g.nb ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
         d.last = 0;
         tail.bad[x] = 0;
         mbar_arrive(bar(kBDesc + x));
@@ -339,7 +366,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (q1 > 0) mbar_wait_bounded(bar(kBQ + 1), (q1 - 1) & 1, &zero);
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (!kQ8 && warp == 10) {
     // ------------------------------------------------------ K and V pages ----
     int gs = 0;              // slots filled
     uint32_t landed = 0;     // parity of each slot's land barrier
@@ -368,7 +395,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           record_status(a.pool.status, PKV_DEV_BAD_PAGE);
           pg = 0;
         }
-        const uint32_t in_slot = (lo & 7) * 4096u + lane * 4096u;
+        const uint32_t in_slot = (lo & (kPages - 1)) * 4096u + lane * 4096u;
         const bool mend = mended(d, b);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
@@ -400,7 +427,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int zero = 0;
     if (my_bar) mbar_wait_bounded(my_bar, my_par, &zero);
     __syncwarp();
-  } else if (warp == 11) {
+  } else if (!kQ8 && warp == 11) {
     // ------------------------------------------------------------ mending ----
     int gs = 0;
     uint32_t landed = 0;
@@ -419,7 +446,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         landed ^= 1u << s;
         uint8_t* v = smem + kRing + s * kHalf;
-        const int t0 = (d.kb + b) * kBlockTok;
+        const int t0 = (d.kb + b) * N;
         int lo, hi;
         pages_of(d, b, lo, hi);
         // tokens of the pages read that no query of the tile attends to
@@ -436,7 +463,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
         // 0 * x is NaN for the others
         uint32_t bits = 0;
-        const uint4* w = reinterpret_cast<const uint4*>(v + (lo & 7) * 4096);
+        const uint4* w = reinterpret_cast<const uint4*>(v + (lo & (kPages - 1)) * 4096);
         const int n16 = (hi - lo) * 256;
         if constexpr (DT == PKV_KV_BF16) {
           __nv_bfloat162 acc = __floats2bfloat162_rn(0.f, 0.f);
@@ -473,19 +500,98 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
     }
     fill_skipped(a);
+  } else if (kQ8 && warp >= 12) {
+    // ------------------------------ q8_0 keys and values as two f16 parts ----
+    const int row = (tid - 384) >> 3, col = (tid - 384) & 7;  // 8 threads a token, 16 codes each
+    int gs = 0;
+    bool ok = true;
+    for (int p = 0; ok; ++p) {
+      const int x = p % kDescs;
+      if (!wait(kBDesc + x, p / kDescs)) break;
+      const Piece d = tail.piece[x];
+      if (d.last) break;
+      const int32_t* bt = a.rows.block_table + static_cast<long long>(d.i) * a.rows.bt_stride;
+      auto entry = [&](int b) {  // lane e: page e of the block, -1 where it is not read
+        int lo, hi;
+        pages_of(d, b, lo, hi);
+        const int q = (d.kb + b) * kPages + lane;
+        int pg = lane < kPages && q >= lo && q < hi ? __ldg(bt + q) : -2;
+        if (pg != -2 && (pg < 0 || pg >= a.pool.num_pages)) {
+          record_status(a.pool.status, PKV_DEV_BAD_PAGE);
+          pg = 0;
+        }
+        return pg;
+      };
+      int next = entry(0);
+      for (int b = 0; b < d.nb && ok; ++b) {
+        const int pg = next;
+        if (b + 1 < d.nb) next = entry(b + 1);
+        const int t0 = (d.kb + b) * N;
+        const bool mend = mended(d, b);
+        uint4 code[2][kPages];
+        __half sc[2][kPages];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+#pragma unroll
+          for (int e = 0; e < kPages; ++e) {  // token `row` of page e
+            const int pe = __shfl_sync(kFull, pg, e);
+            const int t = t0 + e * kPage + row;
+            code[v][e] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // codes 0
+            sc[v][e] = __float2half_rn(0.0f);
+            if (pe >= 0 && t >= d.t_lo && t < d.t_hi) {
+              const long long at = (static_cast<long long>(pe) * a.pool.n_kv + d.h) * kPage + row;
+              code[v][e] = __ldg(reinterpret_cast<const uint4*>((v ? a.pool.v_data : a.pool.k_data) + at * kD) + col);
+              sc[v][e] = __ldg(reinterpret_cast<const __half*>(v ? a.pool.v_scales : a.pool.k_scales) +
+                               at * (kD / kQBlock) + (col >> 1));
+            }
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int s = (gs + v) % kSlots;
+          if (gs + v >= kSlots && !(ok = wait(kBEmpty + s, (gs + v) / kSlots - 1))) break;
+          uint8_t* hi = smem + kRing + s * kHalf;
+          bool odd = false;
+#pragma unroll
+          for (int e = 0; e < kPages; ++e) {
+            odd = odd || !(fabsf(__half2float(sc[v][e])) <= 65504.0f);
+            const __half2 s2 = __half2half2(sc[v][e]);
+            uint4 h0, l0, h1, l1;
+            q8_split8(make_uint2(code[v][e].x, code[v][e].y), s2, h0, l0);
+            q8_split8(make_uint2(code[v][e].z, code[v][e].w), s2, h1, l1);
+            const uint32_t o0 = tile_vec(kPage * e + row, 2 * col), o1 = tile_vec(kPage * e + row, 2 * col + 1);
+            *reinterpret_cast<uint4*>(hi + o0) = h0;
+            *reinterpret_cast<uint4*>(hi + o1) = h1;
+            *reinterpret_cast<uint4*>(hi + kPart + o0) = l0;
+            *reinterpret_cast<uint4*>(hi + kPart + o1) = l1;
+          }
+          if (v == 1 && mend && odd) *(volatile int*)&tail.bad[x] = 1;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBFull + s));
+        }
+        gs += 2;
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
+    }
+    if (warp == 12) fill_skipped(a);
   } else if (warp == 9) {
     // ----------------------------------------------------------- products ----
     const bool leader = tc::elect_one();
-    const uint32_t id_s = tc::idesc(128, 128, false, false, F::kFormat);
+    const uint32_t id_s = tc::idesc(128, N, false, false, F::kFormat);
     const uint32_t id_o = tc::idesc(128, 128, false, true, F::kFormat);
     // scores S_m of the K block in slot s
     auto issue_s = [&](int m, int s) {
       const uint64_t qd = tc::desc(sbase + m * kHalf, 16, 1024), kd = tc::desc(sbase + kRing + s * kHalf, 16, 2048);
       if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_ss(tmem + kTmemS + 128 * m, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                     kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0);
+        for (int part = 0; part < (kQ8 ? 2 : 1); ++part)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_ss(tmem + kTmemS + 128 * m, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                       kd + ((part * kPart + (kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, part > 0 || kk > 0);
         tc::commit(bar(kBS + m));
       }
       __syncwarp();
@@ -496,35 +602,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       bool first, last, two;
     } v{0, 0, 0, false, false, false};
     bool due = false;
-    uint32_t np[2] = {0, 0};  // P blocks consumed per half
+    uint32_t np[2] = {0, 0};  // blocks of P consumed per half
+    // O_m of the due block, the pages of part 0 and then those of part 1 of P
     auto issue_o = [&](int m) {
-      const uint64_t vd = tc::desc(sbase + kRing + v.s * kHalf + v.lo * 4096, 1024, 2048);
-      if (leader) {
-        for (int kk = 0; kk < v.n; ++kk)
-          tc::mma_ts(tmem + kTmemO + 128 * m, tmem + kTmemS + 128 * m + 8 * (v.lo + kk), vd + kk * (4096 >> 4), id_o,
-                     !v.first || kk > 0);
-        if (v.last) tc::commit(bar(kBO + m));
+      const uint64_t vd = tc::desc(sbase + kRing + v.s * kHalf, 1024, 2048);
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        if (!wait(kBP + 2 * m + part, np[m])) return false;
+        tc::fence_after();
+        if (leader) {
+          const int from = max(v.lo, part * (kPages / 2)), to = min(v.lo + v.n, (part + 1) * (kPages / 2));
+          for (int kk = from; kk < to; ++kk) {
+            tc::mma_ts(tmem + kTmemO + 128 * m, tmem + kTmemS + 128 * m + 8 * kk, vd + kk * (4096 >> 4), id_o,
+                       !v.first || kk > v.lo);
+            if constexpr (kQ8)
+              tc::mma_ts(tmem + kTmemO + 128 * m, tmem + kTmemS + 128 * m + 8 * kk, vd + ((kPart + kk * 4096) >> 4),
+                         id_o, 1);
+          }
+          if (part == 1 && v.last) tc::commit(bar(kBO + m));
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      ++np[m];
+      return true;
     };
     int gs = 0;
     bool ok = true, any = false;
     auto half0 = [&]() {  // O_0 of the due block
       if (!due) return true;
-      if (!wait(kBP, np[0]) || !wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kSlots)) return false;
-      ++np[0];
-      tc::fence_after();
-      issue_o(0);
-      return true;
+      return wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kSlots) && issue_o(0);
     };
     auto half1 = [&]() {
       if (!due) return true;
-      if (v.two) {
-        if (!wait(kBP + 1, np[1])) return false;
-        ++np[1];
-        tc::fence_after();
-        issue_o(1);
-      }
+      if (v.two && !issue_o(1)) return false;
       if (leader) tc::commit(bar(kBEmpty + v.s));
       __syncwarp();
       due = false;
@@ -562,7 +672,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         int lo, hi;
         pages_of(d, b, lo, hi);
         v.s = (gs + 1) % kSlots;
-        v.lo = lo & 7;
+        v.lo = lo & (kPages - 1);
         v.n = hi - lo;
         v.first = b == 0;
         v.last = b + 1 == d.nb;
@@ -584,6 +694,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (lane == 0) mbar_wait_bounded(bar(kBDrain), 0, &zero);
       __syncwarp();
     }
+  }
   } else {
     // ------------------------------------------------------------ softmax ----
     const int m = warp >> 2, quarter = warp & 3;
@@ -591,8 +702,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t tS = tmem + lanes + kTmemS + 128 * m, tO = tmem + lanes + kTmemO + 128 * m;
     const int jq = r / G;
+    if constexpr (!kQ8) tc::more_registers<208>();
     uint32_t blocks = 0, pieces = 0;
-    bool ok = true;
+    bool ok = !stalled;
     const float c1 = a.sc.scale * kLog2e;
     const float inv_cap = a.sc.softcap > 0.0f ? a.sc.scale / a.sc.softcap : 0.0f, cap2 = a.sc.softcap * kLog2e;
     for (int p = 0; ok; ++p) {
@@ -611,45 +723,57 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if constexpr (GEN) slope2 = a.sc.slopes ? __ldg(a.sc.slopes + g) * kLog2e : 0.0f;
         float mx = -INFINITY;  // the maximum in force, base 2
         float sub = 0.0f;      // what is taken off the scores: mx - shift (0 before a first score)
-        float2 l2 = make_float2(0.0f, 0.0f);
+        float2 l2[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l2[e] = make_float2(0.0f, 0.0f);
         for (int b = 0; b < d.nb; ++b, ++blocks) {
-          const int t0 = (d.kb + b) * kBlockTok;
-          const bool fast = __all_sync(kFull, t0 >= lo && t0 + kBlockTok <= hi);
+          const int t0 = (d.kb + b) * N;
+          const bool fast = __all_sync(kFull, t0 >= lo && t0 + N <= hi);
           if (!(ok = wait(kBS + m, blocks))) break;
           tc::fence_after();
           if (any) {
-            float s[128];
+            float s[N];
+            constexpr int kH = N / 2;  // columns of a part
+            // the scores of part `part`, and their maximum
+            auto form = [&](int part) {
+              if constexpr (GEN) {
+                const float dist0 = static_cast<float>(P - t0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) tc::ld32(tS + 32 * e, s + 32 * e);
-            tc::wait_ld();
-            if constexpr (GEN) {
-              const float dist0 = static_cast<float>(P - t0);
-#pragma unroll
-              for (int e = 0; e < 128; ++e) {
-                float y;
-                if (a.sc.softcap > 0.0f) {
-                  // tanh z = 1 - 2 / (1 + e^2z)
-                  y = cap2 - __fdividef(2.0f * cap2, 1.0f + tc::ex2(s[e] * (2.0f * kLog2e * inv_cap)));
-                } else {
-                  y = s[e] * c1;
+                for (int e = part * kH; e < (part + 1) * kH; ++e) {
+                  float y;
+                  if (a.sc.softcap > 0.0f) {
+                    // tanh z = 1 - 2 / (1 + e^2z)
+                    y = cap2 - __fdividef(2.0f * cap2, 1.0f + tc::ex2(s[e] * (2.0f * kLog2e * inv_cap)));
+                  } else {
+                    y = s[e] * c1;
+                  }
+                  s[e] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(e)), y);
                 }
-                s[e] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(e)), y);
               }
-            }
-            if (!fast) {
-              const int from = lo - t0, to = hi - t0;
+              if (!fast) {
+                const int from = lo - t0, to = hi - t0;
 #pragma unroll
-              for (int e = 0; e < 128; ++e) s[e] = e >= from && e < to ? s[e] : -INFINITY;
-            }
-            float b0 = s[0], b1 = s[1], b2 = s[2], b3 = s[3];
+                for (int e = part * kH; e < (part + 1) * kH; ++e) s[e] = e >= from && e < to ? s[e] : -INFINITY;
+              }
+              float x0 = s[part * kH], x1 = s[part * kH + 1], x2 = s[part * kH + 2], x3 = s[part * kH + 3];
 #pragma unroll
-            for (int e = 4; e < 128; e += 4) {
-              b0 = fmaxf(b0, s[e]);
-              b1 = fmaxf(b1, s[e + 1]);
-              b2 = fmaxf(b2, s[e + 2]);
-              b3 = fmaxf(b3, s[e + 3]);
-            }
-            float bm = fmaxf(fmaxf(b0, b1), fmaxf(b2, b3));
+              for (int e = part * kH + 4; e + 8 <= (part + 1) * kH; e += 8) {
+                x0 = tc::max3(x0, s[e], s[e + 1]);
+                x1 = tc::max3(x1, s[e + 2], s[e + 3]);
+                x2 = tc::max3(x2, s[e + 4], s[e + 5]);
+                x3 = tc::max3(x3, s[e + 6], s[e + 7]);
+              }
+              const int e = (part + 1) * kH - 4;
+              return tc::max3(tc::max3(x0, s[e], s[e + 1]), tc::max3(x1, s[e + 2], s[e + 3]), fmaxf(x2, x3));
+            };
+#pragma unroll
+            for (int e = 0; e < kH / 32; ++e) tc::ld32(tS + 32 * e, s + 32 * e);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = kH / 32; e < N / 32; ++e) tc::ld32(tS + 32 * e, s + 32 * e);
+            float bm = form(0);
+            tc::wait_ld();
+            bm = fmaxf(bm, form(1));
             if constexpr (!GEN) bm *= c1;
             const bool raise = bm > mx + 8.0f;  // also from -inf
             if (__any_sync(kFull, raise)) {
@@ -658,8 +782,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 al = tc::ex2(mx - bm);
                 mx = bm;
                 sub = bm - F::kShift;
-                l2.x *= al;
-                l2.y *= al;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  l2[e].x *= al;
+                  l2[e].y *= al;
+                }
               }
               if (b > 0) {
                 // the values products so far are complete: S was issued after them
@@ -676,28 +803,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             const float2 mul = make_float2(GEN ? 1.0f : c1, GEN ? 1.0f : c1), off = make_float2(-sub, -sub);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[16];
+            for (int part = 0; part < 2; ++part) {
 #pragma unroll
-              for (int u = 0; u < 16; ++u) {
-                const float2 y = tc::fma2(make_float2(s[32 * e + 2 * u], s[32 * e + 2 * u + 1]), mul, off);
-                const float2 pr = make_float2(tc::ex2(y.x), tc::ex2(y.y));
-                l2 = tc::add2(l2, pr);
-                w[u] = F::pack(pr.x, pr.y);
+              for (int e = part * (kH / 32); e < (part + 1) * (kH / 32); ++e) {
+                uint32_t w[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                  const float2 y = tc::fma2(make_float2(s[32 * e + 2 * u], s[32 * e + 2 * u + 1]), mul, off);
+                  const float2 pr = make_float2(tc::ex2(y.x), tc::ex2(y.y));
+                  l2[u & 3] = tc::add2(l2[u & 3], pr);
+                  w[u] = F::pack(pr.x, pr.y);
+                }
+                tc::st16(tS + 16 * e, w);
               }
-              tc::st16(tS + 16 * e, w);
+              tc::wait_st();
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(kBP + 2 * m + part));
             }
-            tc::wait_st();
+          } else {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(kBP + 2 * m));
+              mbar_arrive(bar(kBP + 2 * m + 1));
+            }
           }
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBP + m));
         }
         if (!ok || !(ok = wait(kBO + m, pieces))) break;
         ++pieces;
         tc::fence_after();
         if (any) {
-          const float l = l2.x + l2.y;
+          const float2 la = tc::add2(tc::add2(l2[0], l2[1]), tc::add2(l2[2], l2[3]));
+          const float l = la.x + la.y;
           const float inv = d.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
           const long long row = static_cast<long long>(d.tok + jq) * a.n_q + g;
           float watch = 0.0f;  // NaN once a value is not finite
@@ -837,37 +975,6 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
   if (a.lse && warp == 0) a.lse[row] = (M + log2f(Lsum)) * kLn2;
 }
 
-// ------------------------------------------------------------------ q8_0 ----
-constexpr int kRowWarps = 8;
-
-template <int DT>
-__global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(const __grid_constant__ ChunkAttnArgs a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0) report_rows(a.rows, a.pool.status);
-  const long long item = static_cast<long long>(blockIdx.x) * kRowWarps + warp;
-  const int tok = static_cast<int>(item / a.n_q), g = static_cast<int>(item % a.n_q);
-  if (tok >= a.rows.total_tokens) return;
-  const int i = row_of_token(a.rows, tok);
-  if (i < 0) return;
-  const RowInfo r = row_info(a.rows, i, nullptr);
-  if (r.n == 0) return;
-  float m = -INFINITY, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (r.L >= 0) {
-    const int P = r.L - r.n + tok - r.start;
-    const int F = a.sc.prefix_lens ? __ldg(a.sc.prefix_lens + i) : 0;
-    const float slope = a.sc.slopes ? __ldg(a.sc.slopes + g) : 0.0f;
-    attend_row<DT>(a.pool, a.rows, a.sc, i, g / (a.n_q / a.pool.n_kv), slope, P,
-                   a.q + (tok * a.q_stride + static_cast<long long>(g) * kD) * 2, seen_from(P, a.pool.window),
-                   seen_to(P, r.L, F), m, l, acc);
-  }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  const long long to = (static_cast<long long>(tok) * a.n_q + g) * kD + 4 * lane;
-  *reinterpret_cast<uint2*>(a.out + to * 2) =
-      make_uint2(Io<DT>::pack(acc[0] * inv, acc[1] * inv), Io<DT>::pack(acc[2] * inv, acc[3] * inv));
-  if (a.lse && lane == 0)
-    a.lse[static_cast<long long>(tok) * a.n_q + g] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
-}
-
 // ------------------------------------------------------------- launchers ----
 template <int DT, bool GEN>
 cudaError_t launch_attention_t(const ChunkAttnArgs& a, const TileMaps& maps, const CUtensorMap& qmap, cudaStream_t st) {
@@ -886,7 +993,7 @@ cudaError_t launch_attention_t(const ChunkAttnArgs& a, const TileMaps& maps, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.chunks);
-  cfg.blockDim = dim3(kAttnThreads);
+  cfg.blockDim = dim3(kAttnThreads<DT>);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -912,12 +1019,6 @@ size_t chunk_attention_workspace(int n_q, int n_kv, int chunks) {
 }
 
 cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, const TileMaps& maps, cudaStream_t st) {
-  if (a.pool.dtype == PKV_KV_Q8_0) {
-    const long long items = static_cast<long long>(a.rows.total_tokens) * a.n_q;
-    const dim3 grid(static_cast<unsigned>((items + kRowWarps - 1) / kRowWarps));
-    chunk_rows_kernel<PKV_KV_Q8_0><<<grid, kRowWarps * 32, 0, st>>>(a);
-    return cudaGetLastError();
-  }
   CUtensorMap qmap;
   cudaError_t e = encode_query_map(&qmap, a.pool.dtype == PKV_KV_BF16, a.q, a.q_stride, a.n_q, a.n_q / a.pool.n_kv,
                                    a.rows.total_tokens, 128 / (a.n_q / a.pool.n_kv));
@@ -926,8 +1027,11 @@ cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, const TileMaps& maps,
   if (a.pool.dtype == PKV_KV_F16)
     return gen ? launch_attention_t<PKV_KV_F16, true>(a, maps, qmap, st)
                : launch_attention_t<PKV_KV_F16, false>(a, maps, qmap, st);
-  return gen ? launch_attention_t<PKV_KV_BF16, true>(a, maps, qmap, st)
-             : launch_attention_t<PKV_KV_BF16, false>(a, maps, qmap, st);
+  if (a.pool.dtype == PKV_KV_BF16)
+    return gen ? launch_attention_t<PKV_KV_BF16, true>(a, maps, qmap, st)
+               : launch_attention_t<PKV_KV_BF16, false>(a, maps, qmap, st);
+  return gen ? launch_attention_t<PKV_KV_Q8_0, true>(a, maps, qmap, st)
+             : launch_attention_t<PKV_KV_Q8_0, false>(a, maps, qmap, st);
 }
 
 // The queries as a 4-D tensor {64 dims, heads, tokens, 2 halves of the dims},

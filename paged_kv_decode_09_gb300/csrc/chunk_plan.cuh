@@ -13,12 +13,15 @@ constexpr int kPlanThreads = 384;  // the first threads of a CTA make its plan
 constexpr int kPlanWarps = kPlanThreads / 32;
 
 // What a kernel tells the plan (Geo below):
-//   int tiles(const RowInfo&)                    tiles of a row
-//   int blocks(const RowInfo&, int F, int t)     blocks of its tile t, at least 1
-//   F is prefix_lens[i], or 0 without.
+//   int tiles(const RowInfo&)                 tiles of a row
+//   int blocks(const RowInfo&, int F, int t)  blocks of its tile t
+//   lead()                                    units a tile costs besides its
+//                                             blocks, at least 1
+// F is prefix_lens[i], or 0 without.  A tile is lead() units, then one per block.
 
-// A place in the work: block `off` of tile `tile` (counted over the batch;
-// tile t of row i) for KV head h.  The end of all work is {n_kv, 0, .., 0}.
+// A place in the work: unit `off` of tile `tile` (counted over the batch; tile
+// t of row i) for KV head h; 0, or lead() + the block that comes next.  The end
+// of all work is {n_kv, 0, .., 0}.
 struct Place {
   int h, tile, i, t, off;
 };
@@ -54,7 +57,7 @@ __device__ __forceinline__ T cta_scan(T x, T* tmp, T& total) {
 // The plan of the call, made by every CTA (all its threads, kPlanThreads or
 // more, call it; `tile_start` holds num_rows + 1 ints and may be reused afterwards).
 // The U units of the batch are cut into C = min(chunks, U) ranges, range k from
-// floor(k U / C); a boundary closer than `snap` blocks to an end of its tile
+// floor(k U / C); a boundary less than `snap` blocks from an end of its tile
 // moves there, since a split tile costs a partial state and its merge.  Writes
 // the boundaries blockIdx.x and blockIdx.x + 1 to bounds[0], bounds[1], and
 // returns the number of tiles.  The threads share out the tiles in contiguous
@@ -103,7 +106,7 @@ __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, const
         F = prefix_lens ? __ldg(prefix_lens + i) : 0;
         seen = i;
       }
-      cost += geo.blocks(r, F, x - tile_start[i]);
+      cost += geo.lead() + geo.blocks(r, F, x - tile_start[i]);
     }
   }
   long long U1;
@@ -123,10 +126,10 @@ __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, const
     for (int x = a; x < b; ++x) {
       while (x >= tile_start[i + 1]) ++i;
       const int F = prefix_lens ? __ldg(prefix_lens + i) : 0;
-      const int nb = geo.blocks(row_info(rows, i, nullptr), F, x - tile_start[i]);
+      const int nb = geo.lead() + geo.blocks(row_info(rows, i, nullptr), F, x - tile_start[i]);
       if (rem < at + nb) {
         Place p{h, x, i, x - tile_start[i], static_cast<int>(rem - at)};
-        if (p.off < snap) {
+        if (p.off < geo.lead() + snap) {
           p.off = 0;
         } else if (nb - p.off < snap) {  // the next tile's start
           p.off = 0;
@@ -185,6 +188,9 @@ struct Walk {
   __device__ __forceinline__ bool more() const { return before(at, end); }
   // the range ends within this tile, or at its start
   __device__ __forceinline__ bool ends_here() const { return at.h == end.h && at.tile == end.tile; }
+  // the tile's blocks in the range: [from, to) of its nb
+  __device__ __forceinline__ int from() const { return max(0, at.off - geo.lead()); }
+  __device__ __forceinline__ int to(int nb) const { return ends_here() ? end.off - geo.lead() : nb; }
   // to the next tile; `end` is not in the tile just left
   __device__ __forceinline__ void next() {
     at.off = 0;
