@@ -75,7 +75,7 @@ static_assert(sizeof(Piece) == 64, "");
 struct Tail {
   uint64_t bars[kNumBars];
   Piece piece[kDescs];
-  float lse2[kLseSlots][128];  // lse of a block's rows in base 2, +inf: not counted
+  float lse2[kLseSlots][128];  // minus the lse of a block's rows in base 2, -inf: not counted
   int odd[kLseSlots];          // the block has a row that is not counted
   volatile int ctl[2];
   uint32_t tmem;
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
         for (int e = 0; e < 4; ++e) {
           const bool fine = fabsf(v[e]) <= 3.0e38f;  // neither infinite nor NaN
           odd = odd || !fine;
-          v[e] = fine ? v[e] * kLog2e : INFINITY;
+          v[e] = fine ? -v[e] * kLog2e : -INFINITY;
         }
         const int ls = gq % kLseSlots;
         if (gq >= kLseSlots && !(ok = wait(kBLseEmpty + ls, gq / kLseSlots - 1))) {
@@ -382,22 +382,27 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
     __syncwarp();
   } else if (warp == 9) {
     // ----------------------------------------------------------- products ----
-    const bool leader = tc::elect_one();
-    const uint32_t id = tc::idesc(128, 128, false, false, DT == PKV_KV_BF16 ? 1u : 0u);
+    // converged and uniform throughout: see tcgen05.cuh
+    const uint32_t lead = tc::elect_one();
+    const uint32_t tm = tc::uniform(tmem);
+    constexpr uint32_t id = tc::idesc(128, 128, false, false, DT == PKV_KV_BF16 ? 1u : 0u);
+    constexpr uint32_t kHiK = tc::desc_hi(2048), kHiQ = tc::desc_hi(1024);
+    const uint32_t k_lo = tc::desc_lo(sbase, 16), q_lo = tc::desc_lo(sbase + kQRing, 16);
     int gq = 0, kp = 0;
     uint32_t used[2] = {0, 0};  // score buffers filled per half
     bool ok = true, any = false;
     for (int p = 0; ok; ++p) {
       const int x = p % kDescs;
       if (!wait(kBDesc + x, p / kDescs)) break;
-      const Piece d = tail.piece[x];
-      if (d.last) break;
-      const bool two = d.t0 + 128 < d.L;
-      for (int b = 0; b < d.nb && ok; ++b, ++gq) {
+      const Piece& d = tail.piece[x];
+      if (tc::uniform(d.last)) break;
+      const bool two = tc::uniform(d.t0) + 128 < tc::uniform(d.L);
+      const int nb = tc::uniform(d.nb);
+      for (int b = 0; b < nb && ok; ++b, ++gq) {
         const int s = gq % kQSlots;
         any = true;
         if (!(ok = wait(kBQFull + s, gq / kQSlots))) break;
-        const uint64_t qd = tc::desc(sbase + kQRing + s * kBuf, 16, 1024);
+        const uint32_t qd = q_lo + s * (kBuf >> 4);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const int ks = (kp + m) % kNB;
@@ -407,33 +412,30 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
             if (used[m] >= 2 && !(ok = wait(kBSFree + 2 * m + buf, used[m] / 2 - 1))) break;
             ++used[m];
             tc::fence_after();
-            const uint64_t kd = tc::desc(sbase + ks * kKBytes, 16, 2048);
-            if (leader) {
+            const uint32_t kd = k_lo + ks * (kKBytes >> 4);
 #pragma unroll
-              for (int part = 0; part < (kQ8 ? 2 : 1); ++part)
+            for (int part = 0; part < (kQ8 ? 2 : 1); ++part)
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                  tc::mma_ss(tmem + 256 * m + 128 * buf, kd + ((part * kBuf + (kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                             qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), id, part > 0 || kk > 0);
-              tc::commit(bar(kBS + 2 * m + buf));
-            }
-            __syncwarp();
+              for (int kk = 0; kk < 8; ++kk)
+                tc::mma_ss<kHiK, kHiQ>(tm + 256 * m + 128 * buf,
+                                       kd + ((part * kBuf + (kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                                       qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), id, part > 0 || kk > 0, lead);
+            tc::commit(bar(kBS + 2 * m + buf), lead);
           }
-          if (b + 1 == d.nb && leader) tc::commit(bar(kBKEmpty + ks));
-          __syncwarp();
+          if (b + 1 == nb) tc::commit(bar(kBKEmpty + ks), lead);
         }
         if (!ok) break;
-        if (leader) tc::commit(bar(kBQEmpty + s));
-        __syncwarp();
+        tc::commit(bar(kBQEmpty + s), lead);
       }
       if (!ok) break;
-      if (d.nb > 0) kp += 2;
+      if (nb > 0) kp += 2;
+      __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
       __syncwarp();
     }
     if (any) {  // every product issued completes before the tensor memory is freed
       const int zero = 0;
-      if (leader) tc::commit(bar(kBDrain));
+      tc::commit(bar(kBDrain), lead);
       __syncwarp();
       if (lane == 0) mbar_wait_bounded(bar(kBDrain), 0, &zero);
       __syncwarp();
@@ -483,7 +485,10 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
           float2 acc[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.0f, 0.0f);
-          // the weights of columns 32 q ..: y = c1 s - lse2
+          // the weights of columns 32 q ..: 2^(c1 s - lse2).  The masked form is
+          // code of its own: a test per column group would cut the arithmetic
+          // into pieces too short to hide each other's latency (3500 cycles a
+          // block instead of 1400).
           auto weigh = [&](float (&v)[32], int q) {
             if constexpr (GEN) {
               const int dist0 = past + j - t;
@@ -499,21 +504,24 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
             }
             const float2 mul = make_float2(GEN ? 1.0f : c1, GEN ? 1.0f : c1);
             const float4* lse4 = reinterpret_cast<const float4*>(&tail.lse2[s][32 * q]);
+            float2 y[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 l = lse4[e >> 2];
-              float2 y0 = tc::fma2(make_float2(v[e], v[e + 1]), mul, make_float2(-l.x, -l.y));
-              float2 y1 = tc::fma2(make_float2(v[e + 2], v[e + 3]), mul, make_float2(-l.z, -l.w));
-              if (!fast) {
-                const int c = 32 * q + e;
-                y0.x = c >= from && c < to && l.x < INFINITY ? y0.x : -INFINITY;
-                y0.y = c + 1 >= from && c + 1 < to && l.y < INFINITY ? y0.y : -INFINITY;
-                y1.x = c + 2 >= from && c + 2 < to && l.z < INFINITY ? y1.x : -INFINITY;
-                y1.y = c + 3 >= from && c + 3 < to && l.w < INFINITY ? y1.y : -INFINITY;
-              }
-              acc[(e >> 1) & 3] = tc::add2(acc[(e >> 1) & 3], make_float2(tc::ex2(y0.x), tc::ex2(y0.y)));
-              acc[((e >> 1) + 1) & 3] = tc::add2(acc[((e >> 1) + 1) & 3], make_float2(tc::ex2(y1.x), tc::ex2(y1.y)));
+            for (int e = 0; e < 8; ++e) {
+              const float4 l = lse4[e];
+              y[2 * e] = tc::fma2(make_float2(v[4 * e], v[4 * e + 1]), mul, make_float2(l.x, l.y));
+              y[2 * e + 1] = tc::fma2(make_float2(v[4 * e + 2], v[4 * e + 3]), mul, make_float2(l.z, l.w));
             }
+            if (!fast) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int c = 32 * q + 2 * e;
+                const float2 l = *reinterpret_cast<const float2*>(&tail.lse2[s][c]);
+                y[e].x = c >= from && c < to && l.x > -INFINITY ? y[e].x : -INFINITY;
+                y[e].y = c + 1 >= from && c + 1 < to && l.y > -INFINITY ? y[e].y : -INFINITY;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e & 3] = tc::add2(acc[e & 3], make_float2(tc::ex2(y[e].x), tc::ex2(y[e].y)));
           };
           // one load from tensor memory ahead of the arithmetic
           float v0[32], v1[32];

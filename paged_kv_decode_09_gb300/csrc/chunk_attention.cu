@@ -12,8 +12,7 @@
 // block exceeds it by more than 8 (a factor of 256, which f16 and bf16 hold).
 // P_m overwrites S_m in tensor memory as 16-bit pairs: S_0, S_1, O_0 and O_1
 // take all 512 columns.  The halves alternate on the tensor cores: while one
-// is in its softmax, the other's products run.  P_m is handed over in two
-// parts, so that the first part's products overlap the second's exponentials.
+// is in its softmax, the other's products run.
 // q8_0 keys and values enter as two f16 parts, hi and lo (q8_tiles.cuh), two
 // products each.
 //
@@ -27,7 +26,7 @@
 //   full, empty[s]    K or V block in ring slot s
 //   land[s]           a V block that warp 11 passes on to full[s]
 //   sfull[m]          S_m computed (and every product issued before it)
-//   pready[m][part]   part of P_m written (all of S_m read with the last)
+//   pready[m]         P_m written, S_m read
 //   ofull[m]          O_m of the piece complete
 // Every wait is bounded; a warp that gives up sets the abort flag, which ends
 // the other waits, and its copies and products are awaited before the CTA ends.
@@ -87,8 +86,8 @@ enum : int {
   kBEmpty = kBFull + kSlots,
   kBLand = kBEmpty + kSlots,
   kBS = kBLand + kSlots,
-  kBP = kBS + 2,  // [half][part]
-  kBO = kBP + 4,
+  kBP = kBS + 2,
+  kBO = kBP + 2,
   kBQ = kBO + 2,
   kBQEmpty = kBQ + 2,
   kBDesc = kBQEmpty + 1,
@@ -177,6 +176,16 @@ struct Io {
   // P is scaled by 2^kShift: f16 weights far below the maximum stay normal
   // (the largest, 2^(8 + 7), is still below f16's 65504); bf16 has the range.
   [[maybe_unused]] static constexpr float kShift = DT == PKV_KV_BF16 ? 0.0f : 7.0f;
+  // two packed values times f
+  static __device__ __forceinline__ uint32_t scale(uint32_t w, float f) {
+    if constexpr (kType == PKV_KV_BF16) {
+      const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(f));
+      return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(f));
+      return *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
   static __device__ __forceinline__ uint32_t pack(float x, float y) {
     if constexpr (kType == PKV_KV_BF16) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
@@ -295,7 +304,6 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   };
 
   if (warp >= 8) {
-  if constexpr (!kQ8) tc::fewer_registers<88>();  // 2 x 208 + 88 = 3 x 168, what the launch has
   if (stalled) {
     // test hook: every warp gave up
   } else if (warp == 8) {
@@ -522,30 +530,31 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         }
         return pg;
       };
-      int next = entry(0);
-      for (int b = 0; b < d.nb && ok; ++b) {
-        const int pg = next;
-        if (b + 1 < d.nb) next = entry(b + 1);
+      uint4 code[2][kPages];
+      __half sc[2][kPages];
+      // K (v = 0) or V of a block whose pages are pg: token `row` of each page
+      auto fetch = [&](int v, int b, int pg) {
         const int t0 = (d.kb + b) * N;
-        const bool mend = mended(d, b);
-        uint4 code[2][kPages];
-        __half sc[2][kPages];
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-#pragma unroll
-          for (int e = 0; e < kPages; ++e) {  // token `row` of page e
-            const int pe = __shfl_sync(kFull, pg, e);
-            const int t = t0 + e * kPage + row;
-            code[v][e] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // codes 0
-            sc[v][e] = __float2half_rn(0.0f);
-            if (pe >= 0 && t >= d.t_lo && t < d.t_hi) {
-              const long long at = (static_cast<long long>(pe) * a.pool.n_kv + d.h) * kPage + row;
-              code[v][e] = __ldg(reinterpret_cast<const uint4*>((v ? a.pool.v_data : a.pool.k_data) + at * kD) + col);
-              sc[v][e] = __ldg(reinterpret_cast<const __half*>(v ? a.pool.v_scales : a.pool.k_scales) +
-                               at * (kD / kQBlock) + (col >> 1));
-            }
+        for (int e = 0; e < kPages; ++e) {
+          const int pe = __shfl_sync(kFull, pg, e);
+          const int t = t0 + e * kPage + row;
+          code[v][e] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // codes 0
+          sc[v][e] = __float2half_rn(0.0f);
+          if (pe >= 0 && t >= d.t_lo && t < d.t_hi) {
+            const long long at = (static_cast<long long>(pe) * a.pool.n_kv + d.h) * kPage + row;
+            code[v][e] = __ldg(reinterpret_cast<const uint4*>((v ? a.pool.v_data : a.pool.k_data) + at * kD) + col);
+            sc[v][e] = __ldg(reinterpret_cast<const __half*>(v ? a.pool.v_scales : a.pool.k_scales) +
+                             at * (kD / kQBlock) + (col >> 1));
           }
         }
+      };
+      int pg = entry(0);
+      fetch(0, 0, pg);
+      fetch(1, 0, pg);
+      for (int b = 0; b < d.nb && ok; ++b) {
+        const bool mend = mended(d, b);
+        int next = b + 1 < d.nb ? entry(b + 1) : -2;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int s = (gs + v) % kSlots;
@@ -565,6 +574,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
             *reinterpret_cast<uint4*>(hi + kPart + o0) = l0;
             *reinterpret_cast<uint4*>(hi + kPart + o1) = l1;
           }
+          // the next block's loads, a block ahead of their use
+          if (b + 1 < d.nb) fetch(v, b + 1, next);
           if (v == 1 && mend && odd) *(volatile int*)&tail.bad[x] = 1;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
@@ -579,22 +590,23 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     if (warp == 12) fill_skipped(a);
   } else if (warp == 9) {
     // ----------------------------------------------------------- products ----
-    const bool leader = tc::elect_one();
-    const uint32_t id_s = tc::idesc(128, N, false, false, F::kFormat);
-    const uint32_t id_o = tc::idesc(128, 128, false, true, F::kFormat);
-    // scores S_m of the K block in slot s
+    // converged and uniform throughout: see tcgen05.cuh
+    const uint32_t lead = tc::elect_one();
+    const uint32_t tm = tc::uniform(tmem);
+    constexpr uint32_t id_s = tc::idesc(128, 128, false, false, F::kFormat);
+    constexpr uint32_t id_o = tc::idesc(128, 128, false, true, F::kFormat);
+    constexpr uint32_t kHiQ = tc::desc_hi(1024), kHiKV = tc::desc_hi(2048);
+    const uint32_t q_lo = tc::desc_lo(sbase, 16), k_lo = tc::desc_lo(sbase + kRing, 16),
+                   v_lo = tc::desc_lo(sbase + kRing, 1024);
+    // scores S_m of the K block in slot s (q8_0: 64 columns with the hi parts,
+    // and 64 with the lo parts, which the softmax adds)
     auto issue_s = [&](int m, int s) {
-      const uint64_t qd = tc::desc(sbase + m * kHalf, 16, 1024), kd = tc::desc(sbase + kRing + s * kHalf, 16, 2048);
-      if (leader) {
+      const uint32_t qd = q_lo + m * (kHalf >> 4), kd = k_lo + s * (kHalf >> 4);
 #pragma unroll
-        for (int part = 0; part < (kQ8 ? 2 : 1); ++part)
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc::mma_ss(tmem + kTmemS + 128 * m, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                       kd + ((part * kPart + (kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, part > 0 || kk > 0);
-        tc::commit(bar(kBS + m));
-      }
-      __syncwarp();
+      for (int kk = 0; kk < 8; ++kk)
+        tc::mma_ss<kHiQ, kHiKV>(tm + kTmemS + 128 * m, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                                kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_s, kk > 0, lead);
+      tc::commit(bar(kBS + m), lead);
     };
     // the block whose values product is due
     struct {
@@ -603,79 +615,79 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     } v{0, 0, 0, false, false, false};
     bool due = false;
     uint32_t np[2] = {0, 0};  // blocks of P consumed per half
-    // O_m of the due block, the pages of part 0 and then those of part 1 of P
-    auto issue_o = [&](int m) {
-      const uint64_t vd = tc::desc(sbase + kRing + v.s * kHalf, 1024, 2048);
-#pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        if (!wait(kBP + 2 * m + part, np[m])) return false;
-        tc::fence_after();
-        if (leader) {
-          const int from = max(v.lo, part * (kPages / 2)), to = min(v.lo + v.n, (part + 1) * (kPages / 2));
-          for (int kk = from; kk < to; ++kk) {
-            tc::mma_ts(tmem + kTmemO + 128 * m, tmem + kTmemS + 128 * m + 8 * kk, vd + kk * (4096 >> 4), id_o,
-                       !v.first || kk > v.lo);
-            if constexpr (kQ8)
-              tc::mma_ts(tmem + kTmemO + 128 * m, tmem + kTmemS + 128 * m + 8 * kk, vd + ((kPart + kk * 4096) >> 4),
-                         id_o, 1);
-          }
-          if (part == 1 && v.last) tc::commit(bar(kBO + m));
-        }
-        __syncwarp();
-      }
-      ++np[m];
-      return true;
-    };
     int gs = 0;
     bool ok = true, any = false;
-    auto half0 = [&]() {  // O_0 of the due block
-      if (!due) return true;
-      return wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kSlots) && issue_o(0);
-    };
-    auto half1 = [&]() {
-      if (!due) return true;
-      if (v.two && !issue_o(1)) return false;
-      if (leader) tc::commit(bar(kBEmpty + v.s));
-      __syncwarp();
-      due = false;
+    // O_m of the due block, whose V is in its slot, once P_m is written
+    auto issue_o = [&](int m) {
+      const uint32_t vd = v_lo + v.s * (kHalf >> 4);
+      const uint32_t to = tm + kTmemO + 128 * m, tp = tm + kTmemS + 128 * m;
+      const int fresh = v.first ? 0 : 1;
+      if (!wait(kBP + m, np[m])) return false;
+      ++np[m];
+      tc::fence_after();
+      if (v.n == kPages) {
+#pragma unroll
+        for (int kk = 0; kk < kPages; ++kk) {
+          tc::mma_ts<kHiKV>(to, tp + 8 * kk, vd + kk * (4096 >> 4), id_o, kk > 0 ? 1 : fresh, lead);
+          if constexpr (kQ8) tc::mma_ts<kHiKV>(to, tp + 8 * kk, vd + ((kPart + kk * 4096) >> 4), id_o, 1, lead);
+        }
+      } else {
+#pragma unroll 1
+        for (int kk = v.lo; kk < v.lo + v.n; ++kk) {
+          tc::mma_ts<kHiKV>(to, tp + 8 * kk, vd + kk * (4096 >> 4), id_o, kk > v.lo ? 1 : fresh, lead);
+          if constexpr (kQ8) tc::mma_ts<kHiKV>(to, tp + 8 * kk, vd + ((kPart + kk * 4096) >> 4), id_o, 1, lead);
+        }
+      }
+      if (v.last) tc::commit(bar(kBO + m), lead);
       return true;
     };
     uint32_t q1 = 0;
     for (int p = 0; ok; ++p) {
       const int x = p % kDescs;
       if (!wait(kBDesc + x, p / kDescs)) { ok = false; break; }
-      const Piece d = tail.piece[x];
-      if (d.last) break;
-      const bool two = d.nq * G > kTileRows / 2;
+      const Piece& d = tail.piece[x];
+      if (tc::uniform(d.last)) break;
+      const int nb = tc::uniform(d.nb), t_lo = tc::uniform(d.t_lo), t_hi = tc::uniform(d.t_hi),
+                kb = tc::uniform(d.kb);
+      const bool two = tc::uniform(d.nq) * G > kTileRows / 2;
       any = true;
-      for (int b = 0; b < d.nb && ok; ++b) {
-        // gs: the slot of this block's K; gs - 1 that of the due block's V
+      for (int b = 0; b < nb && ok; ++b) {
+        // gs: the slot of this block's K; gs - 1 that of the due block's V.
+        // What lands early is waited for first: once P_m is there, its
+        // product and the next scores go out without another wait (a wait
+        // costs some 200 cycles even when there is nothing to wait for).
         const int s = gs % kSlots;
-        ok = half0();
-        if (!ok) break;
-        if (b == 0 && !(ok = wait(kBQ, p))) break;
+        if (due && !(ok = wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kSlots))) break;
+        if (b == 0) {
+          // the piece before is finished while this one's queries land
+          if (due) {
+            if (!(ok = issue_o(0) && (!v.two || issue_o(1)))) break;
+            tc::commit(bar(kBEmpty + v.s), lead);
+            due = false;
+          }
+          if (!(ok = wait(kBQ, p) && (!two || wait(kBQ + 1, q1)))) break;
+        }
         if (!(ok = wait(kBFull + s, gs / kSlots))) break;
-        tc::fence_after();
-        issue_s(0, s);
-        ok = half1();
-        if (!ok) break;
-        if (two) {
-          if (b == 0 && !(ok = wait(kBQ + 1, q1))) break;
+        if (due) {
+          if (!(ok = issue_o(0))) break;
+        } else {
           tc::fence_after();
-          issue_s(1, s);
         }
-        if (leader) {
-          tc::commit(bar(kBEmpty + s));
-          if (b + 1 == d.nb) tc::commit(bar(kBQEmpty));
+        issue_s(0, s);
+        if (due) {
+          if (v.two && !(ok = issue_o(1))) break;
+          tc::commit(bar(kBEmpty + v.s), lead);
         }
-        __syncwarp();
-        int lo, hi;
-        pages_of(d, b, lo, hi);
+        if (two) issue_s(1, s);
+        tc::commit(bar(kBEmpty + s), lead);
+        if (b + 1 == nb) tc::commit(bar(kBQEmpty), lead);
+        const int first = (kb + b) * kPages;
+        const int lo = max(first, t_lo / kPage), hi = min(first + kPages, (t_hi + kPage - 1) / kPage);
         v.s = (gs + 1) % kSlots;
         v.lo = lo & (kPages - 1);
         v.n = hi - lo;
         v.first = b == 0;
-        v.last = b + 1 == d.nb;
+        v.last = b + 1 == nb;
         v.two = two;
         due = true;
         gs += 2;
@@ -685,11 +697,11 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
       __syncwarp();
     }
-    if (ok) ok = half0() && half1();
+    if (ok && due && wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kSlots) && issue_o(0) && v.two) issue_o(1);
     // every product issued completes before the tensor memory is freed
     if (any) {
       const int zero = 0;
-      if (leader) tc::commit(bar(kBDrain));
+      tc::commit(bar(kBDrain), lead);
       __syncwarp();
       if (lane == 0) mbar_wait_bounded(bar(kBDrain), 0, &zero);
       __syncwarp();
@@ -702,7 +714,6 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t tS = tmem + lanes + kTmemS + 128 * m, tO = tmem + lanes + kTmemO + 128 * m;
     const int jq = r / G;
-    if constexpr (!kQ8) tc::more_registers<208>();
     uint32_t blocks = 0, pieces = 0;
     bool ok = !stalled;
     const float c1 = a.sc.scale * kLog2e;
@@ -723,118 +734,135 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         if constexpr (GEN) slope2 = a.sc.slopes ? __ldg(a.sc.slopes + g) * kLog2e : 0.0f;
         float mx = -INFINITY;  // the maximum in force, base 2
         float sub = 0.0f;      // what is taken off the scores: mx - shift (0 before a first score)
-        float2 l2[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) l2[e] = make_float2(0.0f, 0.0f);
+        float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         for (int b = 0; b < d.nb; ++b, ++blocks) {
           const int t0 = (d.kb + b) * N;
           const bool fast = __all_sync(kFull, t0 >= lo && t0 + N <= hi);
           if (!(ok = wait(kBS + m, blocks))) break;
           tc::fence_after();
           if (any) {
-            float s[N];
-            constexpr int kH = N / 2;  // columns of a part
-            // the scores of part `part`, and their maximum
-            auto form = [&](int part) {
-              if constexpr (GEN) {
-                const float dist0 = static_cast<float>(P - t0);
-#pragma unroll
-                for (int e = part * kH; e < (part + 1) * kH; ++e) {
-                  float y;
-                  if (a.sc.softcap > 0.0f) {
-                    // tanh z = 1 - 2 / (1 + e^2z)
-                    y = cap2 - __fdividef(2.0f * cap2, 1.0f + tc::ex2(s[e] * (2.0f * kLog2e * inv_cap)));
-                  } else {
-                    y = s[e] * c1;
-                  }
-                  s[e] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(e)), y);
-                }
-              }
-              if (!fast) {
-                const int from = lo - t0, to = hi - t0;
-#pragma unroll
-                for (int e = part * kH; e < (part + 1) * kH; ++e) s[e] = e >= from && e < to ? s[e] : -INFINITY;
-              }
-              float x0 = s[part * kH], x1 = s[part * kH + 1], x2 = s[part * kH + 2], x3 = s[part * kH + 3];
-#pragma unroll
-              for (int e = part * kH + 4; e + 8 <= (part + 1) * kH; e += 8) {
-                x0 = tc::max3(x0, s[e], s[e + 1]);
-                x1 = tc::max3(x1, s[e + 2], s[e + 3]);
-                x2 = tc::max3(x2, s[e + 4], s[e + 5]);
-                x3 = tc::max3(x3, s[e + 6], s[e + 7]);
-              }
-              const int e = (part + 1) * kH - 4;
-              return tc::max3(tc::max3(x0, s[e], s[e + 1]), tc::max3(x1, s[e + 2], s[e + 3]), fmaxf(x2, x3));
-            };
-#pragma unroll
-            for (int e = 0; e < kH / 32; ++e) tc::ld32(tS + 32 * e, s + 32 * e);
-            tc::wait_ld();
-#pragma unroll
-            for (int e = kH / 32; e < N / 32; ++e) tc::ld32(tS + 32 * e, s + 32 * e);
-            float bm = form(0);
-            tc::wait_ld();
-            bm = fmaxf(bm, form(1));
-            if constexpr (!GEN) bm *= c1;
-            const bool raise = bm > mx + 8.0f;  // also from -inf
-            if (__any_sync(kFull, raise)) {
+            // The block goes by in groups of 32 columns, one load from tensor
+            // memory ahead of the arithmetic, in a loop of two groups: its code
+            // has to stay in the instruction caches that six other loops
+            // share.  A group's exponentials start under the maximum in force,
+            // and the group's own maximum is found beside them; should it
+            // exceed the one in force by more than 8 (rare after a tile's
+            // first block) the maximum is raised and they are taken again.
+            // Raises are by whole powers of two, so that the weights already
+            // written for the block are rescaled without another rounding.
+            // Looking for the maximum first put 450 cycles in front of the
+            // exponentials.
+            constexpr int kGroups = N / 32;
+            auto raise_to = [&](float bm, int group) {
+              const bool raise = bm > mx + 8.0f;  // also from -inf
               float al = 1.0f;
               if (raise) {
-                al = tc::ex2(mx - bm);
-                mx = bm;
-                sub = bm - F::kShift;
+                const float to = mx == -INFINITY ? bm : mx + ceilf(bm - mx);
+                al = tc::ex2(mx - to);  // a power of two, or 0
+                mx = to;
+                sub = to - F::kShift;
+                l2[0].x *= al; l2[0].y *= al; l2[1].x *= al; l2[1].y *= al;
+              }
+#pragma unroll 1
+              for (int e = 0; e < group; ++e) {  // the block's weights so far
+                uint32_t w[16];
+                tc::ld16w(tS + 16 * e, w);
+                tc::wait_ld();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  l2[e].x *= al;
-                  l2[e].y *= al;
-                }
+                for (int u = 0; u < 16; ++u) w[u] = F::scale(w[u], al);
+                tc::st16(tS + 16 * e, w);
               }
               if (b > 0) {
                 // the values products so far are complete: S was issued after them
 #pragma unroll 1
-                for (int e = 0; e < 4; ++e) {
-                  float o[32];
-                  tc::ld32(tO + 32 * e, o);
+                for (int e = 0; e < 8; ++e) {
+                  float o[16];
+                  tc::ld16w(tO + 16 * e, reinterpret_cast<uint32_t(&)[16]>(o));
                   tc::wait_ld();
 #pragma unroll
-                  for (int u = 0; u < 32; ++u) o[u] *= al;
-                  tc::st32(tO + 32 * e, o);
+                  for (int u = 0; u < 16; ++u) o[u] *= al;
+                  tc::st16(tO + 16 * e, reinterpret_cast<uint32_t(&)[16]>(o));
                 }
               }
-            }
-            const float2 mul = make_float2(GEN ? 1.0f : c1, GEN ? 1.0f : c1), off = make_float2(-sub, -sub);
+            };
+            const float2 mul = make_float2(GEN ? 1.0f : c1, GEN ? 1.0f : c1);
+            auto weigh = [&](float (&v)[32], int group) {
+              if constexpr (GEN) {
+                const float dist0 = static_cast<float>(P - t0 - 32 * group);
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
+                for (int e = 0; e < 32; ++e) {
+                  float y;
+                  if (a.sc.softcap > 0.0f) {
+                    // tanh z = 1 - 2 / (1 + e^2z)
+                    y = cap2 - __fdividef(2.0f * cap2, 1.0f + tc::ex2(v[e] * (2.0f * kLog2e * inv_cap)));
+                  } else {
+                    y = v[e] * c1;
+                  }
+                  v[e] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(e)), y);
+                }
+              }
+              if (!fast) {
+                const int from = lo - t0 - 32 * group, to = hi - t0 - 32 * group;
 #pragma unroll
-              for (int e = part * (kH / 32); e < (part + 1) * (kH / 32); ++e) {
-                uint32_t w[16];
+                for (int e = 0; e < 32; ++e) v[e] = e >= from && e < to ? v[e] : -INFINITY;
+              }
+              uint32_t w[16];
+              float2 lb[2];
+#pragma unroll 1
+              while (true) {
+                const float2 off = make_float2(-sub, -sub);
+                float x0 = -INFINITY, x1 = -INFINITY;
+                lb[0] = lb[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int u = 0; u < 16; ++u) {
-                  const float2 y = tc::fma2(make_float2(s[32 * e + 2 * u], s[32 * e + 2 * u + 1]), mul, off);
+                  const float2 y = tc::fma2(make_float2(v[2 * u], v[2 * u + 1]), mul, off);
+                  if (u & 1) x1 = tc::max3(x1, v[2 * u], v[2 * u + 1]); else x0 = tc::max3(x0, v[2 * u], v[2 * u + 1]);
                   const float2 pr = make_float2(tc::ex2(y.x), tc::ex2(y.y));
-                  l2[u & 3] = tc::add2(l2[u & 3], pr);
+                  lb[u & 1] = tc::add2(lb[u & 1], pr);
                   w[u] = F::pack(pr.x, pr.y);
                 }
-                tc::st16(tS + 16 * e, w);
+                const float bm = fmaxf(x0, x1) * (GEN ? 1.0f : c1);
+                if (!__any_sync(kFull, bm > mx + 8.0f)) break;
+                raise_to(bm, group);
               }
-              tc::wait_st();
-              tc::fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(kBP + 2 * m + part));
+              l2[0] = tc::add2(l2[0], lb[0]);
+              l2[1] = tc::add2(l2[1], lb[1]);
+              tc::st16(tS + 16 * group, w);
+            };
+            float v0[32], v1[32];
+            float more[kQ8 ? 32 : 1];  // q8_0: the lo parts' scores
+            auto load = [&](float (&v)[32], int group) {
+              tc::ld32(tS + 32 * group, v);
+              if constexpr (kQ8) tc::ld32(tS + 64 + 32 * group, more);
+            };
+            auto arrived = [&](float (&v)[32]) {
+              tc::wait_ld();
+              if constexpr (kQ8) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] += more[e];
+              }
+            };
+            load(v0, 0);
+#pragma unroll 1
+            for (int group = 0; group < kGroups; group += 2) {
+              arrived(v0);
+              load(v1, group + 1);
+              weigh(v0, group);
+              arrived(v1);
+              if (group + 2 < kGroups) load(v0, group + 2);
+              weigh(v1, group + 1);
             }
-          } else {
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(bar(kBP + 2 * m));
-              mbar_arrive(bar(kBP + 2 * m + 1));
-            }
+            tc::wait_st();
           }
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBP + m));
         }
         if (!ok || !(ok = wait(kBO + m, pieces))) break;
         ++pieces;
         tc::fence_after();
         if (any) {
-          const float2 la = tc::add2(tc::add2(l2[0], l2[1]), tc::add2(l2[2], l2[3]));
+          const float2 la = tc::add2(l2[0], l2[1]);
           const float l = la.x + la.y;
           const float inv = d.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
           const long long row = static_cast<long long>(d.tok + jq) * a.n_q + g;

@@ -15,10 +15,12 @@ namespace tc {
 // and two byte offsets in units of 16 bytes.  K-major operands (rows of 64
 // elements, 8 rows per 1024-byte atom): sbo = bytes between 8-row groups, lbo
 // unused.  MN-major operands: lbo = bytes between the 64-element parts of the
-// M or N extent, sbo = bytes between groups of 8 rows along K.
-__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+// M or N extent, sbo = bytes between groups of 8 rows along K.  The high word
+// does not depend on the address, and an offset of x bytes adds x / 16 to the
+// low word (addresses stay below 2^18), so products take the words apart.
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
 }
 // Instruction descriptor of kind::f16, fp32 accumulation; A and B both f16
 // (format 0) or both bf16 (format 1).
@@ -26,26 +28,47 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn_major, bool
   return (1u << 4) | (format << 7) | (format << 10) | (a_mn_major ? (1u << 15) : 0u) | (b_mn_major ? (1u << 16) : 0u) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// D (tensor memory) = A B (+ D): A and B in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int accumulate) {
+// Products and their commits are instructions of one thread, but they take
+// their operands from the warp's uniform registers.  The whole warp runs the
+// code around them, converged and on values that are the same in every lane
+// (uniform() below), and `lead`, non-zero in one lane, guards the instruction
+// itself: in a branch of one lane every operand of every product is first
+// moved to a uniform register, which made a product cost 63 cycles to issue
+// (one of 128 x 128 x 16 computes for 64).
+
+// x, known to the compiler to be the same in every lane.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(kFull, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(kFull, x, 0); }
+
+// D (tensor memory) = A B (+ D): A and B in shared memory, their descriptors'
+// low words and (constant) high words.
+template <uint32_t A_HI, uint32_t B_HI>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, int accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %7};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(accumulate), "r"(lead), "n"(A_HI), "n"(B_HI)
       : "memory");
 }
 // The same with A in tensor memory: lane = row of A, a 32-bit column two
 // consecutive elements along K.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, int accumulate) {
+template <uint32_t B_HI>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, int accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 y, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(accumulate), "r"(lead), "n"(B_HI)
       : "memory");
 }
-// Arrive on `bar` once every product this thread has issued is complete.
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// Arrive on `bar` once every product the leading thread has issued is complete.
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -88,6 +111,14 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
       : "memory");
 }
 
+__device__ __forceinline__ void ld16w(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 // 2^x by the hardware approximation (about 22 correct bits; 2^-inf = 0,
 // results below 2^-126 flushed to 0).
 __device__ __forceinline__ float ex2(float x) {
@@ -101,16 +132,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// Registers a thread of the (whole, converged) warpgroup may use from here on.
-template <int N>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Two fp32 values a b + c, one instruction.
@@ -134,11 +155,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
-// True in one lane of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
+// Non-zero in one lane of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t pred;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
-  return pred != 0;
+  return pred;
 }
 
 // Tensor copies global -> shared, completing on `bar`: the 5-D box at {0, 0,
@@ -170,26 +191,32 @@ __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// A wait by every lane of a warp (each hand-over is on the critical path:
-// polled without suspending), its outcome the same for all.  False once *abort
-// is set or after kWaitLimitNs; it then has set *abort and recorded
-// PKV_DEV_TIMEOUT.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
-  int ok = test_wait(bar, parity) ? 1 : 0;
-  if (!ok) {
-    const unsigned long long t0 = global_ns();
-    while (!ok) {
+// The long end of a wait: false once *abort is set or after kWaitLimitNs.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  const unsigned long long t0 = global_ns();
+  while (true) {
 #pragma unroll 1
-      for (int i = 0; i < 64 && !ok; ++i) ok = test_wait(bar, parity) ? 1 : 0;
-      if (!ok && (*abort || global_ns() - t0 > kWaitLimitNs)) break;
-    }
+    for (int i = 0; i < 64; ++i)
+      if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(kFull, *abort != 0 || global_ns() - t0 > kWaitLimitNs)) break;
   }
-  if (__all_sync(kFull, ok)) return true;
   if ((threadIdx.x & 31) == 0 && !*abort) {
     *abort = 1;
     record_status(status, PKV_DEV_TIMEOUT);
   }
   return false;
+}
+
+// A wait by every lane of a warp, its outcome the same for all.  False once
+// *abort is set or after kWaitLimitNs; it then has set *abort and recorded
+// PKV_DEV_TIMEOUT.  A wait that has nothing to wait for is on many critical
+// paths: a poll, a vote and a branch (some 35 cycles; a loop that lets lanes
+// leave one by one took 157), and the clock is left to wait_on.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+#pragma unroll 1
+  for (int i = 0; i < 512; ++i)
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+  return wait_on(bar, parity, abort, status);
 }
 
 }  // namespace tc
