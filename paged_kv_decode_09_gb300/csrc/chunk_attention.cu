@@ -19,11 +19,12 @@
 // Warps: 0-3 and 4-7 the softmax of half 0 and 1, 8 walks the work and copies
 // Q, 9 issues the products, 10 copies K and V pages (one tensor copy each)
 // into a ring of five 32 KiB slots, 11 mends V blocks that hold tokens no
-// query of the tile attends to; with q8_0, 12-15 fill the ring instead of 10
-// and 11.  Hand-overs by shared-memory barriers:
+// query of the tile attends to; with q8_0, 10 copies codes and scales into a
+// ring of their own, and 12-15 split them into the ring of slots.  Hand-overs by shared-memory barriers:
 //   dfull, dempty[x]  descriptor x of a piece (a tile's blocks in this range)
 //   qfull[m], qempty  Q_m landed; the piece's last scores are computed
 //   full, empty[s]    K or V block in ring slot s
+//   raw, rawempty[s]  codes and scales of a K or V block (q8_0)
 //   land[s]           a V block that warp 11 passes on to full[s]
 //   sfull[m]          S_m computed (and every product issued before it)
 //   pready[m]         P_m written, S_m read
@@ -62,7 +63,7 @@ constexpr int kBlockTok = DT == PKV_KV_Q8_0 ? 64 : 128;  // cached tokens of a b
 template <int DT>
 constexpr int kAttnThreads = DT == PKV_KV_Q8_0 ? 512 : kPlanThreads;
 #ifndef PKV_CHUNK_TILE_COST
-#define PKV_CHUNK_TILE_COST 2
+#define PKV_CHUNK_TILE_COST 3
 #endif
 #ifndef PKV_CHUNK_SNAP
 #define PKV_CHUNK_SNAP 2
@@ -73,19 +74,30 @@ template <int DT>
 constexpr int kTileCost = PKV_CHUNK_TILE_COST * (128 / kBlockTok<DT>);
 template <int DT>
 constexpr int kSplitSnap = PKV_CHUNK_SNAP * (128 / kBlockTok<DT>);
-constexpr int kSlots = 5;
+template <int DT>
+constexpr int kSlots = DT == PKV_KV_Q8_0 ? 4 : 5;    // ring slots
+constexpr int kMaxSlots = 5;
 constexpr uint32_t kHalf = 32768;                    // bytes of Q_m, and of a ring slot
 constexpr uint32_t kRing = 2 * kHalf;                // the ring, behind Q
-constexpr uint32_t kTail = kRing + kSlots * kHalf;   // barriers and descriptors
+// q8_0: a ring of K or V codes of a block as they are stored, and their scales
+constexpr int kRaws = 3;
+constexpr uint32_t kRawBytes = 64 * kD;
+constexpr uint32_t kRaw = kRing + kSlots<PKV_KV_Q8_0> * kHalf;
+constexpr uint32_t kRawScales = kRaw + kRaws * kRawBytes;
+constexpr uint32_t kRawScaleBytes = 64 * (kD / kQBlock) * 2;
+constexpr uint32_t kTail = kRing + kMaxSlots * kHalf;   // barriers and descriptors
+static_assert(kRawScales + kRaws * kRawScaleBytes <= kTail, "");
 constexpr int kDescs = 4;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;         // S_m at 128 m, O_m at 256 + 128 m
 
 // barriers
 enum : int {
   kBFull = 0,
-  kBEmpty = kBFull + kSlots,
-  kBLand = kBEmpty + kSlots,
-  kBS = kBLand + kSlots,
+  kBEmpty = kBFull + kMaxSlots,
+  kBLand = kBEmpty + kMaxSlots,
+  kBRaw = kBLand + kMaxSlots,
+  kBRawEmpty = kBRaw + kRaws,
+  kBS = kBRawEmpty + kRaws,
   kBP = kBS + 2,
   kBO = kBP + 2,
   kBQ = kBO + 2,
@@ -97,7 +109,7 @@ enum : int {
   kNumBars,
 };
 template <int DT>
-constexpr int kDescReaders = DT == PKV_KV_Q8_0 ? 13 : 11;  // softmax, products, copies and mending (4 warps)
+constexpr int kDescReaders = DT == PKV_KV_Q8_0 ? 14 : 11;  // softmax, products, copies, and mending or splitting
 
 // A piece: blocks kb .. kb + nb - 1 of one tile for KV head h.
 struct Piece {
@@ -221,6 +233,36 @@ __device__ __noinline__ void redo_row(const ChunkAttnArgs& a, const Piece& p, in
   }
 }
 
+// The rare end of a raised maximum, kept out of the softmax's loop: the rows'
+// weights of the block so far (`groups` of 32 columns in P) and, with `o`, their
+// O, times al.
+template <int DT>
+__device__ __forceinline__ void rescale_here(uint32_t tP, uint32_t tO, int groups, bool o, float al) {
+#pragma unroll 1
+  for (int e = 0; e < groups; ++e) {
+    uint32_t w[16];
+    tc::ld16w(tP + 16 * e, w);
+    tc::wait_ld();
+#pragma unroll
+    for (int u = 0; u < 16; ++u) w[u] = Io<DT>::scale(w[u], al);
+    tc::st16(tP + 16 * e, w);
+  }
+#pragma unroll 1
+  for (int e = 0; o && e < 8; ++e) {
+    uint32_t w[16];
+    tc::ld16w(tO + 16 * e, w);
+    tc::wait_ld();
+#pragma unroll
+    for (int u = 0; u < 16; ++u) w[u] = __float_as_uint(__uint_as_float(w[u]) * al);
+    tc::st16(tO + 16 * e, w);
+  }
+  tc::wait_st();
+}
+template <int DT>
+__device__ __noinline__ void rescale(uint32_t tP, uint32_t tO, int groups, bool o, float al) {
+  rescale_here<DT>(tP, tO, groups, o, al);
+}
+
 // Zeros and an lse of -inf for the queries of rows that are skipped (one warp).
 __device__ __forceinline__ void fill_skipped(const ChunkAttnArgs& a) {
   const int lane = threadIdx.x & 31;
@@ -242,6 +284,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                            const __grid_constant__ CUtensorMap qmap) {
   using F = Io<DT>;
   constexpr bool kQ8 = DT == PKV_KV_Q8_0;
+  constexpr int kS = kSlots<DT>;
   constexpr int N = kBlockTok<DT>;                   // tokens of a block
   constexpr int kPages = N / kPage;                  // its pages
   constexpr uint32_t kPart = N * kD * 2;             // bytes of one part of it
@@ -262,7 +305,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     tail.ctl[0] = 0;
     for (int b = 0; b < kNumBars; ++b) {
       int count = 1;
-      if (b < kBEmpty && kQ8) count = 4;
+      if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = 4;
       if (b >= kBP && b < kBO) count = 4;
       if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT>;
       mbar_init(bar(b), count);
@@ -290,7 +333,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   // test hook: every warp gives up here, before any copy
   const bool stalled = test_stall(bar(kBStall), a.pool.test_stall_ns, ctl, a.pool.status);
 
-  auto wait = [&](int b, uint32_t parity) { return tc::warp_wait(bar(b), parity & 1u, ctl, a.pool.status); };
+  auto wait = [&](int b, uint32_t parity) { return tc::warp_wait<!kQ8>(bar(b), parity & 1u, ctl, a.pool.status); };
   auto pages_of = [&](const Piece& p, int b, int& lo, int& hi) {  // pages of a block that are read
     const int first = (p.kb + b) * kPages;
     lo = max(first, p.t_lo / kPage);
@@ -303,7 +346,69 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     return t0 < p.full_lo || t0 + N > p.full_hi;
   };
 
-  if (warp >= 8) {
+  if (kQ8 && warp >= 12) {
+    // 3 x 144 + 80 = 4 x 128 registers a thread, what the launch has
+    if constexpr (kQ8) tc::more_registers<144>();
+    // ------------------------------ q8_0 keys and values as two f16 parts ----
+    const int row = (tid - 384) >> 3, col = (tid - 384) & 7;  // 8 threads a token, 16 codes each
+    int gs = 0;
+    bool ok = !stalled;
+    for (int p = 0; ok; ++p) {
+      const int x = p % kDescs;
+      if (!wait(kBDesc + x, p / kDescs)) break;
+      const Piece d = tail.piece[x];
+      if (d.last) break;
+      for (int b = 0; b < d.nb && ok; ++b) {
+        const bool mend = mended(d, b);
+        const int t0 = (d.kb + b) * N;
+#pragma unroll
+        for (int v = 0; v < 2; ++v, ++gs) {
+          const int rs = gs % kRaws, s = gs % kS;
+          if (!(ok = wait(kBRaw + rs, gs / kRaws))) break;
+          const uint8_t* raw = smem + kRaw + rs * kRawBytes + row * kD + ((col ^ (row & 7)) << 4);
+          const __half* rsc = reinterpret_cast<const __half*>(smem + kRawScales + rs * kRawScaleBytes) +
+                              row * (kD / kQBlock) + (col >> 1);
+          uint4 code[kPages];
+          __half2 sc[kPages];
+          bool odd = false;
+#pragma unroll
+          for (int e = 0; e < kPages; ++e) {  // token `row` of page e; 0 where no query of the tile attends
+            const int t = t0 + e * kPage + row;
+            const bool in = t >= d.t_lo && t < d.t_hi;
+            code[e] = *reinterpret_cast<const uint4*>(raw + e * (kPage * kD));
+            const __half f = in ? rsc[e * kPage * (kD / kQBlock)] : __float2half_rn(0.0f);
+            odd = odd || !(fabsf(__half2float(f)) <= 65504.0f);
+            sc[e] = __half2half2(f);
+          }
+          if (gs >= kS && !(ok = wait(kBEmpty + s, gs / kS - 1))) break;
+          uint8_t* hi = smem + kRing + s * kHalf;
+#pragma unroll
+          for (int e = 0; e < kPages; ++e) {
+            uint4 h0, l0, h1, l1;
+            q8_split8(make_uint2(code[e].x, code[e].y), sc[e], h0, l0);
+            q8_split8(make_uint2(code[e].z, code[e].w), sc[e], h1, l1);
+            const uint32_t o0 = tile_vec(kPage * e + row, 2 * col), o1 = tile_vec(kPage * e + row, 2 * col + 1);
+            *reinterpret_cast<uint4*>(hi + o0) = h0;
+            *reinterpret_cast<uint4*>(hi + o1) = h1;
+            *reinterpret_cast<uint4*>(hi + kPart + o0) = l0;
+            *reinterpret_cast<uint4*>(hi + kPart + o1) = l1;
+          }
+          if (v == 1 && mend && odd) *(volatile int*)&tail.bad[x] = 1;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(kBFull + s));
+            mbar_arrive(bar(kBRawEmpty + rs));
+          }
+        }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
+    }
+    if (warp == 12) fill_skipped(a);
+  } else if (warp >= 8) {
+  if constexpr (kQ8) tc::fewer_registers<80>();
   if (stalled) {
     // test hook: every warp gave up
   } else if (warp == 8) {
@@ -407,13 +512,13 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         const bool mend = mended(d, b);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          const int s = (gs + v) % kSlots;
-          if (gs + v >= kSlots && !wait(kBEmpty + s, (gs + v) / kSlots - 1)) {
+          const int s = (gs + v) % kS;
+          if (gs + v >= kS && !wait(kBEmpty + s, (gs + v) / kS - 1)) {
             ok = false;
             break;
           }
           const int to = v == 1 && mend ? kBLand + s : kBFull + s;
-          const uint32_t par = v == 1 && mend ? (landed >> s) & 1u : static_cast<uint32_t>((gs + v) / kSlots) & 1u;
+          const uint32_t par = v == 1 && mend ? (landed >> s) & 1u : static_cast<uint32_t>((gs + v) / kS) & 1u;
           if (v == 1 && mend) landed ^= 1u << s;
           if (lane == s) {
             my_bar = bar(to);
@@ -435,6 +540,62 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     const int zero = 0;
     if (my_bar) mbar_wait_bounded(my_bar, my_par, &zero);
     __syncwarp();
+  } else if (kQ8 && warp == 10) {
+    // ----------------------------------------- q8_0 codes and scales, raw ----
+    int gs = 0;
+    uint32_t my_bar = 0, my_par = 0;  // lane s: the last copy's barrier of stage s
+    bool ok = true;
+    for (int p = 0; ok; ++p) {
+      const int x = p % kDescs;
+      if (!wait(kBDesc + x, p / kDescs)) break;
+      const Piece d = tail.piece[x];
+      if (d.last) break;
+      const int32_t* bt = a.rows.block_table + static_cast<long long>(d.i) * a.rows.bt_stride;
+      auto entry = [&](int b) {  // lane e: page e of the block, -1 where it is not read
+        int lo, hi;
+        pages_of(d, b, lo, hi);
+        const int q = (d.kb + b) * kPages + lane;
+        return lane < kPages && q >= lo && q < hi ? __ldg(bt + q) : -1;
+      };
+      int next = entry(0);
+      for (int b = 0; b < d.nb && ok; ++b) {
+        int pg = next;
+        if (b + 1 < d.nb) next = entry(b + 1);
+        int lo, hi;
+        pages_of(d, b, lo, hi);
+        const int q = (d.kb + b) * kPages + lane;
+        const bool mine = lane < kPages && q >= lo && q < hi;
+        if (mine && (pg < 0 || pg >= a.pool.num_pages)) {
+          record_status(a.pool.status, PKV_DEV_BAD_PAGE);
+          pg = 0;
+        }
+#pragma unroll
+        for (int v = 0; v < 2; ++v, ++gs) {
+          const int rs = gs % kRaws;
+          if (gs >= kRaws && !(ok = wait(kBRawEmpty + rs, gs / kRaws - 1))) break;
+          if (lane == rs) {
+            my_bar = bar(kBRaw + rs);
+            my_par = static_cast<uint32_t>(gs / kRaws) & 1u;
+          }
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar(kBRaw + rs), static_cast<uint32_t>(hi - lo) * (kPage * kD + kPage * 8));
+          __syncwarp();
+          if (mine) {
+            const long long tile = static_cast<long long>(pg) * a.pool.n_kv + d.h;
+            tc::load_page(sbase + kRaw + rs * kRawBytes + lane * (kPage * kD), v ? &maps.vp : &maps.kp,
+                          static_cast<int>(tile), bar(kBRaw + rs));
+            tc::load_bytes(sbase + kRawScales + rs * kRawScaleBytes + lane * (kPage * 8),
+                           (v ? a.pool.v_scales : a.pool.k_scales) + tile * (kPage * 8), kPage * 8, bar(kBRaw + rs));
+          }
+        }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
+    }
+    const int zero = 0;
+    if (my_bar) mbar_wait_bounded(my_bar, my_par, &zero);
+    __syncwarp();
   } else if (!kQ8 && warp == 11) {
     // ------------------------------------------------------------ mending ----
     int gs = 0;
@@ -447,7 +608,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       if (d.last) break;
       for (int b = 0; b < d.nb; ++b, gs += 2) {
         if (!mended(d, b)) continue;
-        const int s = (gs + 1) % kSlots;
+        const int s = (gs + 1) % kS;
         if (!wait(kBLand + s, (landed >> s) & 1u)) {
           ok = false;
           break;
@@ -508,86 +669,6 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
     }
     fill_skipped(a);
-  } else if (kQ8 && warp >= 12) {
-    // ------------------------------ q8_0 keys and values as two f16 parts ----
-    const int row = (tid - 384) >> 3, col = (tid - 384) & 7;  // 8 threads a token, 16 codes each
-    int gs = 0;
-    bool ok = true;
-    for (int p = 0; ok; ++p) {
-      const int x = p % kDescs;
-      if (!wait(kBDesc + x, p / kDescs)) break;
-      const Piece d = tail.piece[x];
-      if (d.last) break;
-      const int32_t* bt = a.rows.block_table + static_cast<long long>(d.i) * a.rows.bt_stride;
-      auto entry = [&](int b) {  // lane e: page e of the block, -1 where it is not read
-        int lo, hi;
-        pages_of(d, b, lo, hi);
-        const int q = (d.kb + b) * kPages + lane;
-        int pg = lane < kPages && q >= lo && q < hi ? __ldg(bt + q) : -2;
-        if (pg != -2 && (pg < 0 || pg >= a.pool.num_pages)) {
-          record_status(a.pool.status, PKV_DEV_BAD_PAGE);
-          pg = 0;
-        }
-        return pg;
-      };
-      uint4 code[2][kPages];
-      __half sc[2][kPages];
-      // K (v = 0) or V of a block whose pages are pg: token `row` of each page
-      auto fetch = [&](int v, int b, int pg) {
-        const int t0 = (d.kb + b) * N;
-#pragma unroll
-        for (int e = 0; e < kPages; ++e) {
-          const int pe = __shfl_sync(kFull, pg, e);
-          const int t = t0 + e * kPage + row;
-          code[v][e] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // codes 0
-          sc[v][e] = __float2half_rn(0.0f);
-          if (pe >= 0 && t >= d.t_lo && t < d.t_hi) {
-            const long long at = (static_cast<long long>(pe) * a.pool.n_kv + d.h) * kPage + row;
-            code[v][e] = __ldg(reinterpret_cast<const uint4*>((v ? a.pool.v_data : a.pool.k_data) + at * kD) + col);
-            sc[v][e] = __ldg(reinterpret_cast<const __half*>(v ? a.pool.v_scales : a.pool.k_scales) +
-                             at * (kD / kQBlock) + (col >> 1));
-          }
-        }
-      };
-      int pg = entry(0);
-      fetch(0, 0, pg);
-      fetch(1, 0, pg);
-      for (int b = 0; b < d.nb && ok; ++b) {
-        const bool mend = mended(d, b);
-        int next = b + 1 < d.nb ? entry(b + 1) : -2;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int s = (gs + v) % kSlots;
-          if (gs + v >= kSlots && !(ok = wait(kBEmpty + s, (gs + v) / kSlots - 1))) break;
-          uint8_t* hi = smem + kRing + s * kHalf;
-          bool odd = false;
-#pragma unroll
-          for (int e = 0; e < kPages; ++e) {
-            odd = odd || !(fabsf(__half2float(sc[v][e])) <= 65504.0f);
-            const __half2 s2 = __half2half2(sc[v][e]);
-            uint4 h0, l0, h1, l1;
-            q8_split8(make_uint2(code[v][e].x, code[v][e].y), s2, h0, l0);
-            q8_split8(make_uint2(code[v][e].z, code[v][e].w), s2, h1, l1);
-            const uint32_t o0 = tile_vec(kPage * e + row, 2 * col), o1 = tile_vec(kPage * e + row, 2 * col + 1);
-            *reinterpret_cast<uint4*>(hi + o0) = h0;
-            *reinterpret_cast<uint4*>(hi + o1) = h1;
-            *reinterpret_cast<uint4*>(hi + kPart + o0) = l0;
-            *reinterpret_cast<uint4*>(hi + kPart + o1) = l1;
-          }
-          // the next block's loads, a block ahead of their use
-          if (b + 1 < d.nb) fetch(v, b + 1, next);
-          if (v == 1 && mend && odd) *(volatile int*)&tail.bad[x] = 1;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBFull + s));
-        }
-        gs += 2;
-      }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
-    }
-    if (warp == 12) fill_skipped(a);
   } else if (warp == 9) {
     // ----------------------------------------------------------- products ----
     // converged and uniform throughout: see tcgen05.cuh
@@ -656,8 +737,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         // What lands early is waited for first: once P_m is there, its
         // product and the next scores go out without another wait (a wait
         // costs some 200 cycles even when there is nothing to wait for).
-        const int s = gs % kSlots;
-        if (due && !(ok = wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kSlots))) break;
+        const int s = gs % kS;
+        if (due && !(ok = wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kS))) break;
         if (b == 0) {
           // the piece before is finished while this one's queries land
           if (due) {
@@ -667,7 +748,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
           }
           if (!(ok = wait(kBQ, p) && (!two || wait(kBQ + 1, q1)))) break;
         }
-        if (!(ok = wait(kBFull + s, gs / kSlots))) break;
+        if (!(ok = wait(kBFull + s, gs / kS))) break;
         if (due) {
           if (!(ok = issue_o(0))) break;
         } else {
@@ -683,7 +764,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         if (b + 1 == nb) tc::commit(bar(kBQEmpty), lead);
         const int first = (kb + b) * kPages;
         const int lo = max(first, t_lo / kPage), hi = min(first + kPages, (t_hi + kPage - 1) / kPage);
-        v.s = (gs + 1) % kSlots;
+        v.s = (gs + 1) % kS;
         v.lo = lo & (kPages - 1);
         v.n = hi - lo;
         v.first = b == 0;
@@ -697,7 +778,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
       __syncwarp();
     }
-    if (ok && due && wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kSlots) && issue_o(0) && v.two) issue_o(1);
+    if (ok && due && wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kS) && issue_o(0) && v.two) issue_o(1);
     // every product issued completes before the tensor memory is freed
     if (any) {
       const int zero = 0;
@@ -709,6 +790,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   }
   } else {
     // ------------------------------------------------------------ softmax ----
+    if constexpr (kQ8) tc::more_registers<144>();
     const int m = warp >> 2, quarter = warp & 3;
     const int r = 128 * m + 32 * quarter + lane;  // row of the tile
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
@@ -763,26 +845,12 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                 sub = to - F::kShift;
                 l2[0].x *= al; l2[0].y *= al; l2[1].x *= al; l2[1].y *= al;
               }
-#pragma unroll 1
-              for (int e = 0; e < group; ++e) {  // the block's weights so far
-                uint32_t w[16];
-                tc::ld16w(tS + 16 * e, w);
-                tc::wait_ld();
-#pragma unroll
-                for (int u = 0; u < 16; ++u) w[u] = F::scale(w[u], al);
-                tc::st16(tS + 16 * e, w);
-              }
-              if (b > 0) {
-                // the values products so far are complete: S was issued after them
-#pragma unroll 1
-                for (int e = 0; e < 8; ++e) {
-                  float o[16];
-                  tc::ld16w(tO + 16 * e, reinterpret_cast<uint32_t(&)[16]>(o));
-                  tc::wait_ld();
-#pragma unroll
-                  for (int u = 0; u < 16; ++u) o[u] *= al;
-                  tc::st16(tO + 16 * e, reinterpret_cast<uint32_t(&)[16]>(o));
-                }
+              // the block's weights so far, and O: the values products before
+              // are complete, S was issued after them
+              tc::wait_ld();
+              if (group > 0 || b > 0) {
+                if constexpr (kQ8) rescale_here<DT>(tS, tO, group, b > 0, al);  // no registers for a call
+                else rescale<DT>(tS, tO, group, b > 0, al);
               }
             };
             const float2 mul = make_float2(GEN ? 1.0f : c1, GEN ? 1.0f : c1);
@@ -801,7 +869,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                   v[e] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(e)), y);
                 }
               }
-              if (!fast) {
+              if (__builtin_expect(!fast, 0)) {
                 const int from = lo - t0 - 32 * group, to = hi - t0 - 32 * group;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = e >= from && e < to ? v[e] : -INFINITY;
@@ -822,7 +890,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                   w[u] = F::pack(pr.x, pr.y);
                 }
                 const float bm = fmaxf(x0, x1) * (GEN ? 1.0f : c1);
-                if (!__any_sync(kFull, bm > mx + 8.0f)) break;
+                if (__builtin_expect(!__any_sync(kFull, bm > mx + 8.0f), 1)) break;
                 raise_to(bm, group);
               }
               l2[0] = tc::add2(l2[0], lb[0]);

@@ -134,6 +134,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Registers a thread of the (whole, converged) warpgroup may use from here on.
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Two fp32 values a b + c, one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   uint64_t x, y, z, d;
@@ -171,6 +181,19 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const void* tmap, int v,
       "l"(tmap), "r"(0), "r"(v), "r"(bar)
       : "memory");
 }
+// The 3-D box at {0, 0, z} (a page of codes), and `bytes` contiguous bytes.
+__device__ __forceinline__ void load_page(uint32_t dst, const void* tmap, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(tmap), "r"(0), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
 __device__ __forceinline__ void load_rows(uint32_t dst, const void* tmap, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %2}], "
@@ -192,7 +215,7 @@ __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
 }
 
 // The long end of a wait: false once *abort is set or after kWaitLimitNs.
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+__device__ __forceinline__ bool wait_on_here(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
   const unsigned long long t0 = global_ns();
   while (true) {
 #pragma unroll 1
@@ -207,16 +230,24 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile 
   return false;
 }
 
+// The same as a call, which keeps it out of the callers' loops.
+static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  return wait_on_here(bar, parity, abort, status);
+}
+
 // A wait by every lane of a warp, its outcome the same for all.  False once
 // *abort is set or after kWaitLimitNs; it then has set *abort and recorded
 // PKV_DEV_TIMEOUT.  A wait that has nothing to wait for is on many critical
 // paths: a poll, a vote and a branch (some 35 cycles; a loop that lets lanes
-// leave one by one took 157), and the clock is left to wait_on.
+// leave one by one took 157), and the clock is left to wait_on.  CALL: as a
+// call, where the caller has registers for one.
+template <bool CALL = true>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
 #pragma unroll 1
   for (int i = 0; i < 512; ++i)
     if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
-  return wait_on(bar, parity, abort, status);
+  if constexpr (CALL) return wait_on(bar, parity, abort, status);
+  return wait_on_here(bar, parity, abort, status);
 }
 
 }  // namespace tc
