@@ -425,7 +425,10 @@ def paged_decode_combine(seq_lens, n_q_heads: int, n_kv_heads: int, bt_stride: i
 
 
 # ------------------------------------------------------------- long prompts ----
+# The kernels behind these calls take a few microseconds for a decode step, so their arguments are looked at
+# with few attribute reads; what does not fit is looked at again by _need, for its message.
 _KIND = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 class _Scores(ctypes.Structure):  # pkv_scores
@@ -433,39 +436,56 @@ class _Scores(ctypes.Structure):  # pkv_scores
                 ("prefix_lens", _vp)]
 
 
-def _scores(scale, softcap, slopes, prefix_lens, n_q, rows, device):
-    if slopes is not None:
-        _need(slopes, torch.float32, "slopes", (n_q,), device)
-    if prefix_lens is not None:
-        _need(prefix_lens, torch.int32, "prefix_lens", (rows,), device)
-    return _Scores(float(scale), float(softcap), _ptr(slopes), _ptr(prefix_lens))
+def _array(t, dtype, name, shape, pool):
+    """The address of a contiguous tensor of this dtype and shape on the pool's device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and
+            t.get_device() == pool.device.index):
+        _need(t, dtype, name, shape, pool.device)
+    return t.data_ptr()
 
 
-def _chunk_rows(cu_seqlens, block_table, seq_lens, device):
-    rows, stride = _rows(block_table, seq_lens, device)
-    _need(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), device)
-    return rows, stride
+def _optional(t, dtype, name, shape, pool):
+    return None if t is None else _array(t, dtype, name, shape, pool)
 
 
-def _token_array(t, name, tokens, heads, dtype, device):
-    """Checks a token array [tokens][heads][128] whose tokens may be strided; its stride."""
+def _table(t, name, rows, pool):
+    """The address and the stride of a block table of `rows` rows."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be a tensor [rows][stride]")
+    return _array(t, torch.int32, name, t.shape, pool), t.shape[1]
+
+
+def _token_array(t, name, tokens, heads, dtype, pool):
+    """Checks a token array [tokens][heads][128] whose tokens may be strided; its address and stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 3 or t.shape[2] != HEAD_DIM or (tokens is not None and t.shape[0] != tokens) or \
-            (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{tokens}][{heads}][{HEAD_DIM}]")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != HEAD_DIM)):
+    if t.get_device() != pool.device.index:
+        raise ValueError(f"{name} is on {t.device}, expected {pool.device}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != HEAD_DIM or (tokens is not None and shape[0] != tokens) or \
+            (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{tokens}][{heads}][{HEAD_DIM}]")
+    stride = t.stride()
+    if (stride[2] != 1 or (shape[1] > 1 and stride[1] != HEAD_DIM)) and t.numel():
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * HEAD_DIM
 
 
-def _on(pool):
-    """The pool's device as the current one: launches go to the current device."""
-    return torch.cuda.device(pool.device)
+def _call(name, pool, stream, *args):
+    """The C entry `name` on the pool's device and the given stream, or its current one: launches go to the
+    current device."""
+    index = pool.device.index
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    fn = getattr(_lib, name)
+    if _current_device() == index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status:
+        raise PkvError(status, name, _lib.pkv_last_error_message().decode())
 
 
 def kv_rope_append(pool: KVPool, layer: int, q, k, v, positions, inv_freq, sections, cu_seqlens, block_table,
@@ -474,44 +494,48 @@ def kv_rope_append(pool: KVPool, layer: int, q, k, v, positions, inv_freq, secti
     pkv_chunk.h).  q [tokens][n_q][128] (None: keys and values only), k and v [tokens][n_kv][128] of one
     type (f16, bf16, f32), tokens strided at will; positions int32 [axes][tokens]; inv_freq fp32 [rot / 2];
     sections: pairs of each axis.  Returns q_out (the type of q unless given; it may be q)."""
-    rows, stride = _chunk_rows(cu_seqlens, block_table, seq_lens, pool.device)
+    bt, stride = _table(block_table, "block_table", None, pool)
+    rows = block_table.shape[0]
     if not isinstance(k, torch.Tensor) or k.dtype not in _KIND:
         raise TypeError("k must be a float16, bfloat16 or float32 tensor")
-    tokens = k.shape[0]
-    ks = _token_array(k, "k", tokens, pool.n_kv, k.dtype, pool.device)
-    vs = _token_array(v, "v", tokens, pool.n_kv, k.dtype, pool.device)
-    n_q = qs = 0
-    kind_out = _KIND[k.dtype]
+    dtype, tokens = k.dtype, k.shape[0]
+    kp, ks = _token_array(k, "k", tokens, pool.n_kv, dtype, pool)
+    vp, vs = _token_array(v, "v", tokens, pool.n_kv, dtype, pool)
+    kind = kind_out = _KIND[dtype]
+    qp = qs = n_q = 0
+    op = None
     if q is not None:
-        qs = _token_array(q, "q", tokens, None, k.dtype, pool.device)
+        qp, qs = _token_array(q, "q", tokens, None, dtype, pool)
         n_q = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(tokens, n_q, HEAD_DIM, dtype=q.dtype, device=pool.device)
-        if q_out.dtype not in _KIND:
-            raise TypeError(f"q_out must be float16, bfloat16 or float32, got {q_out.dtype}")
-        _need(q_out, q_out.dtype, "q_out", (tokens, n_q, HEAD_DIM), pool.device)
-        kind_out = _KIND[q_out.dtype]
+            q_out = torch.empty(tokens, n_q, HEAD_DIM, dtype=dtype, device=pool.device)
+        if not isinstance(q_out, torch.Tensor) or q_out.dtype not in _KIND:
+            raise TypeError("q_out must be a float16, bfloat16 or float32 tensor")
+        op, kind_out = _array(q_out, q_out.dtype, "q_out", (tokens, n_q, HEAD_DIM), pool), _KIND[q_out.dtype]
     elif q_out is not None:
         raise ValueError("q_out without q")
-    sections = [int(x) for x in sections]
-    _need(inv_freq, torch.float32, "inv_freq", device=pool.device)
-    _need(positions, torch.int32, "positions", (len(sections), tokens), pool.device)
-    sec = (ctypes.c_int * max(len(sections), 1))(*sections)
-    with _on(pool):
-        _check(lib().kv_rope_append(pool.handle, layer, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _KIND[k.dtype],
-                                    _ptr(q_out), kind_out, _ptr(positions), len(sections), sec, _ptr(inv_freq),
-                                    2 * inv_freq.numel(), int(interleaved), _ptr(cu_seqlens), tokens,
-                                    _ptr(block_table), stride, _ptr(seq_lens), rows, n_q, _stream(stream)),
-               "kv_rope_append")
+    axes = len(sections)
+    freq = _array(inv_freq, torch.float32, "inv_freq", inv_freq.shape, pool)
+    _call("kv_rope_append", pool, stream, pool.handle, layer, qp, qs, kp, ks, vp, vs, kind, op, kind_out,
+          _array(positions, torch.int32, "positions", (axes, tokens), pool), axes,
+          (_i * max(axes, 1))(*sections), freq, 2 * inv_freq.numel(), 1 if interleaved else 0,
+          _array(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), pool), tokens, bt, stride,
+          _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows, n_q)
     return q_out
 
 
+_sm_counts = {}  # device index: SMs, the default chunks of a call
+
+
 def _default_chunks_chunk(pool, n_q_heads):
-    c = ctypes.c_int(0)
-    with _on(pool):
-        _check(lib().paged_chunk_default_chunks(pool.handle, n_q_heads, ctypes.byref(c)),
-               "paged_chunk_default_chunks")
-    return c.value
+    chunks = _sm_counts.get(pool.device.index)
+    if chunks is None:
+        c = ctypes.c_int(0)
+        with torch.cuda.device(pool.device):
+            _check(lib().paged_chunk_default_chunks(pool.handle, n_q_heads, ctypes.byref(c)),
+                   "paged_chunk_default_chunks")
+        chunks = _sm_counts[pool.device.index] = c.value
+    return chunks
 
 
 class WorkspaceChunk:
@@ -537,6 +561,12 @@ class WorkspaceMass:
         self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=pool.device)
 
 
+def _scratch(workspace, pool):
+    if workspace.tensor.get_device() != pool.device.index:
+        raise ValueError(f"workspace is on {workspace.tensor.device}, expected {pool.device}")
+    return workspace.tensor.data_ptr(), workspace.nbytes, workspace.num_chunks
+
+
 def _q_type(pool):
     return torch.bfloat16 if pool.dtype == BF16 else torch.float16
 
@@ -547,23 +577,23 @@ def paged_chunk_attention(pool: KVPool, layer: int, q, cu_seqlens, block_table, 
     """Attention of a ragged chunk over the paged cache (paged_chunk_attention in pkv_chunk.h): q
     [tokens][n_q][128] in bf16 for bf16 pools and f16 for f16 and q8_0 pools.  Returns out, like q; `lse`
     (fp32 [tokens][n_q]) receives the log of the softmax denominators."""
-    rows, stride = _chunk_rows(cu_seqlens, block_table, seq_lens, pool.device)
-    qs = _token_array(q, "q", None, None, _q_type(pool), pool.device)
-    tokens, n_q = q.shape[:2]
+    bt, stride = _table(block_table, "block_table", None, pool)
+    rows = block_table.shape[0]
+    dtype = _q_type(pool)
+    qp, qs = _token_array(q, "q", None, None, dtype, pool)
+    tokens, n_q = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty(tokens, n_q, HEAD_DIM, dtype=q.dtype, device=pool.device)
-    _need(out, q.dtype, "out", (tokens, n_q, HEAD_DIM), pool.device)
-    if lse is not None:
-        _need(lse, torch.float32, "lse", (tokens, n_q), pool.device)
-    sc = _scores(scale, softcap, slopes, prefix_lens, n_q, rows, pool.device)
+        out = torch.empty(tokens, n_q, HEAD_DIM, dtype=dtype, device=pool.device)
+    op = _array(out, dtype, "out", (tokens, n_q, HEAD_DIM), pool)
+    lp = _optional(lse, torch.float32, "lse", (tokens, n_q), pool)
+    sc = _Scores(scale, softcap, _optional(slopes, torch.float32, "slopes", (n_q,), pool),
+                 _optional(prefix_lens, torch.int32, "prefix_lens", (rows,), pool))
     if workspace is None:
         workspace = WorkspaceChunk(pool, n_q)
-    with _on(pool):
-        _check(lib().paged_chunk_attention(pool.handle, layer, _ptr(q), qs, _KIND[q.dtype], _ptr(cu_seqlens),
-                                           tokens, _ptr(block_table), stride, _ptr(seq_lens), rows, n_q,
-                                           ctypes.byref(sc), _ptr(out), _ptr(lse), _ptr(workspace.tensor),
-                                           workspace.nbytes, workspace.num_chunks, _stream(stream)),
-               "paged_chunk_attention")
+    _call("paged_chunk_attention", pool, stream, pool.handle, layer, qp, qs, _KIND[dtype],
+          _array(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), pool), tokens, bt, stride,
+          _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows, n_q, ctypes.addressof(sc), op, lp,
+          *_scratch(workspace, pool))
     return out
 
 
@@ -572,29 +602,29 @@ def paged_attention_mass(pool: KVPool, layer: int, q, lse, cu_seqlens, block_tab
                          mass_in=None, mass_out=None, workspace: WorkspaceMass | None = None, stream=None):
     """Add the chunk's attention weights to each cached token's (paged_attention_mass in pkv_chunk.h):
     mass_in and mass_out fp32 [rows][n_kv][stride], which may be the same tensor.  Returns mass_out."""
-    rows, stride = _chunk_rows(cu_seqlens, block_table, seq_lens, pool.device)
-    qs = _token_array(q, "q", None, None, _q_type(pool), pool.device)
-    tokens, n_q = q.shape[:2]
-    _need(lse, torch.float32, "lse", (tokens, n_q), pool.device)
+    bt, stride = _table(block_table, "block_table", None, pool)
+    rows = block_table.shape[0]
+    dtype = _q_type(pool)
+    qp, qs = _token_array(q, "q", None, None, dtype, pool)
+    tokens, n_q = q.shape[0], q.shape[1]
+    lp = _array(lse, torch.float32, "lse", (tokens, n_q), pool)
     if mass_out is None:
         if mass_in is None:
             raise ValueError("mass_in or mass_out is needed")
         mass_out = mass_in
-    _need(mass_out, torch.float32, "mass_out", device=pool.device)
-    if mass_out.dim() != 3 or mass_out.shape[:2] != (rows, pool.n_kv):
-        raise ValueError("mass_out must be [rows][n_kv][stride]")
-    if mass_in is not None:
-        _need(mass_in, torch.float32, "mass_in", mass_out.shape, pool.device)
-    sc = _scores(scale, softcap, slopes, prefix_lens, n_q, rows, pool.device)
+    if not isinstance(mass_out, torch.Tensor) or mass_out.dim() != 3 or mass_out.shape[:2] != (rows, pool.n_kv):
+        raise ValueError("mass_out must be a tensor [rows][n_kv][stride]")
+    shape = mass_out.shape
+    mo = _array(mass_out, torch.float32, "mass_out", shape, pool)
+    mi = _optional(mass_in, torch.float32, "mass_in", shape, pool)
+    sc = _Scores(scale, softcap, _optional(slopes, torch.float32, "slopes", (n_q,), pool),
+                 _optional(prefix_lens, torch.int32, "prefix_lens", (rows,), pool))
     if workspace is None:
         workspace = WorkspaceMass(pool, n_q)
-    with _on(pool):
-        _check(lib().paged_attention_mass(pool.handle, layer, _ptr(q), qs, _KIND[q.dtype], _ptr(lse),
-                                          _ptr(cu_seqlens), tokens, _ptr(block_table), stride, _ptr(seq_lens),
-                                          rows, n_q, ctypes.byref(sc), last_queries, _ptr(mass_in),
-                                          _ptr(mass_out), mass_out.shape[2], _ptr(workspace.tensor),
-                                          workspace.nbytes, workspace.num_chunks, _stream(stream)),
-               "paged_attention_mass")
+    _call("paged_attention_mass", pool, stream, pool.handle, layer, qp, qs, _KIND[dtype], lp,
+          _array(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), pool), tokens, bt, stride,
+          _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows, n_q, ctypes.addressof(sc),
+          last_queries, mi, mo, shape[2], *_scratch(workspace, pool))
     return mass_out
 
 
@@ -603,30 +633,24 @@ def kv_evict(pool: KVPool, layer: int, mass, block_table, seq_lens, keep_lens, d
     """Shorten rows to keep_lens tokens per KV head by their attention weight (kv_evict in pkv_chunk.h);
     the kept K and V go to the pages of dst_block_table.  keep_idx int32 [rows][n_kv][stride] (made here
     unless given, as wide as the new pages hold).  Returns (keep_idx, new_lens)."""
-    rows, stride = _rows(block_table, seq_lens, pool.device)
-    _need(mass, torch.float32, "mass", device=pool.device)
-    if mass.dim() != 3 or mass.shape[:2] != (rows, pool.n_kv):
-        raise ValueError("mass must be [rows][n_kv][stride]")
-    _need(keep_lens, torch.int32, "keep_lens", (rows,), pool.device)
-    _need(dst_block_table, torch.int32, "dst_block_table", device=pool.device)
-    if dst_block_table.dim() != 2 or dst_block_table.shape[0] != rows:
-        raise ValueError("dst_block_table must be [rows][stride]")
+    bt, stride = _table(block_table, "block_table", None, pool)
+    rows = block_table.shape[0]
+    dst, dst_stride = _table(dst_block_table, "dst_block_table", rows, pool)
+    if not isinstance(mass, torch.Tensor) or mass.dim() != 3 or mass.shape[:2] != (rows, pool.n_kv):
+        raise ValueError("mass must be a tensor [rows][n_kv][stride]")
     if keep_idx is None:
-        keep_idx = torch.full((rows, pool.n_kv, PAGE * dst_block_table.shape[1]), -1, dtype=torch.int32,
-                              device=pool.device)
-    _need(keep_idx, torch.int32, "keep_idx", device=pool.device)
-    if keep_idx.dim() != 3 or keep_idx.shape[:2] != (rows, pool.n_kv):
-        raise ValueError("keep_idx must be [rows][n_kv][stride]")
+        keep_idx = torch.full((rows, pool.n_kv, PAGE * dst_stride), -1, dtype=torch.int32, device=pool.device)
+    if not isinstance(keep_idx, torch.Tensor) or keep_idx.dim() != 3 or keep_idx.shape[:2] != (rows, pool.n_kv):
+        raise ValueError("keep_idx must be a tensor [rows][n_kv][stride]")
     if new_lens is None:
         new_lens = torch.empty_like(seq_lens)
-    _need(new_lens, torch.int32, "new_lens", (rows,), pool.device)
-    if dst_mass is not None:
-        _need(dst_mass, torch.float32, "dst_mass", keep_idx.shape, pool.device)
-    with _on(pool):
-        _check(lib().kv_evict(pool.handle, layer, _ptr(mass), mass.shape[2], _ptr(block_table), stride,
-                              _ptr(seq_lens), rows, _ptr(keep_lens), first, recent, _ptr(dst_block_table),
-                              dst_block_table.shape[1], _ptr(keep_idx), keep_idx.shape[2], _ptr(dst_mass),
-                              _ptr(new_lens), _stream(stream)), "kv_evict")
+    shape = keep_idx.shape
+    _call("kv_evict", pool, stream, pool.handle, layer, _array(mass, torch.float32, "mass", mass.shape, pool),
+          mass.shape[2], bt, stride, _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows,
+          _array(keep_lens, torch.int32, "keep_lens", (rows,), pool), first, recent, dst, dst_stride,
+          _array(keep_idx, torch.int32, "keep_idx", shape, pool), shape[2],
+          _optional(dst_mass, torch.float32, "dst_mass", shape, pool),
+          _array(new_lens, torch.int32, "new_lens", (rows,), pool))
     return keep_idx, new_lens
 
 
