@@ -165,7 +165,7 @@ struct QueryTiles {
 // Records of the boundaries (Rec), then two partial slots per chunk: slot 2k
 // for the piece at the start of range k, 2k + 1 for the one at its end.  A
 // slot: (m, l) of its 256 rows, then O as [32 groups of 4 dims][256 rows].
-struct Rec {
+struct __align__(16) Rec {
   int inside;  // the boundary cuts a tile
   int h, tile, tok, nq, pad[3];
 };
@@ -1007,60 +1007,91 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
 }
 
 // ---------------------------------------------------------------- merge ----
-// CTA (k, y): if boundary k is the first to cut its tile, the tile's rows
-// 32 y .. from its pieces: the end of range k - 1 and the starts of the ranges
-// whose boundaries cut it.
+// CTA (k, y): if boundary k + 1 is the first to cut its tile, the tile's rows
+// 32 y .. from its pieces: the end of range k and the starts of the ranges
+// whose boundaries cut it.  A thread takes 16 dims of a row; the records, and
+// then the pieces four at a time, are loaded together, so that a merge of a few
+// pieces is three trips to memory.
 constexpr int kMergeThreads = 256;
 template <int DT>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkAttnArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int k0 = blockIdx.x + 1;
   grid_dependency_wait();
   grid_launch_dependents();
   const Rec* rec = reinterpret_cast<const Rec*>(a.workspace);
-  const int k0 = blockIdx.x + 1;
-  const Rec me = rec[k0];
-  if (!me.inside) return;
-  const Rec prev = rec[k0 - 1];
-  if (prev.inside && prev.h == me.h && prev.tile == me.tile) return;
+  auto load_rec = [&](int k) { return *reinterpret_cast<const int4*>(rec + k); };
+  const int4 prev = load_rec(k0 - 1), me = load_rec(k0);  // inside, h, tile, tok
+  const int nq = rec[k0].nq;
+  int4 ahead = make_int4(0, 0, 0, 0);  // lane l: boundary k0 + 1 + l
+  if (k0 + 1 + lane < a.chunks) ahead = load_rec(k0 + 1 + lane);
+  if (!me.x || (prev.x && prev.y == me.y && prev.z == me.z)) return;
   const int G = a.n_q / a.pool.n_kv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = 32 * blockIdx.y + lane;
-  if (32 * static_cast<int>(blockIdx.y) >= me.nq * G) return;
-  int k1 = k0;
-  while (k1 + 1 < a.chunks) {
-    const Rec n = rec[k1 + 1];
-    if (!n.inside || n.h != me.h || n.tile != me.tile) break;
-    ++k1;
+  if (32 * static_cast<int>(blockIdx.y) >= nq * G) return;
+  // the boundaries after k0 that cut the tile
+  int cuts = 0;
+  for (int base = k0 + 1;; base += 32) {
+    const unsigned same = __ballot_sync(kFull, ahead.x && ahead.y == me.y && ahead.z == me.z);
+    if (same != kFull) {
+      cuts += __ffs(~same) - 1;
+      break;
+    }
+    cuts += 32;
+    ahead = base + 32 + lane < a.chunks ? load_rec(base + 32 + lane) : make_int4(0, 0, 0, 0);
   }
-  if (r >= me.nq * G) return;
-  // pieces: slot 2 (k0 - 1) + 1, then 2 k for k0 .. k1
-  auto slot_of = [&](int k) { return k < k0 ? 2 * k + 1 : 2 * k; };
-  float M = -INFINITY;
-  for (int k = k0 - 1; k <= k1; ++k) {
-    const float2 ml = slot_ml(a, slot_of(k))[r];
-    if (ml.y > 0.0f || ml.y != ml.y) M = fmaxf(M, ml.x);
-  }
-  float Lsum = 0.0f;
+  if (r >= nq * G) return;
+  // piece 0: slot 2 (k0 - 1) + 1; piece u: slot 2 (k0 + u - 1)
+  const int pieces = cuts + 2;
+  float M = -INFINITY, Lsum = 0.0f;
   float4 acc[4];  // dims 16 warp ..
 #pragma unroll
   for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = k0 - 1; k <= k1; ++k) {
-    const int s = slot_of(k);
-    const float2 ml = slot_ml(a, s)[r];
-    if (ml.y == 0.0f) continue;  // no token of the row in the piece
-    const float w = tc::ex2(ml.x - M);
-    Lsum += w * ml.y;
-    const float4* src = slot_acc(a, s) + r;
+  for (int u0 = 0; u0 < pieces; u0 += 4) {
+    float2 ml[4];
+    float4 v[4][4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.0f);
+      if (u0 + u < pieces) {
+        const int s = u0 + u == 0 ? 2 * k0 - 1 : 2 * (k0 + u0 + u - 1);
+        ml[u] = slot_ml(a, s)[r];
+        const float4* src = slot_acc(a, s) + r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[u][e] = src[(4 * warp + e) * kTileRows];
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (ml[u].y != 0.0f) m = fmaxf(m, ml[u].x);
+    if (m == -INFINITY) m = 0.0f;  // no token of the row so far
+    const float keep = tc::ex2(M - m);
+    Lsum *= keep;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float4 v = src[(4 * warp + e) * kTileRows];
-      acc[e].x = fmaf(w, v.x, acc[e].x);
-      acc[e].y = fmaf(w, v.y, acc[e].y);
-      acc[e].z = fmaf(w, v.z, acc[e].z);
-      acc[e].w = fmaf(w, v.w, acc[e].w);
+      acc[e].x *= keep;
+      acc[e].y *= keep;
+      acc[e].z *= keep;
+      acc[e].w *= keep;
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (ml[u].y == 0.0f) continue;  // no token of the row in the piece (or no piece)
+      const float w = tc::ex2(ml[u].x - m);
+      Lsum = fmaf(w, ml[u].y, Lsum);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[e].x = fmaf(w, v[u][e].x, acc[e].x);
+        acc[e].y = fmaf(w, v[u][e].y, acc[e].y);
+        acc[e].z = fmaf(w, v[u][e].z, acc[e].z);
+        acc[e].w = fmaf(w, v[u][e].w, acc[e].w);
+      }
+    }
+    if (Lsum != 0.0f) M = m;
   }
   const float inv = 1.0f / Lsum;
-  const long long row = static_cast<long long>(me.tok + r / G) * a.n_q + me.h * G + r % G;
+  const long long row = static_cast<long long>(me.w + r / G) * a.n_q + me.y * G + r % G;
   uint4* to = reinterpret_cast<uint4*>(a.out + (row * kD + 16 * warp) * 2);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {

@@ -4,16 +4,16 @@
 // Selecting.  A token's key is its weight as an unsigned integer of the same
 // order (NaN lowest; the protected first and recent tokens highest), so the B
 // kept tokens of a (row, KV head) are the B largest keys with ties to the
-// lowest index.  The B-th largest key T is found digit by digit from the top
+// lowest index.  One CTA holds the keys in registers, token 512 k + tid as the
+// thread's k-th, and finds the B-th largest key T digit by digit from the top
 // (11, 11 and 10 bits): a histogram of the digit over the keys that match the
-// digits found so far, and the digit at which the count from above reaches B.
-// Then token t is kept if its key exceeds T, or equals T with fewer than
-// (B - #greater) equals before it; its place among the kept is
+// digits found so far, in four copies to spread its atomics, and the digit at
+// which the count from above reaches B.  Then token t is kept if its key
+// exceeds T, or equals T with fewer than (B - #greater) equals before it; its
+// place among the kept is
 //     #greater before t + min(#equal before t, B - #greater),
-// two prefix sums.  A cluster of CTAs shares one (row, KV head), each with a
-// contiguous slice of its tokens; the histograms and the slices' counts meet
-// through distributed shared memory.  The keys are read once and kept in
-// shared memory while the slice fits, and re-read (from L2) beyond.
+// prefix sums of votes over groups of 32 tokens in order.  Rows longer than the
+// registers hold re-read their weights (from L2) in every pass.
 //
 // Gathering.  The kept tokens go to fresh pages, so every copy is independent:
 // a CTA takes 64 kept tokens of a head and moves their K and V in 16-byte
@@ -26,29 +26,12 @@
 namespace pkv {
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kCachedKeys = 8192;  // a slice of this many keys stays in shared memory
+constexpr int kCopies = 4;
 constexpr int kGatherTokens = 64;
 constexpr int kGatherThreads = 256;
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// Arrive and wait with release / acquire order over the cluster's threads.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A word of CTA `rank`'s shared memory, at the place `addr` has in this CTA's.
-__device__ __forceinline__ uint32_t peer_load(uint32_t addr, uint32_t rank) {
-  uint32_t a, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
 
 // The row's tokens L and budget B, clamped to what the tables hold.
 __device__ __forceinline__ void row_budget(const EvictArgs& a, int i, int32_t* status, int& L, int& B) {
@@ -73,149 +56,179 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return (b >> 31) ? ~b : (b | 0x80000000u);
 }
 
-struct SelShared {
-  uint32_t hist[kBins];
-  uint32_t scan[kSelWarps];
-  uint32_t pick[2];      // the digit, and the count above it
-  uint32_t totals[2];    // greater and equal keys of this CTA's slice
-  uint32_t seg[2][kSelWarps];
-};
-
-template <int CS>
+// KPT: keys of a thread, in registers; 0: re-read in every step.
+template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
-  extern __shared__ __align__(16) uint32_t keys[];  // [kCachedKeys]
-  __shared__ SelShared sm;
+  constexpr int kPasses = KPT > 0 ? KPT : 1;
+  __shared__ __align__(16) uint32_t hist[kCopies][kBins];
+  __shared__ uint32_t bin_sums[kSelWarps];
+  __shared__ uint32_t pick[2];  // the digit, and the count above it
+  // votes of each (pass, warp): greater in the low half, equal in the high one
+  __shared__ uint32_t votes[kPasses * kSelWarps];
+  __shared__ unsigned long long scan_sums[kSelWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = CS > 1 ? cluster_rank() : 0u;
-  const int seg = blockIdx.x / CS;  // (row, KV head)
+  const int seg = blockIdx.x;  // (row, KV head)
   const int i = seg / a.pool.n_kv, h = seg - i * a.pool.n_kv;
   grid_dependency_wait();
   grid_launch_dependents();
   int L, B;
-  row_budget(a, i, (h == 0 && rank == 0 && tid == 0) ? a.pool.status : nullptr, L, B);
+  row_budget(a, i, (h == 0 && tid == 0) ? a.pool.status : nullptr, L, B);
   const float* mass = a.mass + static_cast<long long>(seg) * a.mass_stride;
   int32_t* keep = a.keep_idx + static_cast<long long>(seg) * a.keep_stride;
-  float* kept_mass = a.dst_mass ? a.dst_mass + static_cast<long long>(seg) * a.keep_stride : nullptr;
-  if (h == 0 && rank == 0 && tid == 0) a.new_lens[i] = B;
-  if (B == L || B == 0) {  // uniform over the cluster: everything kept, or nothing
-    for (int t = static_cast<int>(rank) * kSelThreads + tid; t < B; t += CS * kSelThreads) {
-      keep[t] = t;
-      if (kept_mass) kept_mass[t] = mass[t];
-    }
+  if (h == 0 && tid == 0) a.new_lens[i] = B;
+  if (B == L || B == 0) {  // everything kept, or nothing
+    for (int t = tid; t < B; t += kSelThreads) keep[t] = t;
     return;
   }
   const int recent = min(a.recent, B), first = min(a.first, B - recent);
-  // this CTA's slice [s0, s1), cut at multiples of 32
-  const int groups = (L + 31) / 32, per = (groups + CS - 1) / CS;
-  const int s0 = min(L, static_cast<int>(rank) * per * 32), s1 = min(L, s0 + per * 32);
-  const bool cached = s1 - s0 <= kCachedKeys;
-  auto fetch = [&](int t) {
-    if (t < first || t >= L - recent) return 0xFFFFFFFFu;
-    return key_of(__ldg(mass + t));
-  };
-  auto key = [&](int t) { return cached ? keys[t - s0] : fetch(t); };
-  if (cached)
-    for (int t = s0 + tid; t < s1; t += kSelThreads) keys[t - s0] = fetch(t);
-
-  uint32_t prefix = 0, mask = 0;  // the digits of T found so far
-  uint32_t want = static_cast<uint32_t>(B);
-  const uint32_t hist_at = smem_addr(sm.hist);
+  const int passes = (L + kSelThreads - 1) / kSelThreads;
+  auto key_at = [&](int t, float x) { return t < first || t >= L - recent ? 0xFFFFFFFFu : key_of(x); };
+  auto fetch = [&](int t) { return key_at(t, __ldg(mass + t)); };
+  uint32_t key[kPasses];
+  if constexpr (KPT > 0) {
+    // every load first: the keys' arithmetic between them would wait for each
+#pragma unroll
+    for (int k = 0; k < KPT; ++k)
+      if (k < passes) key[k] = __float_as_uint(__ldg(mass + min(k * kSelThreads + tid, L - 1)));
+#pragma unroll
+    for (int k = 0; k < KPT; ++k)
+      if (k < passes) key[k] = key_at(k * kSelThreads + tid, __uint_as_float(key[k]));
+  }
+  uint32_t T = 0, mask = 0;  // the digits of T found so far
+  int want = B;              // how many of the keys that match them are kept
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t digit_mask = pass == 2 ? 1023u : 2047u;
-    for (int b = tid; b < kBins; b += kSelThreads) sm.hist[b] = 0u;
+    const uint32_t digit = pass == 2 ? 1023u : 2047u;
+    for (int e = tid; e < kCopies * kBins / 4; e += kSelThreads)
+      reinterpret_cast<uint4*>(hist)[e] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
-    for (int t = s0 + tid; t < s1; t += kSelThreads) {
-      const uint32_t x = key(t);
-      if ((x & mask) == prefix) atomicAdd(&sm.hist[(x >> shift) & digit_mask], 1u);
-    }
-    if (CS > 1) cluster_sync(); else __syncthreads();
-    // thread tid holds two bins, counted from the top
-    const int b0 = kBins - 1 - 2 * tid, b1 = b0 - 1;
-    uint32_t c0 = 0, c1 = 0;
+    uint32_t* mine = hist[warp % kCopies];
+    auto count = [&](int t, uint32_t x) {
+      if (t < L && (x & mask) == T) atomicAdd(&mine[(x >> shift) & digit], 1u);
+    };
+    if constexpr (KPT > 0) {
 #pragma unroll
-    for (int r = 0; r < CS; ++r) {
-      c0 += CS > 1 ? peer_load(hist_at + 4 * b0, r) : sm.hist[b0];
-      c1 += CS > 1 ? peer_load(hist_at + 4 * b1, r) : sm.hist[b1];
+      for (int k = 0; k < KPT; ++k)
+        if (k < passes) count(k * kSelThreads + tid, key[k]);
+    } else {
+      for (int t = tid; t < L; t += kSelThreads) count(t, fetch(t));
     }
-    uint32_t v = c0 + c1;  // inclusive scan of the pairs
+    __syncthreads();
+    // a thread's bins, from the top: 4 consecutive ones
+    constexpr int kPer = kBins / kSelThreads;
+    static_assert(kPer == 4, "");
+    const int b0 = kBins - kPer * (tid + 1);
+    uint32_t c[kPer] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int r = 0; r < kCopies; ++r) {
+      const uint4 v = *reinterpret_cast<const uint4*>(&hist[r][b0]);
+      c[3] += v.x;
+      c[2] += v.y;
+      c[1] += v.z;
+      c[0] += v.w;
+    }
+    const uint32_t sum = c[0] + c[1] + c[2] + c[3];
+    uint32_t run = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(kFull, v, o);
-      if (lane >= o) v += u;
+      const uint32_t u = __shfl_up_sync(kFull, run, o);
+      if (lane >= o) run += u;
     }
-    if (lane == 31) sm.scan[warp] = v;
+    if (lane == 31) bin_sums[warp] = run;
     __syncthreads();
-    uint32_t before = lane < warp ? sm.scan[lane] : 0u;
+    uint32_t above = run - sum + __reduce_add_sync(kFull, lane < warp ? bin_sums[lane & (kSelWarps - 1)] : 0u);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(kFull, before, o);
-    const uint32_t above0 = before + v - c0 - c1, above1 = above0 + c0;
-    if (above0 < want && want <= above0 + c0) {
-      sm.pick[0] = static_cast<uint32_t>(b0);
-      sm.pick[1] = above0;
-    } else if (above1 < want && want <= above1 + c1) {
-      sm.pick[0] = static_cast<uint32_t>(b1);
-      sm.pick[1] = above1;
+    for (int u = 0; u < kPer; ++u) {
+      if (above < static_cast<uint32_t>(want) && static_cast<uint32_t>(want) <= above + c[u]) {
+        pick[0] = static_cast<uint32_t>(b0 + kPer - 1 - u);
+        pick[1] = above;
+      }
+      above += c[u];
     }
-    if (CS > 1) cluster_sync(); else __syncthreads();  // every peer has read this CTA's counts
-    prefix |= sm.pick[0] << shift;
-    mask |= digit_mask << shift;
-    want -= sm.pick[1];
     __syncthreads();
+    T |= pick[0] << shift;
+    mask |= digit << shift;
+    want -= static_cast<int>(pick[1]);
   }
-  // want: how many keys equal to T = prefix are kept.  Each warp takes a
-  // contiguous part of the slice.
-  const int len = s1 - s0;
-  const int wgroups = ((len + 31) / 32 + kSelWarps - 1) / kSelWarps;
-  const int w0 = min(s1, s0 + warp * wgroups * 32), w1 = min(s1, w0 + wgroups * 32);
-  uint32_t ngt = 0, neq = 0;
-  for (int t = w0 + lane; t - lane < w1; t += 32) {
-    const uint32_t x = t < w1 ? key(t) : 0u;
-    ngt += __popc(__ballot_sync(kFull, t < w1 && x > prefix));
-    neq += __popc(__ballot_sync(kFull, t < w1 && x == prefix));
-  }
-  if (lane == 0) {
-    sm.seg[0][warp] = ngt;
-    sm.seg[1][warp] = neq;
-  }
-  __syncthreads();
-  uint32_t gt = lane < warp ? sm.seg[0][lane] : 0u, eq = lane < warp ? sm.seg[1][lane] : 0u;
+  const unsigned below = (1u << lane) - 1u;
+  // token t of key x, with g greater and e equal keys before it
+  auto place = [&](int t, uint32_t x, uint32_t g, uint32_t e) {
+    if (t < L && (x > T || (x == T && e < static_cast<uint32_t>(want)))) {
+      keep[g + min(e, static_cast<uint32_t>(want))] = t;
+    }
+  };
+  if constexpr (KPT > 0) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    gt += __shfl_xor_sync(kFull, gt, o);
-    eq += __shfl_xor_sync(kFull, eq, o);
-  }
-  if (CS > 1) {
-    if (warp == kSelWarps - 1 && lane == 0) {
-      sm.totals[0] = gt + ngt;
-      sm.totals[1] = eq + neq;
+    for (int k = 0; k < KPT; ++k)
+      if (k < passes) {
+        const bool in = k * kSelThreads + tid < L;
+        const int g = __popc(__ballot_sync(kFull, in && key[k] > T)), e = __popc(__ballot_sync(kFull, in && key[k] == T));
+        if (lane == 0) votes[k * kSelWarps + warp] = static_cast<uint32_t>(g) | (static_cast<uint32_t>(e) << 16);
+      }
+    __syncthreads();
+    // exclusive prefix sums of the votes in order, a thread a few consecutive ones
+    constexpr int kPer = (KPT * kSelWarps + kSelThreads - 1) / kSelThreads;
+    unsigned long long mine[kPer], sum = 0;
+    const int n = passes * kSelWarps;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int at = tid * kPer + u;
+      const uint32_t v = at < n ? votes[at] : 0u;
+      mine[u] = (v & 0xFFFFu) | (static_cast<unsigned long long>(v >> 16) << 32);
+      sum += mine[u];
     }
-    cluster_sync();
-    const uint32_t at = smem_addr(sm.totals);
-    for (uint32_t r = 0; r < rank; ++r) {
-      gt += peer_load(at, r);
-      eq += peer_load(at + 4, r);
+    unsigned long long run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(kFull, run, o);
+      if (lane >= o) run += u;
+    }
+    if (lane == 31) scan_sums[warp] = run;
+    __syncthreads();
+    unsigned long long pre = run - sum;
+    {
+      unsigned long long w = lane < warp ? scan_sums[lane & (kSelWarps - 1)] : 0ull;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(kFull, w, o);
+      pre += w;
+    }
+    uint2* before = reinterpret_cast<uint2*>(hist);  // the histograms are done with
+    static_assert(KPT * kSelWarps * sizeof(uint2) <= sizeof(hist), "");
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int at = tid * kPer + u;
+      if (at < n) before[at] = make_uint2(static_cast<uint32_t>(pre), static_cast<uint32_t>(pre >> 32));
+      pre += mine[u];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < KPT; ++k)
+      if (k < passes) {
+        const int t = k * kSelThreads + tid;
+        const uint2 b = before[k * kSelWarps + warp];
+        const unsigned mg = __ballot_sync(kFull, t < L && key[k] > T), me = __ballot_sync(kFull, t < L && key[k] == T);
+        place(t, key[k], b.x + __popc(mg & below), b.y + __popc(me & below));
+      }
+  } else {
+    uint32_t gt = 0, eq = 0;  // greater and equal keys in the passes before
+    for (int k = 0; k < passes; ++k) {
+      const int t = k * kSelThreads + tid;
+      const uint32_t x = t < L ? fetch(t) : 0u;
+      const unsigned mg = __ballot_sync(kFull, t < L && x > T), me = __ballot_sync(kFull, t < L && x == T);
+      if (lane == 0) votes[warp] = static_cast<uint32_t>(__popc(mg)) | (static_cast<uint32_t>(__popc(me)) << 16);
+      __syncthreads();
+      const uint32_t v = lane < kSelWarps ? votes[lane] : 0u;
+      const uint32_t all = __reduce_add_sync(kFull, v), pre = __reduce_add_sync(kFull, lane < warp ? v : 0u);
+      place(t, x, gt + (pre & 0xFFFFu) + __popc(mg & below), eq + (pre >> 16) + __popc(me & below));
+      gt += all & 0xFFFFu;
+      eq += all >> 16;
+      __syncthreads();
     }
   }
-  for (int t = w0 + lane; t - lane < w1; t += 32) {
-    const uint32_t x = t < w1 ? key(t) : 0u;
-    const bool is_gt = t < w1 && x > prefix, is_eq = t < w1 && x == prefix;
-    const unsigned mg = __ballot_sync(kFull, is_gt), me = __ballot_sync(kFull, is_eq);
-    const unsigned below = (1u << lane) - 1u;
-    const uint32_t g = gt + __popc(mg & below), e = eq + __popc(me & below);
-    if (is_gt || (is_eq && e < want)) {
-      const uint32_t to = g + min(e, want);
-      keep[to] = t;
-      if (kept_mass) kept_mass[to] = mass[t];
-    }
-    gt += __popc(mg);
-    eq += __popc(me);
-  }
-  if (CS > 1) cluster_sync();  // no CTA leaves while a peer may read its totals
 }
 
-// K and V of 64 kept tokens of one (row, KV head).
+// K, V and the weights of 64 kept tokens of one (row, KV head).
 template <int DT>
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ long long src_at[kGatherTokens], dst_at[kGatherTokens];  // token rows in the pool, -1: no copy
@@ -239,6 +252,10 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __gr
     const long long d = (static_cast<long long>(dp) * a.pool.n_kv + h) * kPage + b % kPage;
     src_at[tid] = ok && s != d ? s : -1;
     dst_at[tid] = d;
+    if (a.dst_mass) {
+      const long long seg = static_cast<long long>(i) * a.pool.n_kv + h;
+      a.dst_mass[seg * a.keep_stride + b] = __ldg(a.mass + seg * a.mass_stride + t);
+    }
   }
   __syncthreads();
   const int total = n * kUnits;  // a piece of K and the same piece of V
@@ -273,23 +290,18 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __gr
   }
 }
 
-template <int CS>
+template <int KPT>
 cudaError_t launch_select(const EvictArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.num_rows) * a.pool.n_kv * CS);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_rows) * a.pool.n_kv);
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = kCachedKeys * sizeof(uint32_t);
   cfg.stream = st;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CS;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CS > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel<CS>, a);
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -314,11 +326,13 @@ cudaError_t launch_gather(const EvictArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
-  // The CTAs that share a (row, KV head), by the longest row the tables allow.
+  // The keys of a thread, by the longest row the tables allow.
   const long long cap = a.mass_stride < static_cast<long long>(a.bt_stride) * kPage
                             ? a.mass_stride
                             : static_cast<long long>(a.bt_stride) * kPage;
-  cudaError_t e = cap <= 4096 ? launch_select<1>(a, st) : launch_select<4>(a, st);
+  cudaError_t e = cap <= 8 * kSelThreads    ? launch_select<8>(a, st)
+                  : cap <= 64 * kSelThreads ? launch_select<64>(a, st)
+                                            : launch_select<0>(a, st);
   if (e != cudaSuccess) return e;
   if (a.pool.dtype == PKV_KV_F16 || a.pool.dtype == PKV_KV_BF16) return launch_gather<PKV_KV_F16>(a, st);
   if (a.pool.dtype == PKV_KV_F32) return launch_gather<PKV_KV_F32>(a, st);
