@@ -150,14 +150,15 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
     prefetch_tensormap(&maps.kp);
     prefetch_tensormap(&qmap);
     tail.ctl[0] = 0;
-    for (int b = 0; b < kNumBars; ++b) {
-      int count = 1;
-      if (b < kBKEmpty && kQ8) count = 4;
-      if (b >= kBLseEmpty && b < kBS) count = 8;
-      if (b >= kBSFree && b < kBDesc) count = 4;
-      if (b >= kBDescEmpty && b < kBDrain) count = kReaders;
-      mbar_init(bar(b), count);
-    }
+  }
+  if (tid < kNumBars) {
+    const int b = tid;
+    int count = 1;
+    if (b < kBKEmpty && kQ8) count = 4;
+    if (b >= kBLseEmpty && b < kBS) count = 8;
+    if (b >= kBSFree && b < kBDesc) count = 4;
+    if (b >= kBDescEmpty && b < kBDrain) count = kReaders;
+    mbar_init(bar(b), count);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -170,11 +171,35 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
   grid_dependency_wait();
   grid_launch_dependents();
   const TokenTiles geo{QT, a.pool.window, a.last_queries, a.mass_stride};
-  const int T = chunk_plan(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, 1, tail.tile_start, &tail.scratch,
+  // a small call's plan is made by the one warp that walks the work
+  const bool small = a.rows.num_rows <= 32 && min(a.mass_stride, a.rows.bt_stride * kPage) <= 16 * kMassTok;
+  int T = 0;
+  if (small)
+    __syncthreads();
+  else
+    T = chunk_plan(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, 1, tail.tile_start, &tail.scratch,
                            tail.bounds);
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tail.tmem);
-  const Place begin = tail.bounds[0], end = tail.bounds[1];
+  Place begin = tail.bounds[0], end = tail.bounds[1];  // of a small call: made by warp 8
+  if (warp == 8) {  // before the test hook: the merge reads every range's record
+    if (small) T = chunk_plan_warp(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, 1, begin, end);
+    if (lane == 0) {  // the boundary at this range's start, for the merge
+      Rec x{};
+      x.inside = begin.h < a.pool.n_kv && begin.off > 0;
+      if (x.inside) {
+        const RowInfo r = row_info(a.rows, begin.i, nullptr);
+        x.h = begin.h;
+        x.tile = begin.tile;
+        x.i = begin.i;
+        x.t0 = begin.t * kMassTok;
+        x.L = r.L;
+        x.n = r.n;
+      }
+      reinterpret_cast<Rec*>(a.workspace)[blockIdx.x] = x;
+    }
+    __syncwarp();
+  }
   const bool stalled = test_stall(bar(kBStall), a.pool.test_stall_ns, ctl, a.pool.status);
 
   auto wait = [&](int b, uint32_t parity) { return tc::warp_wait(bar(b), parity & 1u, ctl, a.pool.status); };
@@ -564,20 +589,6 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
     }
   }
 
-  if (tid == 0) {  // the boundary at this range's start, for the merge
-    Rec x{};
-    x.inside = begin.h < a.pool.n_kv && begin.off > 0;
-    if (x.inside) {
-      const RowInfo r = row_info(a.rows, begin.i, nullptr);
-      x.h = begin.h;
-      x.tile = begin.tile;
-      x.i = begin.i;
-      x.t0 = begin.t * kMassTok;
-      x.L = r.L;
-      x.n = r.n;
-    }
-    reinterpret_cast<Rec*>(a.workspace)[blockIdx.x] = x;
-  }
   tc::fence_before();
   __syncthreads();
   if (warp == 9) {

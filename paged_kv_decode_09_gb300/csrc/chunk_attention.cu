@@ -303,13 +303,14 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     prefetch_tensormap(&maps.vp);
     prefetch_tensormap(&qmap);
     tail.ctl[0] = 0;
-    for (int b = 0; b < kNumBars; ++b) {
-      int count = 1;
-      if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = 4;
-      if (b >= kBP && b < kBO) count = 4;
-      if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT>;
-      mbar_init(bar(b), count);
-    }
+  }
+  if (tid < kNumBars) {
+    const int b = tid;
+    int count = 1;
+    if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = 4;
+    if (b >= kBP && b < kBO) count = 4;
+    if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT>;
+    mbar_init(bar(b), count);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -322,14 +323,42 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   grid_dependency_wait();
   grid_launch_dependents();
   const QueryTiles<DT> geo{QT, a.pool.window};
-  const int T = chunk_plan(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, kSplitSnap<DT>,
+  // a small call's plan is made by the one warp that walks the work
+  const bool small = a.rows.num_rows <= 32 && a.rows.total_tokens <= 32 * QT;
+  int T = 0;
+  if (small)
+    __syncthreads();
+  else
+    T = chunk_plan(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, kSplitSnap<DT>,
                            reinterpret_cast<int*>(smem + kRing), &tail.scratch, tail.bounds);
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tail.tmem);
-  const Place begin = tail.bounds[0], end = tail.bounds[1];
-  // the ring is written next by the async proxy, after the plan's plain accesses
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncthreads();
+  Place begin, end;
+  if (!small) {
+    begin = tail.bounds[0];
+    end = tail.bounds[1];
+    // the ring is written next by the async proxy, after the plan's plain accesses
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+  }
+  if (warp == 8) {  // before the test hook: the merge reads every range's record
+    if (small)
+      T = chunk_plan_warp(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, kSplitSnap<DT>, begin, end);
+    if (lane == 0) {  // the boundary at this range's start, for the merge
+      Rec x{};
+      x.inside = begin.h < a.pool.n_kv && begin.off > 0;
+      if (x.inside) {
+        const RowInfo r = row_info(a.rows, begin.i, nullptr);
+        const TileGeom g = geo.tile(r, 0, begin.t);
+        x.h = begin.h;
+        x.tile = begin.tile;
+        x.tok = r.start + begin.t * QT;
+        x.nq = g.nq;
+      }
+      reinterpret_cast<Rec*>(a.workspace)[blockIdx.x] = x;
+    }
+    __syncwarp();
+  }
   // test hook: every warp gives up here, before any copy
   const bool stalled = test_stall(bar(kBStall), a.pool.test_stall_ns, ctl, a.pool.status);
 
@@ -983,21 +1012,6 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     }
   }
 
-  // the boundary at this range's start, for the merge
-  if (tid == 0) {
-    Rec* rec = reinterpret_cast<Rec*>(a.workspace) + blockIdx.x;
-    Rec x{};
-    x.inside = begin.h < a.pool.n_kv && begin.off > 0;
-    if (x.inside) {
-      const RowInfo r = row_info(a.rows, begin.i, nullptr);
-      const TileGeom g = geo.tile(r, 0, begin.t);
-      x.h = begin.h;
-      x.tile = begin.tile;
-      x.tok = r.start + begin.t * QT;
-      x.nq = g.nq;
-    }
-    *rec = x;
-  }
   tc::fence_before();
   __syncthreads();
   if (warp == 9) {
