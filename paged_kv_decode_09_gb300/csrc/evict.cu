@@ -4,21 +4,24 @@
 // Selecting.  A token's key is its weight as an unsigned integer of the same
 // order (NaN lowest; the protected first and recent tokens highest), so the B
 // kept tokens of a (row, KV head) are the B largest keys with ties to the
-// lowest index.  One CTA holds the keys in registers, token 512 k + tid as the
-// thread's k-th, and finds the B-th largest key T digit by digit from the top
-// (11, 11 and 10 bits): a histogram of the digit over the keys that match the
-// digits found so far, in four copies to spread its atomics, and the digit at
-// which the count from above reaches B.  Then token t is kept if its key
-// exceeds T, or equals T with fewer than (B - #greater) equals before it; its
-// place among the kept is
+// lowest index.  One CTA holds the keys in shared memory and finds the B-th
+// largest key T digit by digit from the top (11, 11 and 10 bits): a histogram of
+// the digit over the keys that match the digits found so far, in four copies to
+// spread its atomics, and the digit at which the count from above reaches B.
+// Then token t is kept if its key exceeds T, or equals T with fewer than
+// (B - #greater) equals before it; its place among the kept is
 //     #greater before t + min(#equal before t, B - #greater),
 // prefix sums of votes over groups of 32 tokens in order.  Rows longer than the
-// registers hold re-read their weights (from L2) in every pass.
+// shared memory holds re-read their weights (from L2) in every pass.  Each loop
+// runs once over the keys, from a cold instruction cache: they are loops of a
+// few instructions (with the keys in registers and the loops unrolled, the code
+// took 32 us to fetch, whatever the rows' lengths).
 //
 // Gathering.  The kept tokens go to fresh pages, so every copy is independent:
 // a CTA takes 64 kept tokens of a head and moves their K and V in 16-byte
 // pieces.  Bound by memory: the bytes are the kept K and V, read and written
 // once; the weights of the whole row are a few percent of them.
+#include <atomic>
 #include <cstdint>
 
 #include "chunk_device.cuh"
@@ -30,6 +33,7 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kCopies = 4;
+constexpr int kKeys = 47 * 1024;  // 188 KiB beside the histograms' 32
 constexpr int kGatherTokens = 64;
 constexpr int kGatherThreads = 256;
 
@@ -56,16 +60,14 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return (b >> 31) ? ~b : (b | 0x80000000u);
 }
 
-// KPT: keys of a thread, in registers; 0: re-read in every step.
-template <int KPT>
+// CACHED: the keys stay in shared memory (kKeys at most).
+template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
-  constexpr int kPasses = KPT > 0 ? KPT : 1;
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(16) uint32_t hist[kCopies][kBins];
   __shared__ uint32_t bin_sums[kSelWarps];
   __shared__ uint32_t pick[2];  // the digit, and the count above it
-  // votes of each (pass, warp): greater in the low half, equal in the high one
-  __shared__ uint32_t votes[kPasses * kSelWarps];
-  __shared__ unsigned long long scan_sums[kSelWarps];
+  __shared__ uint2 votes[kSelWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seg = blockIdx.x;  // (row, KV head)
   const int i = seg / a.pool.n_kv, h = seg - i * a.pool.n_kv;
@@ -81,18 +83,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     return;
   }
   const int recent = min(a.recent, B), first = min(a.first, B - recent);
-  const int passes = (L + kSelThreads - 1) / kSelThreads;
-  auto key_at = [&](int t, float x) { return t < first || t >= L - recent ? 0xFFFFFFFFu : key_of(x); };
-  auto fetch = [&](int t) { return key_at(t, __ldg(mass + t)); };
-  uint32_t key[kPasses];
-  if constexpr (KPT > 0) {
-    // every load first: the keys' arithmetic between them would wait for each
+  auto fetch = [&](int t) {
+    const float x = __ldg(mass + t);
+    return t < first || t >= L - recent ? 0xFFFFFFFFu : key_of(x);
+  };
+  auto key = [&](int t) { return CACHED ? keys[t] : fetch(t); };
+  if constexpr (CACHED) {
+#pragma unroll 1
+    for (int t0 = 0; t0 < L; t0 += 8 * kSelThreads) {  // eight loads in flight
+      float x[8];
 #pragma unroll
-    for (int k = 0; k < KPT; ++k)
-      if (k < passes) key[k] = __float_as_uint(__ldg(mass + min(k * kSelThreads + tid, L - 1)));
+      for (int u = 0; u < 8; ++u) x[u] = __ldg(mass + min(t0 + u * kSelThreads + tid, L - 1));
 #pragma unroll
-    for (int k = 0; k < KPT; ++k)
-      if (k < passes) key[k] = key_at(k * kSelThreads + tid, __uint_as_float(key[k]));
+      for (int u = 0; u < 8; ++u) {
+        const int t = t0 + u * kSelThreads + tid;
+        if (t < L) keys[t] = t < first || t >= L - recent ? 0xFFFFFFFFu : key_of(x[u]);
+      }
+    }
   }
   uint32_t T = 0, mask = 0;  // the digits of T found so far
   int want = B;              // how many of the keys that match them are kept
@@ -100,19 +107,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t digit = pass == 2 ? 1023u : 2047u;
+#pragma unroll 1
     for (int e = tid; e < kCopies * kBins / 4; e += kSelThreads)
       reinterpret_cast<uint4*>(hist)[e] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     uint32_t* mine = hist[warp % kCopies];
-    auto count = [&](int t, uint32_t x) {
-      if (t < L && (x & mask) == T) atomicAdd(&mine[(x >> shift) & digit], 1u);
-    };
-    if constexpr (KPT > 0) {
-#pragma unroll
-      for (int k = 0; k < KPT; ++k)
-        if (k < passes) count(k * kSelThreads + tid, key[k]);
-    } else {
-      for (int t = tid; t < L; t += kSelThreads) count(t, fetch(t));
+#pragma unroll 4
+    for (int t = tid; t < L; t += kSelThreads) {
+      const uint32_t x = key(t);
+      if ((x & mask) == T) atomicAdd(&mine[(x >> shift) & digit], 1u);
     }
     __syncthreads();
     // a thread's bins, from the top: 4 consecutive ones
@@ -151,80 +154,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     mask |= digit << shift;
     want -= static_cast<int>(pick[1]);
   }
+  // each warp takes a contiguous part of the tokens, in groups of 32
+  const int groups = (L + 31) / 32, per = (groups + kSelWarps - 1) / kSelWarps;
+  const int w0 = min(L, warp * per * 32), w1 = min(L, w0 + per * 32);
+  uint32_t gt = 0, eq = 0;
+#pragma unroll 4
+  for (int t0 = w0; t0 < w1; t0 += 32) {
+    const int t = t0 + lane;
+    const uint32_t x = t < w1 ? key(t) : 0u;
+    gt += __popc(__ballot_sync(kFull, t < w1 && x > T));
+    eq += __popc(__ballot_sync(kFull, t < w1 && x == T));
+  }
+  if (lane == 0) votes[warp] = make_uint2(gt, eq);
+  __syncthreads();
+  const uint2 v = lane < warp ? votes[lane & (kSelWarps - 1)] : make_uint2(0u, 0u);
+  gt = __reduce_add_sync(kFull, v.x);
+  eq = __reduce_add_sync(kFull, v.y);
   const unsigned below = (1u << lane) - 1u;
-  // token t of key x, with g greater and e equal keys before it
-  auto place = [&](int t, uint32_t x, uint32_t g, uint32_t e) {
-    if (t < L && (x > T || (x == T && e < static_cast<uint32_t>(want)))) {
-      keep[g + min(e, static_cast<uint32_t>(want))] = t;
-    }
-  };
-  if constexpr (KPT > 0) {
-#pragma unroll
-    for (int k = 0; k < KPT; ++k)
-      if (k < passes) {
-        const bool in = k * kSelThreads + tid < L;
-        const int g = __popc(__ballot_sync(kFull, in && key[k] > T)), e = __popc(__ballot_sync(kFull, in && key[k] == T));
-        if (lane == 0) votes[k * kSelWarps + warp] = static_cast<uint32_t>(g) | (static_cast<uint32_t>(e) << 16);
-      }
-    __syncthreads();
-    // exclusive prefix sums of the votes in order, a thread a few consecutive ones
-    constexpr int kPer = (KPT * kSelWarps + kSelThreads - 1) / kSelThreads;
-    unsigned long long mine[kPer], sum = 0;
-    const int n = passes * kSelWarps;
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int at = tid * kPer + u;
-      const uint32_t v = at < n ? votes[at] : 0u;
-      mine[u] = (v & 0xFFFFu) | (static_cast<unsigned long long>(v >> 16) << 32);
-      sum += mine[u];
-    }
-    unsigned long long run = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long u = __shfl_up_sync(kFull, run, o);
-      if (lane >= o) run += u;
-    }
-    if (lane == 31) scan_sums[warp] = run;
-    __syncthreads();
-    unsigned long long pre = run - sum;
-    {
-      unsigned long long w = lane < warp ? scan_sums[lane & (kSelWarps - 1)] : 0ull;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(kFull, w, o);
-      pre += w;
-    }
-    uint2* before = reinterpret_cast<uint2*>(hist);  // the histograms are done with
-    static_assert(KPT * kSelWarps * sizeof(uint2) <= sizeof(hist), "");
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int at = tid * kPer + u;
-      if (at < n) before[at] = make_uint2(static_cast<uint32_t>(pre), static_cast<uint32_t>(pre >> 32));
-      pre += mine[u];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < KPT; ++k)
-      if (k < passes) {
-        const int t = k * kSelThreads + tid;
-        const uint2 b = before[k * kSelWarps + warp];
-        const unsigned mg = __ballot_sync(kFull, t < L && key[k] > T), me = __ballot_sync(kFull, t < L && key[k] == T);
-        place(t, key[k], b.x + __popc(mg & below), b.y + __popc(me & below));
-      }
-  } else {
-    uint32_t gt = 0, eq = 0;  // greater and equal keys in the passes before
-    for (int k = 0; k < passes; ++k) {
-      const int t = k * kSelThreads + tid;
-      const uint32_t x = t < L ? fetch(t) : 0u;
-      const unsigned mg = __ballot_sync(kFull, t < L && x > T), me = __ballot_sync(kFull, t < L && x == T);
-      if (lane == 0) votes[warp] = static_cast<uint32_t>(__popc(mg)) | (static_cast<uint32_t>(__popc(me)) << 16);
-      __syncthreads();
-      const uint32_t v = lane < kSelWarps ? votes[lane] : 0u;
-      const uint32_t all = __reduce_add_sync(kFull, v), pre = __reduce_add_sync(kFull, lane < warp ? v : 0u);
-      place(t, x, gt + (pre & 0xFFFFu) + __popc(mg & below), eq + (pre >> 16) + __popc(me & below));
-      gt += all & 0xFFFFu;
-      eq += all >> 16;
-      __syncthreads();
-    }
+#pragma unroll 4
+  for (int t0 = w0; t0 < w1; t0 += 32) {
+    const int t = t0 + lane;
+    const uint32_t x = t < w1 ? key(t) : 0u;
+    const bool is_gt = t < w1 && x > T, is_eq = t < w1 && x == T;
+    const unsigned mg = __ballot_sync(kFull, is_gt), me = __ballot_sync(kFull, is_eq);
+    const uint32_t g = gt + __popc(mg & below), e = eq + __popc(me & below);
+    if (is_gt || (is_eq && e < static_cast<uint32_t>(want))) keep[g + min(e, static_cast<uint32_t>(want))] = t;
+    gt += __popc(mg);
+    eq += __popc(me);
   }
 }
 
@@ -290,18 +246,31 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __gr
   }
 }
 
-template <int KPT>
-cudaError_t launch_select(const EvictArgs& a, cudaStream_t st) {
+template <bool CACHED>
+cudaError_t launch_select(const EvictArgs& a, size_t smem, cudaStream_t st) {
+  if (smem > 8192) {  // above the default limit with the static arrays
+    static std::atomic<int> granted[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !granted[dev].load(std::memory_order_relaxed)) {
+      e = cudaFuncSetAttribute(evict_select_kernel<CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kKeys * static_cast<int>(sizeof(uint32_t)));
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) granted[dev].store(1, std::memory_order_relaxed);
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.num_rows) * a.pool.n_kv);
   cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel<CACHED>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -326,13 +295,12 @@ cudaError_t launch_gather(const EvictArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
-  // The keys of a thread, by the longest row the tables allow.
+  // Shared memory for the keys of the longest row the tables allow.
   const long long cap = a.mass_stride < static_cast<long long>(a.bt_stride) * kPage
                             ? a.mass_stride
                             : static_cast<long long>(a.bt_stride) * kPage;
-  cudaError_t e = cap <= 8 * kSelThreads    ? launch_select<8>(a, st)
-                  : cap <= 64 * kSelThreads ? launch_select<64>(a, st)
-                                            : launch_select<0>(a, st);
+  cudaError_t e = cap <= kKeys ? launch_select<true>(a, static_cast<size_t>(cap) * sizeof(uint32_t), st)
+                               : launch_select<false>(a, 0, st);
   if (e != cudaSuccess) return e;
   if (a.pool.dtype == PKV_KV_F16 || a.pool.dtype == PKV_KV_BF16) return launch_gather<PKV_KV_F16>(a, st);
   if (a.pool.dtype == PKV_KV_F32) return launch_gather<PKV_KV_F32>(a, st);
