@@ -29,6 +29,7 @@
 #include "chunk_device.cuh"
 #include "chunk_plan.cuh"
 #include "q8_tiles.cuh"
+#include "score32.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -128,7 +129,8 @@ __device__ __forceinline__ float* slot_sums(const MassArgs& a, int slot) {
 template <int DT>
 constexpr int kMassThreads = DT == PKV_KV_Q8_0 ? 512 : 384;
 
-template <int DT, bool GEN>
+// GEN: 0 plain scores; 1 capped; 2 with a distance bias, capped or not.
+template <int DT, int GEN>
 __global__ void __launch_bounds__(kMassThreads<DT>, 1)
     attention_mass_kernel(const __grid_constant__ MassArgs a, const __grid_constant__ TileMaps maps,
                           const __grid_constant__ CUtensorMap qmap) {
@@ -470,8 +472,9 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
     const int m = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const float c1 = a.sc.scale * kLog2e;
-    const float z2 = a.sc.softcap > 0.0f ? 2.0f * kLog2e * a.sc.scale / a.sc.softcap : 0.0f;
+    const float cap_k = a.sc.softcap > 0.0f ? a.sc.scale / a.sc.softcap : 0.0f;
     const float cap2 = a.sc.softcap * kLog2e;
+    const NearCap cap(cap_k, cap2);
     const int lg = G == 4 ? 2 : G == 2 ? 1 : 0;
     int gq = 0;
     uint32_t used = 0;
@@ -489,8 +492,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
       const long long jend = a.pool.window > 0 ? static_cast<long long>(t) + a.pool.window - past : d.nq;
       const int jhi = static_cast<int>(max(0ll, min(static_cast<long long>(d.nq), jend)));
       float slope2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (GEN) {
-        if (a.sc.slopes)
+      if constexpr (GEN == 2) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) slope2[e] = __ldg(a.sc.slopes + d.h * G + (e & (G - 1))) * kLog2e;
       }
@@ -515,26 +517,49 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
           // into pieces too short to hide each other's latency (3500 cycles a
           // block instead of 1400).
           auto weigh = [&](float (&v)[32], int q) {
-            if constexpr (GEN) {
-              const int dist0 = past + j - t;
+            float2 mul = make_float2(c1, c1);
+            float cq[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // GEN 1: the factor is q(v^2)
+            if constexpr (GEN == 1) {
+              if (__builtin_expect(cap.beyond(v), 0)) {
+                cap32(v, tS + 32 * q, cap_k, cap2);
+                cq[0] = 1.0f;
+              } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float y;
-                if (a.sc.softcap > 0.0f)
-                  y = cap2 - __fdividef(2.0f * cap2, 1.0f + tc::ex2(v[e] * z2));
-                else
-                  y = v[e] * c1;
-                v[e] = fmaf(-slope2[e & 3], fabsf(static_cast<float>(dist0 + ((32 * q + e) >> lg))), y);
+                for (int e = 0; e < 4; ++e) cq[e] = cap.q[e];
               }
             }
-            const float2 mul = make_float2(GEN ? 1.0f : c1, GEN ? 1.0f : c1);
+            if constexpr (GEN == 2) {
+              if (a.sc.softcap > 0.0f) {
+                cap32(v, tS + 32 * q, cap_k, cap2);
+                mul = make_float2(1.0f, 1.0f);
+              }
+            }
+            if constexpr (GEN == 2) {
+              const float dist0 = static_cast<float>(past + j - t + ((32 * q) >> lg));  // P - t of the first column
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float step = lg == 2 ? static_cast<float>(e >> 2) : lg == 1 ? static_cast<float>(e >> 1) : static_cast<float>(e);
+                v[e] = fmaf(-slope2[e & 3], fabsf(dist0 + step), v[e] * mul.x);
+              }
+              mul = make_float2(1.0f, 1.0f);
+            }
             const float4* lse4 = reinterpret_cast<const float4*>(&tail.lse2[s][32 * q]);
             float2 y[16];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float4 l = lse4[e];
-              y[2 * e] = tc::fma2(make_float2(v[4 * e], v[4 * e + 1]), mul, make_float2(l.x, l.y));
-              y[2 * e + 1] = tc::fma2(make_float2(v[4 * e + 2], v[4 * e + 3]), mul, make_float2(l.z, l.w));
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float2 x = make_float2(v[4 * e + 2 * h], v[4 * e + 2 * h + 1]);
+                float2 f = mul;
+                if constexpr (GEN == 1) {
+                  const float2 xx = tc::fma2(x, x, make_float2(0.0f, 0.0f));
+                  f = tc::fma2(xx, make_float2(cq[3], cq[3]), make_float2(cq[2], cq[2]));
+                  f = tc::fma2(xx, f, make_float2(cq[1], cq[1]));
+                  f = tc::fma2(xx, f, make_float2(cq[0], cq[0]));
+                }
+                y[2 * e + h] = tc::fma2(x, f, h ? make_float2(l.z, l.w) : make_float2(l.x, l.y));
+              }
             }
             if (!fast) {
 #pragma unroll
@@ -548,23 +573,36 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[e & 3] = tc::add2(acc[e & 3], make_float2(tc::ex2(y[e].x), tc::ex2(y[e].y)));
           };
-          // one load from tensor memory ahead of the arithmetic
-          float v0[32], v1[32];
-          tc::ld32(tS, v0);
-          tc::wait_ld();
-          tc::ld32(tS + 32, v1);
-          weigh(v0, 0);
-          tc::wait_ld();
-          tc::ld32(tS + 64, v0);
-          weigh(v1, 1);
-          tc::wait_ld();
-          tc::ld32(tS + 96, v1);
-          weigh(v0, 2);
-          tc::wait_ld();
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBSFree + 2 * m + (used & 1)));
-          weigh(v1, 3);
+          auto release = [&] {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBSFree + 2 * m + (used & 1)));
+          };
+          if constexpr (GEN != 0) {  // one copy of the longer code
+            float v[32];
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              tc::ld32(tS + 32 * q, v);
+              tc::wait_ld();
+              weigh(v, q);
+            }
+            release();
+          } else {  // one load from tensor memory ahead of the arithmetic
+            float v0[32], v1[32];
+            tc::ld32(tS, v0);
+            tc::wait_ld();
+            tc::ld32(tS + 32, v1);
+            weigh(v0, 0);
+            tc::wait_ld();
+            tc::ld32(tS + 64, v0);
+            weigh(v1, 1);
+            tc::wait_ld();
+            tc::ld32(tS + 96, v1);
+            weigh(v0, 2);
+            tc::wait_ld();
+            release();
+            weigh(v1, 3);
+          }
           ++used;
           const float2 a2 = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
           // compensated: a tile may see hundreds of blocks
@@ -619,7 +657,7 @@ __global__ void __launch_bounds__(kMassTok) mass_merge_kernel(const __grid_const
   a.mass_out[at] = (a.mass_in && t < me.L - me.n ? a.mass_in[at] : 0.0f) + sum;
 }
 
-template <int DT, bool GEN>
+template <int DT, int GEN>
 cudaError_t launch_mass_t(const MassArgs& a, const TileMaps& maps, const CUtensorMap& qmap, cudaStream_t st) {
   static std::atomic<int> granted[64];
   int dev = 0;
@@ -653,6 +691,13 @@ cudaError_t launch_mass_t(const MassArgs& a, const TileMaps& maps, const CUtenso
   return cudaGetLastError();
 }
 
+template <int DT>
+cudaError_t launch_mass_g(const MassArgs& a, const TileMaps& maps, const CUtensorMap& qmap, cudaStream_t st) {
+  if (a.sc.slopes) return launch_mass_t<DT, 2>(a, maps, qmap, st);
+  if (a.sc.softcap > 0.0f) return launch_mass_t<DT, 1>(a, maps, qmap, st);
+  return launch_mass_t<DT, 0>(a, maps, qmap, st);
+}
+
 }  // namespace
 
 size_t attention_mass_workspace(int chunks) {
@@ -665,15 +710,9 @@ cudaError_t launch_attention_mass(const MassArgs& a, const TileMaps& maps, cudaS
   cudaError_t e = encode_query_map(&qmap, a.pool.dtype == PKV_KV_BF16, a.q, a.q_stride, a.n_q, G,
                                    a.rows.total_tokens, 128 / G);
   if (e != cudaSuccess) return e;
-  const bool gen = a.sc.softcap > 0.0f || a.sc.slopes != nullptr;
-  if (a.pool.dtype == PKV_KV_F16)
-    return gen ? launch_mass_t<PKV_KV_F16, true>(a, maps, qmap, st)
-               : launch_mass_t<PKV_KV_F16, false>(a, maps, qmap, st);
-  if (a.pool.dtype == PKV_KV_BF16)
-    return gen ? launch_mass_t<PKV_KV_BF16, true>(a, maps, qmap, st)
-               : launch_mass_t<PKV_KV_BF16, false>(a, maps, qmap, st);
-  return gen ? launch_mass_t<PKV_KV_Q8_0, true>(a, maps, qmap, st)
-             : launch_mass_t<PKV_KV_Q8_0, false>(a, maps, qmap, st);
+  if (a.pool.dtype == PKV_KV_F16) return launch_mass_g<PKV_KV_F16>(a, maps, qmap, st);
+  if (a.pool.dtype == PKV_KV_BF16) return launch_mass_g<PKV_KV_BF16>(a, maps, qmap, st);
+  return launch_mass_g<PKV_KV_Q8_0>(a, maps, qmap, st);
 }
 
 }  // namespace pkv

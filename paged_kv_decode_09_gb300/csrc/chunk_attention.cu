@@ -52,6 +52,7 @@
 #include "chunk_device.cuh"
 #include "chunk_plan.cuh"
 #include "q8_tiles.cuh"
+#include "score32.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -277,8 +278,9 @@ __device__ __forceinline__ void fill_skipped(const ChunkAttnArgs& a) {
   }
 }
 
-// GEN: scores with a cap, a bias, or a scale that is not positive.
-template <int DT, bool GEN>
+// GEN: 0 plain scores; 1 capped (at most 1e9); 2 with a distance bias, capped
+// or not, with a scale that is not positive, or a higher cap.
+template <int DT, int GEN>
 __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkAttnArgs a, const __grid_constant__ TileMaps maps,
                            const __grid_constant__ CUtensorMap qmap) {
@@ -363,15 +365,19 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   const bool stalled = test_stall(bar(kBStall), a.pool.test_stall_ns, ctl, a.pool.status);
 
   auto wait = [&](int b, uint32_t parity) { return tc::warp_wait<!kQ8>(bar(b), parity & 1u, ctl, a.pool.status); };
+  // block b of a piece: with a bias from the last one back, where the scores
+  // are highest (a steep bias would raise the maximum with every group of 32
+  // columns otherwise: 1100 us instead of 474 for a prompt of 8191 tokens)
+  auto block = [](int kb, int nb, int b) { return GEN == 2 ? kb + nb - 1 - b : kb + b; };
   auto pages_of = [&](const Piece& p, int b, int& lo, int& hi) {  // pages of a block that are read
-    const int first = (p.kb + b) * kPages;
+    const int first = block(p.kb, p.nb, b) * kPages;
     lo = max(first, p.t_lo / kPage);
     hi = min(first + kPages, (p.t_hi + kPage - 1) / kPage);
   };
   // V blocks that warp 11 sees: with tokens outside [t_lo, t_hi) in their
   // pages (zeroed), or masked for part of the tile (searched)
   auto mended = [&](const Piece& p, int b) {
-    const int t0 = (p.kb + b) * N;
+    const int t0 = block(p.kb, p.nb, b) * N;
     return t0 < p.full_lo || t0 + N > p.full_hi;
   };
 
@@ -389,7 +395,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       if (d.last) break;
       for (int b = 0; b < d.nb && ok; ++b) {
         const bool mend = mended(d, b);
-        const int t0 = (d.kb + b) * N;
+        const int t0 = block(d.kb, d.nb, b) * N;
 #pragma unroll
         for (int v = 0; v < 2; ++v, ++gs) {
           const int rs = gs % kRaws, s = gs % kS;
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       auto entry = [&](int b) {  // lane e: page e of the block, -1 where it is not read
         int lo, hi;
         pages_of(d, b, lo, hi);
-        const int q = (d.kb + b) * kPages + lane;
+        const int q = block(d.kb, d.nb, b) * kPages + lane;
         return lane < kPages && q >= lo && q < hi ? __ldg(bt + q) : -1;
       };
       int next = entry(0);
@@ -592,7 +598,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         if (b + 1 < d.nb) next = entry(b + 1);
         int lo, hi;
         pages_of(d, b, lo, hi);
-        const int q = (d.kb + b) * kPages + lane;
+        const int q = block(d.kb, d.nb, b) * kPages + lane;
         const bool mine = lane < kPages && q >= lo && q < hi;
         if (mine && (pg < 0 || pg >= a.pool.num_pages)) {
           record_status(a.pool.status, PKV_DEV_BAD_PAGE);
@@ -644,7 +650,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         }
         landed ^= 1u << s;
         uint8_t* v = smem + kRing + s * kHalf;
-        const int t0 = (d.kb + b) * N;
+        const int t0 = block(d.kb, d.nb, b) * N;
         int lo, hi;
         pages_of(d, b, lo, hi);
         // tokens of the pages read that no query of the tile attends to
@@ -791,7 +797,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         if (two) issue_s(1, s);
         tc::commit(bar(kBEmpty + s), lead);
         if (b + 1 == nb) tc::commit(bar(kBQEmpty), lead);
-        const int first = (kb + b) * kPages;
+        const int first = block(kb, nb, b) * kPages;
         const int lo = max(first, t_lo / kPage), hi = min(first + kPages, (t_hi + kPage - 1) / kPage);
         v.s = (gs + 1) % kS;
         v.lo = lo & (kPages - 1);
@@ -828,7 +834,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     uint32_t blocks = 0, pieces = 0;
     bool ok = !stalled;
     const float c1 = a.sc.scale * kLog2e;
-    const float inv_cap = a.sc.softcap > 0.0f ? a.sc.scale / a.sc.softcap : 0.0f, cap2 = a.sc.softcap * kLog2e;
+    const float cap_k = a.sc.softcap > 0.0f ? a.sc.scale / a.sc.softcap : 0.0f, cap2 = a.sc.softcap * kLog2e;
+    const NearCap cap(cap_k, cap2);
     for (int p = 0; ok; ++p) {
       const int x = p % kDescs;
       if (!wait(kBDesc + x, p / kDescs)) break;
@@ -842,12 +849,17 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         const int lo = valid ? seen_from(P, a.pool.window) : 0;
         const int hi = valid ? seen_to(P, d.L, d.F) : 0x7FFFFFFF;
         float slope2 = 0.0f;
-        if constexpr (GEN) slope2 = a.sc.slopes ? __ldg(a.sc.slopes + g) * kLog2e : 0.0f;
-        float mx = -INFINITY;  // the maximum in force, base 2
+        bool behind = true;
+        if constexpr (GEN == 2) {
+          slope2 = a.sc.slopes ? __ldg(a.sc.slopes + g) * kLog2e : 0.0f;
+          behind = __all_sync(kFull, !valid || hi <= P + 1);
+        }
+        constexpr float kMasked = GEN == 1 ? -1e15f : -INFINITY, kNone = GEN == 1 ? -1e14f : -INFINITY;
+        float mx = kNone;      // the maximum in force, base 2
         float sub = 0.0f;      // what is taken off the scores: mx - shift (0 before a first score)
         float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         for (int b = 0; b < d.nb; ++b, ++blocks) {
-          const int t0 = (d.kb + b) * N;
+          const int t0 = block(d.kb, d.nb, b) * N;
           const bool fast = __all_sync(kFull, t0 >= lo && t0 + N <= hi);
           if (!(ok = wait(kBS + m, blocks))) break;
           tc::fence_after();
@@ -865,10 +877,10 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
             // exponentials.
             constexpr int kGroups = N / 32;
             auto raise_to = [&](float bm, int group) {
-              const bool raise = bm > mx + 8.0f;  // also from -inf
+              const bool raise = bm > mx + 8.0f;  // also from none
               float al = 1.0f;
               if (raise) {
-                const float to = mx == -INFINITY ? bm : mx + ceilf(bm - mx);
+                const float to = mx == kNone ? bm : mx + ceilf(bm - mx);
                 al = tc::ex2(mx - to);  // a power of two, or 0
                 mx = to;
                 sub = to - F::kShift;
@@ -882,43 +894,82 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                 else rescale<DT>(tS, tO, group, b > 0, al);
               }
             };
-            const float2 mul = make_float2(GEN ? 1.0f : c1, GEN ? 1.0f : c1);
+            // With a bias the scores get slope (t - P) with the exponentials'
+            // subtraction, -slope (t - P) for tokens after the query; a cap
+            // is their factor there, q(v^2) instead of c1: there a masked
+            // score is one far below the cap's, whose square is finite.
             auto weigh = [&](float (&v)[32], int group) {
-              if constexpr (GEN) {
-                const float dist0 = static_cast<float>(P - t0 - 32 * group);
+              float2 mul = make_float2(c1, c1);
+              float bias = 0.0f, step = 0.0f;  // of the group's first column; per column
+              float cq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              if constexpr (GEN == 1) {
+                if (__builtin_expect(cap.beyond(v, fast), 0)) {
+                  cap32(v, tS + 32 * group, cap_k, cap2);
+                  cq[0] = 1.0f;
+                } else {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  float y;
-                  if (a.sc.softcap > 0.0f) {
-                    // tanh z = 1 - 2 / (1 + e^2z)
-                    y = cap2 - __fdividef(2.0f * cap2, 1.0f + tc::ex2(v[e] * (2.0f * kLog2e * inv_cap)));
-                  } else {
-                    y = v[e] * c1;
-                  }
-                  v[e] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(e)), y);
+                  for (int e = 0; e < 4; ++e) cq[e] = cap.q[e];
+                }
+              }
+              if constexpr (GEN == 2) {
+                if (a.sc.softcap > 0.0f) {
+                  cap32(v, tS + 32 * group, cap_k, cap2);
+                  mul = make_float2(1.0f, 1.0f);
+                } else if (!(c1 > 0.0f)) {  // the mask's -inf has to stay one
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] *= c1;
+                  mul = make_float2(1.0f, 1.0f);
+                }
+              }
+              if constexpr (GEN == 2) {
+                const float dist0 = static_cast<float>(t0 + 32 * group - P);  // t - P of the first column
+                const bool before = behind || dist0 <= -31.0f, after = dist0 >= 0.0f;
+                if (__builtin_expect(__any_sync(kFull, valid && !before && !after), 0)) {  // seen on both sides
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] = fmaf(-slope2, fabsf(dist0 + static_cast<float>(e)), v[e] * mul.x);
+                  mul = make_float2(1.0f, 1.0f);
+                } else {
+                  step = before ? slope2 : -slope2;
+                  bias = step * dist0;
                 }
               }
               if (__builtin_expect(!fast, 0)) {
                 const int from = lo - t0 - 32 * group, to = hi - t0 - 32 * group;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = e >= from && e < to ? v[e] : -INFINITY;
+                for (int e = 0; e < 32; ++e) v[e] = e >= from && e < to ? v[e] : kMasked;
               }
               uint32_t w[16];
               float2 lb[2];
 #pragma unroll 1
               while (true) {
-                const float2 off = make_float2(-sub, -sub);
+                float2 off[4];  // of columns 2u, 2u + 1 and every eighth after
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  off[u] = make_float2(bias - sub, bias - sub);
+                  if constexpr (GEN == 2) off[u] = make_float2(fmaf(step, 2.0f * u, off[u].x), fmaf(step, 2.0f * u + 1.0f, off[u].y));
+                }
+                const float2 next = make_float2(8.0f * step, 8.0f * step);
                 float x0 = -INFINITY, x1 = -INFINITY;
                 lb[0] = lb[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int u = 0; u < 16; ++u) {
-                  const float2 y = tc::fma2(make_float2(v[2 * u], v[2 * u + 1]), mul, off);
-                  if (u & 1) x1 = tc::max3(x1, v[2 * u], v[2 * u + 1]); else x0 = tc::max3(x0, v[2 * u], v[2 * u + 1]);
+                  const float2 x = make_float2(v[2 * u], v[2 * u + 1]);
+                  float2 f = mul;
+                  if constexpr (GEN == 1) {
+                    const float2 xx = tc::fma2(x, x, make_float2(0.0f, 0.0f));
+                    f = tc::fma2(xx, make_float2(cq[3], cq[3]), make_float2(cq[2], cq[2]));
+                    f = tc::fma2(xx, f, make_float2(cq[1], cq[1]));
+                    f = tc::fma2(xx, f, make_float2(cq[0], cq[0]));
+                  }
+                  const float2 y = tc::fma2(x, f, off[u & 3]);
+                  if constexpr (GEN == 2) off[u & 3] = tc::add2(off[u & 3], next);
+                  const float2 z = GEN != 0 ? y : x;
+                  if (u & 1) x1 = tc::max3(x1, z.x, z.y); else x0 = tc::max3(x0, z.x, z.y);
                   const float2 pr = make_float2(tc::ex2(y.x), tc::ex2(y.y));
                   lb[u & 1] = tc::add2(lb[u & 1], pr);
                   w[u] = F::pack(pr.x, pr.y);
                 }
-                const float bm = fmaxf(x0, x1) * (GEN ? 1.0f : c1);
+                const float bm = GEN != 0 ? fmaxf(x0, x1) + sub : fmaxf(x0, x1) * c1;
                 if (__builtin_expect(!__any_sync(kFull, bm > mx + 8.0f), 1)) break;
                 raise_to(bm, group);
               }
@@ -939,15 +990,24 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                 for (int e = 0; e < 32; ++e) v[e] += more[e];
               }
             };
-            load(v0, 0);
+            if constexpr (GEN != 0) {  // one copy of the longer code
 #pragma unroll 1
-            for (int group = 0; group < kGroups; group += 2) {
-              arrived(v0);
-              load(v1, group + 1);
-              weigh(v0, group);
-              arrived(v1);
-              if (group + 2 < kGroups) load(v0, group + 2);
-              weigh(v1, group + 1);
+              for (int group = 0; group < kGroups; ++group) {
+                load(v0, group);
+                arrived(v0);
+                weigh(v0, group);
+              }
+            } else {
+              load(v0, 0);
+#pragma unroll 1
+              for (int group = 0; group < kGroups; group += 2) {
+                arrived(v0);
+                load(v1, group + 1);
+                weigh(v0, group);
+                arrived(v1);
+                if (group + 2 < kGroups) load(v0, group + 2);
+                weigh(v1, group + 1);
+              }
             }
             tc::wait_st();
           }
@@ -1117,7 +1177,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
 }
 
 // ------------------------------------------------------------- launchers ----
-template <int DT, bool GEN>
+template <int DT, int GEN>
 cudaError_t launch_attention_t(const ChunkAttnArgs& a, const TileMaps& maps, const CUtensorMap& qmap, cudaStream_t st) {
   static std::atomic<int> granted[64];
   int dev = 0;
@@ -1151,6 +1211,13 @@ cudaError_t launch_attention_t(const ChunkAttnArgs& a, const TileMaps& maps, con
   return cudaGetLastError();
 }
 
+template <int DT>
+cudaError_t launch_attention_g(const ChunkAttnArgs& a, const TileMaps& maps, const CUtensorMap& qmap, cudaStream_t st) {
+  if (a.sc.slopes || !(a.sc.scale > 0.0f) || a.sc.softcap > 1e9f) return launch_attention_t<DT, 2>(a, maps, qmap, st);
+  if (a.sc.softcap > 0.0f) return launch_attention_t<DT, 1>(a, maps, qmap, st);
+  return launch_attention_t<DT, 0>(a, maps, qmap, st);
+}
+
 }  // namespace
 
 size_t chunk_attention_workspace(int n_q, int n_kv, int chunks) {
@@ -1164,15 +1231,9 @@ cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, const TileMaps& maps,
   cudaError_t e = encode_query_map(&qmap, a.pool.dtype == PKV_KV_BF16, a.q, a.q_stride, a.n_q, a.n_q / a.pool.n_kv,
                                    a.rows.total_tokens, 128 / (a.n_q / a.pool.n_kv));
   if (e != cudaSuccess) return e;
-  const bool gen = a.sc.softcap > 0.0f || a.sc.slopes != nullptr || !(a.sc.scale > 0.0f);
-  if (a.pool.dtype == PKV_KV_F16)
-    return gen ? launch_attention_t<PKV_KV_F16, true>(a, maps, qmap, st)
-               : launch_attention_t<PKV_KV_F16, false>(a, maps, qmap, st);
-  if (a.pool.dtype == PKV_KV_BF16)
-    return gen ? launch_attention_t<PKV_KV_BF16, true>(a, maps, qmap, st)
-               : launch_attention_t<PKV_KV_BF16, false>(a, maps, qmap, st);
-  return gen ? launch_attention_t<PKV_KV_Q8_0, true>(a, maps, qmap, st)
-             : launch_attention_t<PKV_KV_Q8_0, false>(a, maps, qmap, st);
+  if (a.pool.dtype == PKV_KV_F16) return launch_attention_g<PKV_KV_F16>(a, maps, qmap, st);
+  if (a.pool.dtype == PKV_KV_BF16) return launch_attention_g<PKV_KV_BF16>(a, maps, qmap, st);
+  return launch_attention_g<PKV_KV_Q8_0>(a, maps, qmap, st);
 }
 
 // The queries as a 4-D tensor {64 dims, heads, tokens, 2 halves of the dims},
