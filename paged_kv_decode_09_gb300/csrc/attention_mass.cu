@@ -112,7 +112,9 @@ struct TokenTiles {
     range(r, F, t, b0, b1);
     return b1 - b0;
   }
-  __device__ __forceinline__ int lead() const { return kTileCost; }
+  static constexpr int kMostWeight = 1;
+  __device__ __forceinline__ int weight(const RowInfo&, int) const { return 1; }
+  __device__ __forceinline__ int lead(int) const { return kTileCost; }
 };
 
 struct Rec {

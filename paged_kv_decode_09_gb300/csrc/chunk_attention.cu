@@ -12,7 +12,11 @@
 // block exceeds it by more than 8 (a factor of 256, which f16 and bf16 hold).
 // P_m overwrites S_m in tensor memory as 16-bit pairs: S_0, S_1, O_0 and O_1
 // take all 512 columns.  The halves alternate on the tensor cores: while one
-// is in its softmax, the other's products run.
+// is in its softmax, the other's products run.  A tile of up to 128 rows (a
+// token of a row, the end of a chunk) would leave half 1 idle and each block
+// waiting for the one before: there the halves hold the same rows and take the
+// blocks in turn, and half 0 joins the two states at the end (8 rows of one
+// token 28.5 -> 23.3 us).
 // q8_0 keys and values enter as two f16 parts, hi and lo (q8_tiles.cuh), two
 // products each.
 //
@@ -29,6 +33,8 @@
 //   sfull[m]          S_m computed (and every product issued before it)
 //   pready[m]         P_m written, S_m read
 //   ofull[m]          O_m of the piece complete
+//   half, joined      half 1's maximum and sum are in shared memory; half 0 has
+//                     read them and O_1
 // Every wait is bounded; a warp that gives up sets the abort flag, which ends
 // the other waits, and its copies and products are awaited before the CTA ends.
 //
@@ -65,6 +71,9 @@ template <int DT>
 constexpr int kAttnThreads = DT == PKV_KV_Q8_0 ? 512 : kPlanThreads;
 #ifndef PKV_CHUNK_TILE_COST
 #define PKV_CHUNK_TILE_COST 3
+#endif
+#ifndef PKV_CHUNK_SMALL_COST
+#define PKV_CHUNK_SMALL_COST 10
 #endif
 #ifndef PKV_CHUNK_SNAP
 #define PKV_CHUNK_SNAP 2
@@ -105,7 +114,9 @@ enum : int {
   kBQEmpty = kBQ + 2,
   kBDesc = kBQEmpty + 1,
   kBDescEmpty = kBDesc + kDescs,
-  kBDrain = kBDescEmpty + kDescs,
+  kBHalf = kBDescEmpty + kDescs,  // alternating halves: half 1's state handed over, half 0's epilogue over
+  kBJoined,
+  kBDrain,
   kBStall,
   kNumBars,
 };
@@ -128,6 +139,7 @@ struct Tail {
   int bad[kDescs];  // a masked V block of the piece holds a value that is not finite
   volatile int ctl[2];
   uint32_t tmem;
+  float2 half[kTileRows / 2];  // half 1's maximum and sum of each row
   Place bounds[2];
   PlanScratch scratch;
 };
@@ -159,7 +171,16 @@ struct QueryTiles {
     return g;
   }
   __device__ __forceinline__ int blocks(const RowInfo& r, int F, int t) const { return tile(r, F, t).nb; }
-  __device__ __forceinline__ int lead() const { return kTileCost<DT>; }
+  // Units: 4 a block, 2 in a tile of up to 128 rows (half the arithmetic); 12
+  // and 10 a tile.  A batch of two chunks and 30 single tokens takes 122 us, 142
+  // at 3 units for the smaller blocks, 156 at 4.  q8_0 has no turns to gain by.
+  static constexpr int kMostWeight = 4;
+  __device__ __forceinline__ int weight(const RowInfo& r, int t) const {
+    return DT == PKV_KV_Q8_0 || 2 * (r.n - t * QT) > QT ? 4 : 2;
+  }
+  __device__ __forceinline__ int lead(int weight) const {
+    return (weight == 4 ? 4 * PKV_CHUNK_TILE_COST : PKV_CHUNK_SMALL_COST) * (128 / kBlockTok<DT>);
+  }
 };
 
 // ------------------------------------------------------------ workspace ----
@@ -290,6 +311,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   constexpr int N = kBlockTok<DT>;                   // tokens of a block
   constexpr int kPages = N / kPage;                  // its pages
   constexpr uint32_t kPart = N * kD * 2;             // bytes of one part of it
+  // The halves take a smaller tile's blocks in turn (q8_0: no registers left)
+  constexpr bool kTurns = !kQ8;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   Tail& tail = *reinterpret_cast<Tail*>(smem + kTail);
@@ -310,7 +333,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     const int b = tid;
     int count = 1;
     if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = 4;
-    if (b >= kBP && b < kBO) count = 4;
+    if ((b >= kBP && b < kBO) || b == kBHalf || b == kBJoined) count = 4;
     if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT>;
     mbar_init(bar(b), count);
     fence_mbar_init();
@@ -716,8 +739,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                    v_lo = tc::desc_lo(sbase + kRing, 1024);
     // scores S_m of the K block in slot s (q8_0: 64 columns with the hi parts,
     // and 64 with the lo parts, which the softmax adds)
-    auto issue_s = [&](int m, int s) {
-      const uint32_t qd = q_lo + m * (kHalf >> 4), kd = k_lo + s * (kHalf >> 4);
+    auto issue_s = [&](int m, int s, int q) {
+      const uint32_t qd = q_lo + q * (kHalf >> 4), kd = k_lo + s * (kHalf >> 4);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
         tc::mma_ss<kHiQ, kHiKV>(tm + kTmemS + 128 * m, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
@@ -726,9 +749,9 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     };
     // the block whose values product is due
     struct {
-      int s, lo, n;          // V slot, first page in it, pages
+      int s, lo, n, m;       // V slot, first page in it, pages; the (first) half
       bool first, last, two;
-    } v{0, 0, 0, false, false, false};
+    } v{0, 0, 0, 0, false, false, false};
     bool due = false;
     uint32_t np[2] = {0, 0};  // blocks of P consumed per half
     int gs = 0;
@@ -757,6 +780,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       if (v.last) tc::commit(bar(kBO + m), lead);
       return true;
     };
+    auto finish_o = [&] { return (v.m == 1 || issue_o(0)) && (!(v.two || v.m == 1) || issue_o(1)); };
     uint32_t q1 = 0;
     for (int p = 0; ok; ++p) {
       const int x = p % kDescs;
@@ -769,32 +793,47 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       any = true;
       for (int b = 0; b < nb && ok; ++b) {
         // gs: the slot of this block's K; gs - 1 that of the due block's V.
-        // What lands early is waited for first: once P_m is there, its
-        // product and the next scores go out without another wait (a wait
-        // costs some 200 cycles even when there is nothing to wait for).
+        // What lands early is waited for first: once P_m is there, its product
+        // and the next scores go out without another wait.  The halves are
+        // constants everywhere: with a variable half the products' addresses
+        // are not uniform registers (438 us instead of 405 for the prompt).
         const int s = gs % kS;
         if (due && !(ok = wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kS))) break;
         if (b == 0) {
           // the piece before is finished while this one's queries land
           if (due) {
-            if (!(ok = issue_o(0) && (!v.two || issue_o(1)))) break;
+            if (!(ok = finish_o())) break;
             tc::commit(bar(kBEmpty + v.s), lead);
             due = false;
           }
           if (!(ok = wait(kBQ, p) && (!two || wait(kBQ + 1, q1)))) break;
         }
         if (!(ok = wait(kBFull + s, gs / kS))) break;
-        if (due) {
-          if (!(ok = issue_o(0))) break;
+        if (!kTurns || two) {
+          if (due) {
+            if (!(ok = issue_o(0))) break;
+          } else {
+            tc::fence_after();
+          }
+          issue_s(0, s, 0);
+          if (due) {
+            if (v.two && !(ok = issue_o(1))) break;
+            tc::commit(bar(kBEmpty + v.s), lead);
+          }
+          if (two) issue_s(1, s, 1);
         } else {
+          // the scores go out before the product of the block before, whose
+          // weights are still made
           tc::fence_after();
+          if (b & 1) {
+            issue_s(1, s, 0);
+            if (due && !(ok = issue_o(0))) break;
+          } else {
+            issue_s(0, s, 0);
+            if (due && !(ok = issue_o(1))) break;
+          }
+          if (due) tc::commit(bar(kBEmpty + v.s), lead);
         }
-        issue_s(0, s);
-        if (due) {
-          if (v.two && !(ok = issue_o(1))) break;
-          tc::commit(bar(kBEmpty + v.s), lead);
-        }
-        if (two) issue_s(1, s);
         tc::commit(bar(kBEmpty + s), lead);
         if (b + 1 == nb) tc::commit(bar(kBQEmpty), lead);
         const int first = block(kb, nb, b) * kPages;
@@ -802,8 +841,9 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         v.s = (gs + 1) % kS;
         v.lo = lo & (kPages - 1);
         v.n = hi - lo;
-        v.first = b == 0;
-        v.last = b + 1 == nb;
+        v.m = kTurns && !two ? b & 1 : 0;
+        v.first = b < (!kTurns || two ? 1 : 2);
+        v.last = b + (!kTurns || two ? 1 : 2) >= nb;
         v.two = two;
         due = true;
         gs += 2;
@@ -813,7 +853,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
       __syncwarp();
     }
-    if (ok && due && wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kS) && issue_o(0) && v.two) issue_o(1);
+    if (ok && due && wait(kBFull + v.s, static_cast<uint32_t>(gs - 1) / kS)) finish_o();
     // every product issued completes before the tensor memory is freed
     if (any) {
       const int zero = 0;
@@ -827,11 +867,10 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     // ------------------------------------------------------------ softmax ----
     if constexpr (kQ8) tc::more_registers<144>();
     const int m = warp >> 2, quarter = warp & 3;
-    const int r = 128 * m + 32 * quarter + lane;  // row of the tile
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    const uint32_t tS = tmem + lanes + kTmemS + 128 * m, tO = tmem + lanes + kTmemO + 128 * m;
-    const int jq = r / G;
-    uint32_t blocks = 0, pieces = 0;
+    const uint32_t tS = tmem + lanes + kTmemS + 128 * m, tO = tS + (kTmemO - kTmemS);
+    const int r_half = 32 * quarter + lane, jq_full = (r_half + 128 * m) / G;
+    uint32_t blocks = 0, pieces = 0, joins = 0;
     bool ok = !stalled;
     const float c1 = a.sc.scale * kLog2e;
     const float cap_k = a.sc.softcap > 0.0f ? a.sc.scale / a.sc.softcap : 0.0f, cap2 = a.sc.softcap * kLog2e;
@@ -842,7 +881,14 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       const Piece d = tail.piece[x];
       if (d.last) break;
       const bool two = d.nq * G > kTileRows / 2;
-      if (m == 0 || two) {
+      // A tile of up to 128 rows: the halves take its blocks in turn, so that
+      // one's scores are made while the other's go through the softmax.
+      const bool join = kTurns && !two && d.nb > 1;
+      bool begun = false;  // O holds an earlier block
+      const int r = kTurns && !two ? r_half : r_half + 128 * m;  // row of the tile
+      const int jq = kTurns ? r / G : jq_full;                   // its query
+      const int every = !kTurns || two ? 1 : 2;
+      if (m == 0 || two || join) {
         const bool valid = jq < d.nq;
         const bool any = __any_sync(kFull, valid);
         const int P = d.P0 + jq, g = d.h * G + r % G;
@@ -858,7 +904,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         float mx = kNone;      // the maximum in force, base 2
         float sub = 0.0f;      // what is taken off the scores: mx - shift (0 before a first score)
         float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        for (int b = 0; b < d.nb; ++b, ++blocks) {
+        for (int b = !kTurns || two ? 0 : m; b < d.nb; b += every, ++blocks, begun = true) {
           const int t0 = block(d.kb, d.nb, b) * N;
           const bool fast = __all_sync(kFull, t0 >= lo && t0 + N <= hi);
           if (!(ok = wait(kBS + m, blocks))) break;
@@ -889,9 +935,9 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
               // the block's weights so far, and O: the values products before
               // are complete, S was issued after them
               tc::wait_ld();
-              if (group > 0 || b > 0) {
+              if (group > 0 || (kTurns ? begun : b > 0)) {
                 if constexpr (kQ8) rescale_here<DT>(tS, tO, group, b > 0, al);  // no registers for a call
-                else rescale<DT>(tS, tO, group, b > 0, al);
+                else rescale<DT>(tS, tO, group, begun, al);
               }
             };
             // With a bias the scores get slope (t - P) with the exponentials'
@@ -1018,10 +1064,32 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         if (!ok || !(ok = wait(kBO + m, pieces))) break;
         ++pieces;
         tc::fence_after();
-        if (any) {
-          const float2 la = tc::add2(l2[0], l2[1]);
-          const float l = la.x + la.y;
+        const float2 la = tc::add2(l2[0], l2[1]);
+        float l = la.x + la.y;
+        float f0 = 1.0f, f1 = 0.0f;  // the halves' factors
+        if (join && m == 1) {  // O_1 is complete, and half 0 reads it
+          tail.half[32 * quarter + lane] = make_float2(sub, l);
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBHalf));
+          if (!(ok = wait(kBJoined, joins))) break;  // before the next piece's P_1
+          ++joins;
+        } else if (join) {
+          if (!(ok = wait(kBHalf, joins))) break;
+          ++joins;
+          tc::fence_after();
+          const float2 o = tail.half[32 * quarter + lane];
+          // a half without tokens of the row weighs nothing
+          const float top = !(o.y > 0.0f) ? sub : !(l > 0.0f) ? o.x : fmaxf(sub, o.x);
+          f0 = l == 0.0f ? 0.0f : tc::ex2(sub - top);
+          f1 = o.y == 0.0f ? 0.0f : tc::ex2(o.x - top);
+          l = fmaf(f0, l, f1 * o.y);
+          sub = top;
+        }
+        if (any && (two || m == 0)) {
           const float inv = d.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+          f0 *= inv;
+          f1 *= inv;
           const long long row = static_cast<long long>(d.tok + jq) * a.n_q + g;
           float watch = 0.0f;  // NaN once a value is not finite
 #pragma unroll 1
@@ -1030,10 +1098,16 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
             tc::ld32(tO + 32 * e, o);
             tc::wait_ld();
 #pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              o[u] *= inv;
-              watch = fmaf(o[u], 0.0f, watch);
+            for (int u = 0; u < 32; ++u) o[u] *= f0;
+            if (join) {
+              float o1[32];
+              tc::ld32(tO + 128 + 32 * e, o1);
+              tc::wait_ld();
+#pragma unroll
+              for (int u = 0; u < 32; ++u) o[u] = fmaf(f1, o1[u], o[u]);
             }
+#pragma unroll
+            for (int u = 0; u < 32; ++u) watch = fmaf(o[u], 0.0f, watch);
             if (valid) {
               if (d.slot >= 0) {
                 float4* acc = slot_acc(a, d.slot) + r;
@@ -1062,9 +1136,14 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
             while (again) {
               const int u = __ffs(again) - 1;
               again &= again - 1;
-              redo_row<DT>(a, d, 128 * m + 32 * quarter + u);
+              redo_row<DT>(a, d, r - lane + u);
             }
           }
+        }
+        if (join && m == 0) {
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBJoined));
         }
       }
       __syncwarp();

@@ -15,13 +15,15 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 // What a kernel tells the plan (Geo below):
 //   int tiles(const RowInfo&)                 tiles of a row
 //   int blocks(const RowInfo&, int F, int t)  blocks of its tile t
-//   lead()                                    units a tile costs besides its
-//                                             blocks, at least 1
-// F is prefix_lens[i], or 0 without.  A tile is lead() units, then one per block.
+//   weight(const RowInfo&, int t)             units of each of its blocks
+//   kMostWeight                               the largest weight
+//   lead(int weight)                          units a tile costs besides its
+//                                             blocks, at least kMostWeight
+// F is prefix_lens[i], or 0 without.
 
-// A place in the work: unit `off` of tile `tile` (counted over the batch; tile
-// t of row i) for KV head h; 0, or lead() + the block that comes next.  The end
-// of all work is {n_kv, 0, .., 0}.
+// A place in the work: tile `tile` (counted over the batch; tile t of row i)
+// for KV head h, and the block `off` that comes next.  The end of all work is
+// {n_kv, 0, .., 0}.
 struct Place {
   int h, tile, i, t, off;
 };
@@ -56,12 +58,16 @@ __device__ __forceinline__ T cta_scan(T x, T* tmp, T& total) {
 
 // The plan of the call, made by every CTA (all its threads, kPlanThreads or
 // more, call it; `tile_start` holds num_rows + 1 ints and may be reused afterwards).
-// The U units of the batch are cut into C = min(chunks, U) ranges, range k from
-// floor(k U / C); a boundary less than `snap` blocks from an end of its tile
+// The U units of the batch are cut into C = min(chunks, U / kMostWeight) ranges,
+// range k from floor(k U / C), so that no two boundaries fall on one block; a boundary less than `snap` blocks from an end of its tile
 // moves there, since a split tile costs a partial state and its merge.  Writes
 // the boundaries blockIdx.x and blockIdx.x + 1 to bounds[0], bounds[1], and
 // returns the number of tiles.  The threads share out the tiles in contiguous
 // runs, so that their work is the same whatever the rows' lengths.
+// The block that comes next at unit u of a tile.
+__device__ __forceinline__ int block_of(unsigned u, unsigned lead, unsigned w) {
+  return u < lead ? 0 : static_cast<int>((u - lead) / w);
+}
 struct PlanScratch {
   long long wide[kPlanWarps];
   int narrow[kPlanWarps];
@@ -111,13 +117,14 @@ __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, const
         F = prefix_lens ? __ldg(prefix_lens + i) : 0;
         seen = i;
       }
-      cost += geo.lead() + geo.blocks(r, F, x - tile_start[i]);
+      const int w = geo.weight(r, x - tile_start[i]);
+      cost += geo.lead(w) + w * geo.blocks(r, F, x - tile_start[i]);
     }
   }
   long long U1;
   const long long first = cta_scan(cost, tmp->wide, U1);
   const long long U = U1 * n_kv;
-  const long long C = U < chunks ? U : chunks;
+  const long long C = min(static_cast<long long>(chunks), U / Geo::kMostWeight);
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     const long long k = static_cast<long long>(blockIdx.x) + e;
@@ -140,10 +147,12 @@ __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, const
     for (int x = a; x < b; ++x) {
       while (x >= tile_start[i + 1]) ++i;
       const int F = prefix_lens ? __ldg(prefix_lens + i) : 0;
-      const int nb = geo.lead() + geo.blocks(row_info(rows, i, nullptr), F, x - tile_start[i]);
-      if (rem < at + nb) {
-        Place p{h, x, i, x - tile_start[i], static_cast<int>(rem - at)};
-        if (p.off < geo.lead() + snap) {
+      const RowInfo r = row_info(rows, i, nullptr);
+      const int w = geo.weight(r, x - tile_start[i]), nb = geo.blocks(r, F, x - tile_start[i]);
+      const long long units = geo.lead(w) + static_cast<long long>(w) * nb;
+      if (rem < at + units) {
+        Place p{h, x, i, x - tile_start[i], block_of(static_cast<unsigned>(rem - at), geo.lead(w), w)};
+        if (p.off < snap) {
           p.off = 0;
         } else if (nb - p.off < snap) {  // the next tile's start
           p.off = 0;
@@ -157,7 +166,7 @@ __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, const
         bounds[e] = p;
         break;
       }
-      at += nb;
+      at += units;
     }
   }
   __syncthreads();
@@ -180,7 +189,10 @@ __device__ __forceinline__ int chunk_plan_warp(const ChunkRows& rows, int n_kv, 
   }
   const int n = r.L >= 0 ? geo.tiles(r) : 0;
   long long cost = 0;
-  for (int t = 0; t < n; ++t) cost += geo.lead() + geo.blocks(r, F, t);
+  for (int t = 0; t < n; ++t) {
+    const int w = geo.weight(r, t);
+    cost += geo.lead(w) + w * geo.blocks(r, F, t);
+  }
   int tiles = n;
   long long units = cost;  // inclusive prefix sums
 #pragma unroll
@@ -193,7 +205,8 @@ __device__ __forceinline__ int chunk_plan_warp(const ChunkRows& rows, int n_kv, 
     }
   }
   const int T = __shfl_sync(kFull, tiles, 31);
-  const long long U1 = __shfl_sync(kFull, units, 31), U = U1 * n_kv, C = U < chunks ? U : chunks;
+  const long long U1 = __shfl_sync(kFull, units, 31), U = U1 * n_kv,
+                  C = min(static_cast<long long>(chunks), U / Geo::kMostWeight);
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     Place p{n_kv, 0, 0, 0, 0};
@@ -211,16 +224,19 @@ __device__ __forceinline__ int chunk_plan_warp(const ChunkRows& rows, int n_kv, 
       const bool here = rem >= units - cost && rem < units;
       if (here) {  // in one lane
         long long off = rem - (units - cost);
-        int t = 0, nb = geo.lead() + geo.blocks(r, F, 0);
-        while (off >= nb) {
-          off -= nb;
+        int t = 0, nb, w;
+        while (true) {
+          nb = geo.blocks(r, F, t);
+          w = geo.weight(r, t);
+          const long long tile = geo.lead(w) + static_cast<long long>(w) * nb;
+          if (off < tile) break;
+          off -= tile;
           ++t;
-          nb = geo.lead() + geo.blocks(r, F, t);
         }
         p.i = lane;
         p.t = t;
-        p.off = static_cast<int>(off);
-        if (p.off < geo.lead() + snap) {
+        p.off = block_of(static_cast<unsigned>(off), geo.lead(w), w);
+        if (p.off < snap) {
           p.off = 0;
         } else if (nb - p.off < snap) {  // the next tile's start
           p.off = 0;
@@ -286,8 +302,8 @@ struct Walk {
   // the range ends within this tile, or at its start
   __device__ __forceinline__ bool ends_here() const { return at.h == end.h && at.tile == end.tile; }
   // the tile's blocks in the range: [from, to) of its nb
-  __device__ __forceinline__ int from() const { return max(0, at.off - geo.lead()); }
-  __device__ __forceinline__ int to(int nb) const { return ends_here() ? end.off - geo.lead() : nb; }
+  __device__ __forceinline__ int from() const { return at.off; }
+  __device__ __forceinline__ int to(int nb) const { return ends_here() ? end.off : nb; }
   // to the next tile; `end` is not in the tile just left
   __device__ __forceinline__ void next() {
     at.off = 0;
