@@ -210,6 +210,7 @@ struct Io {
   // P is scaled by 2^kShift: f16 weights far below the maximum stay normal
   // (the largest, 2^(8 + 7), is still below f16's 65504); bf16 has the range.
   [[maybe_unused]] static constexpr float kShift = DT == PKV_KV_BF16 ? 0.0f : 7.0f;
+  [[maybe_unused]] static constexpr float kScale = DT == PKV_KV_BF16 ? 1.0f : 128.0f;
   // two packed values times f
   static __device__ __forceinline__ uint32_t scale(uint32_t w, float f) {
     if constexpr (kType == PKV_KV_BF16) {
@@ -903,7 +904,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         constexpr float kMasked = GEN == 1 ? -1e15f : -INFINITY, kNone = GEN == 1 ? -1e14f : -INFINITY;
         float mx = kNone;      // the maximum in force, base 2
         float sub = 0.0f;      // what is taken off the scores: mx - shift (0 before a first score)
-        float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        float l = 0.0f;
+        float most = -1.0f;    // a group's sum beyond which its maximum is looked at
         for (int b = !kTurns || two ? 0 : m; b < d.nb; b += every, ++blocks, begun = true) {
           const int t0 = block(d.kb, d.nb, b) * N;
           const bool fast = __all_sync(kFull, t0 >= lo && t0 + N <= hi);
@@ -913,14 +915,14 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
             // The block goes by in groups of 32 columns, one load from tensor
             // memory ahead of the arithmetic, in a loop of two groups: its code
             // has to stay in the instruction caches that six other loops
-            // share.  A group's exponentials start under the maximum in force,
-            // and the group's own maximum is found beside them; should it
-            // exceed the one in force by more than 8 (rare after a tile's
-            // first block) the maximum is raised and they are taken again.
-            // Raises are by whole powers of two, so that the weights already
-            // written for the block are rescaled without another rounding.
-            // Looking for the maximum first put 450 cycles in front of the
-            // exponentials.
+            // share.  A group's exponentials start under the maximum in force.
+            // Should their sum exceed 256 (or a row have no maximum yet), the
+            // group's own maximum is found; if that exceeds the one in force by
+            // more than 8 (rare after a tile's first block) the maximum is raised
+            // and they are taken again.  Raises are by whole powers of two, so
+            // that the weights already written for the block are rescaled
+            // without another rounding.  The maximum of every group costs 8 us of
+            // 403 beside the exponentials, and 450 cycles a block before them.
             constexpr int kGroups = N / 32;
             auto raise_to = [&](float bm, int group) {
               const bool raise = bm > mx + 8.0f;  // also from none
@@ -930,7 +932,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                 al = tc::ex2(mx - to);  // a power of two, or 0
                 mx = to;
                 sub = to - F::kShift;
-                l2[0].x *= al; l2[0].y *= al; l2[1].x *= al; l2[1].y *= al;
+                l *= al;
+                most = 256.0f * F::kScale;
               }
               // the block's weights so far, and O: the values products before
               // are complete, S was issued after them
@@ -986,6 +989,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
               }
               uint32_t w[16];
               float2 lb[2];
+              float group_sum;
 #pragma unroll 1
               while (true) {
                 float2 off[4];  // of columns 2u, 2u + 1 and every eighth after
@@ -1009,18 +1013,27 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                   }
                   const float2 y = tc::fma2(x, f, off[u & 3]);
                   if constexpr (GEN == 2) off[u & 3] = tc::add2(off[u & 3], next);
-                  const float2 z = GEN != 0 ? y : x;
-                  if (u & 1) x1 = tc::max3(x1, z.x, z.y); else x0 = tc::max3(x0, z.x, z.y);
+                  if constexpr (GEN != 0) {
+                    if (u & 1) x1 = tc::max3(x1, y.x, y.y); else x0 = tc::max3(x0, y.x, y.y);
+                  }
                   const float2 pr = make_float2(tc::ex2(y.x), tc::ex2(y.y));
                   lb[u & 1] = tc::add2(lb[u & 1], pr);
                   w[u] = F::pack(pr.x, pr.y);
+                }
+                const float2 both = tc::add2(lb[0], lb[1]);
+                group_sum = both.x + both.y;
+                if constexpr (GEN == 0) {
+                  if (__builtin_expect(!__any_sync(kFull, group_sum > most), 1)) break;
+#pragma unroll
+                  for (int u = 0; u < 16; ++u) {
+                    if (u & 1) x1 = tc::max3(x1, v[2 * u], v[2 * u + 1]); else x0 = tc::max3(x0, v[2 * u], v[2 * u + 1]);
+                  }
                 }
                 const float bm = GEN != 0 ? fmaxf(x0, x1) + sub : fmaxf(x0, x1) * c1;
                 if (__builtin_expect(!__any_sync(kFull, bm > mx + 8.0f), 1)) break;
                 raise_to(bm, group);
               }
-              l2[0] = tc::add2(l2[0], lb[0]);
-              l2[1] = tc::add2(l2[1], lb[1]);
+              l += group_sum;
               tc::st16(tS + 16 * group, w);
             };
             float v0[32], v1[32];
@@ -1064,8 +1077,6 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         if (!ok || !(ok = wait(kBO + m, pieces))) break;
         ++pieces;
         tc::fence_after();
-        const float2 la = tc::add2(l2[0], l2[1]);
-        float l = la.x + la.y;
         float f0 = 1.0f, f1 = 0.0f;  // the halves' factors
         if (join && m == 1) {  // O_1 is complete, and half 0 reads it
           tail.half[32 * quarter + lane] = make_float2(sub, l);
