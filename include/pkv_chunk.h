@@ -85,7 +85,7 @@ pkv_status kv_rope_append(const pkv_pool *pool, int layer, const void *q, long l
  * causal, but within the row's first F = prefix_lens[i] tokens seen from
  * everywhere (prefix_lens NULL: F = 0), and W the layer's sliding window (0:
  * none).  slopes is fp32 [n_q_heads], prefix_lens int32 [num_rows], both on the
- * device; softcap 0 means none. */
+ * device; softcap 0 means none, others are 1e-30 to 1e30. */
 typedef struct pkv_scores {
     float scale;
     float softcap;

@@ -9,6 +9,7 @@ missing library raises on first use.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -473,6 +474,12 @@ def _token_array(t, name, tokens, heads, dtype, pool):
     return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * HEAD_DIM
 
 
+def _made_on(stream):
+    """Tensors made within belong to the call's stream: filled in its order, and their memory is reused in
+    its order once they are gone."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _call(name, pool, stream, *args):
     """The C entry `name` on the pool's device and the given stream, or its current one: launches go to the
     current device."""
@@ -508,7 +515,8 @@ def kv_rope_append(pool: KVPool, layer: int, q, k, v, positions, inv_freq, secti
         qp, qs = _token_array(q, "q", tokens, None, dtype, pool)
         n_q = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(tokens, n_q, HEAD_DIM, dtype=dtype, device=pool.device)
+            with _made_on(stream):
+                q_out = torch.empty(tokens, n_q, HEAD_DIM, dtype=dtype, device=pool.device)
         if not isinstance(q_out, torch.Tensor) or q_out.dtype not in _KIND:
             raise TypeError("q_out must be a float16, bfloat16 or float32 tensor")
         op, kind_out = _array(q_out, q_out.dtype, "q_out", (tokens, n_q, HEAD_DIM), pool), _KIND[q_out.dtype]
@@ -583,13 +591,15 @@ def paged_chunk_attention(pool: KVPool, layer: int, q, cu_seqlens, block_table, 
     qp, qs = _token_array(q, "q", None, None, dtype, pool)
     tokens, n_q = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty(tokens, n_q, HEAD_DIM, dtype=dtype, device=pool.device)
+        with _made_on(stream):
+            out = torch.empty(tokens, n_q, HEAD_DIM, dtype=dtype, device=pool.device)
     op = _array(out, dtype, "out", (tokens, n_q, HEAD_DIM), pool)
     lp = _optional(lse, torch.float32, "lse", (tokens, n_q), pool)
     sc = _Scores(scale, softcap, _optional(slopes, torch.float32, "slopes", (n_q,), pool),
                  _optional(prefix_lens, torch.int32, "prefix_lens", (rows,), pool))
     if workspace is None:
-        workspace = WorkspaceChunk(pool, n_q)
+        with _made_on(stream):
+            workspace = WorkspaceChunk(pool, n_q)
     _call("paged_chunk_attention", pool, stream, pool.handle, layer, qp, qs, _KIND[dtype],
           _array(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), pool), tokens, bt, stride,
           _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows, n_q, ctypes.addressof(sc), op, lp,
@@ -620,7 +630,8 @@ def paged_attention_mass(pool: KVPool, layer: int, q, lse, cu_seqlens, block_tab
     sc = _Scores(scale, softcap, _optional(slopes, torch.float32, "slopes", (n_q,), pool),
                  _optional(prefix_lens, torch.int32, "prefix_lens", (rows,), pool))
     if workspace is None:
-        workspace = WorkspaceMass(pool, n_q)
+        with _made_on(stream):
+            workspace = WorkspaceMass(pool, n_q)
     _call("paged_attention_mass", pool, stream, pool.handle, layer, qp, qs, _KIND[dtype], lp,
           _array(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), pool), tokens, bt, stride,
           _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows, n_q, ctypes.addressof(sc),
@@ -639,11 +650,13 @@ def kv_evict(pool: KVPool, layer: int, mass, block_table, seq_lens, keep_lens, d
     if not isinstance(mass, torch.Tensor) or mass.dim() != 3 or mass.shape[:2] != (rows, pool.n_kv):
         raise ValueError("mass must be a tensor [rows][n_kv][stride]")
     if keep_idx is None:
-        keep_idx = torch.full((rows, pool.n_kv, PAGE * dst_stride), -1, dtype=torch.int32, device=pool.device)
+        with _made_on(stream):
+            keep_idx = torch.full((rows, pool.n_kv, PAGE * dst_stride), -1, dtype=torch.int32, device=pool.device)
     if not isinstance(keep_idx, torch.Tensor) or keep_idx.dim() != 3 or keep_idx.shape[:2] != (rows, pool.n_kv):
         raise ValueError("keep_idx must be a tensor [rows][n_kv][stride]")
     if new_lens is None:
-        new_lens = torch.empty_like(seq_lens)
+        with _made_on(stream):
+            new_lens = torch.empty_like(seq_lens)
     shape = keep_idx.shape
     _call("kv_evict", pool, stream, pool.handle, layer, _array(mass, torch.float32, "mass", mass.shape, pool),
           mass.shape[2], bt, stride, _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows,

@@ -71,6 +71,8 @@ pkv_status check_scores(const pkv_scores* sc) {
   if (!std::isfinite(sc->scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
   if (!(sc->softcap >= 0.0f) || !std::isfinite(sc->softcap))
     return fail(PKV_ERR_INVALID_ARG, "softcap below 0 or not finite");
+  if (sc->softcap > 0.0f && (sc->softcap < 1e-30f || sc->softcap > 1e30f || !std::isfinite(sc->scale / sc->softcap)))
+    return fail(PKV_ERR_INVALID_ARG, "softcap outside 1e-30 .. 1e30, or scale / softcap not finite");
   if (!aligned(sc->slopes, 4) || !aligned(sc->prefix_lens, 4))
     return fail(PKV_ERR_INVALID_ARG, "slopes / prefix_lens not 4-byte aligned");
   return PKV_OK;

@@ -78,11 +78,11 @@ __device__ __forceinline__ void cap32(float (&v)[32], uint32_t tS, float k, floa
     tc::wait_ld();
     return;
   }
-  const float2 zero = make_float2(0.0f, 0.0f), kk = make_float2(k * k, k * k);
+  const float2 zero = make_float2(0.0f, 0.0f), kk = make_float2(k, k);
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
     const float2 x = make_float2(v[e], v[e + 1]);
-    const float2 w = tc::fma2(tc::fma2(x, kk, zero), x, zero);
+    const float2 z = tc::fma2(x, kk, zero), w = tc::fma2(z, z, zero);
     float2 q = make_float2(kc * kQ[5], kc * kQ[5]);
 #pragma unroll
     for (int i = 4; i >= 0; --i) q = tc::fma2(q, w, make_float2(kc * kQ[i], kc * kQ[i]));

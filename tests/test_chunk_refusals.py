@@ -155,3 +155,9 @@ def evict(pools, kv=api.F16):
 ])
 def test_evict(lib, pools, changes, status):
     refused(lib, "kv_evict", evict(pools), changes, status)
+
+
+@pytest.mark.parametrize("scale,softcap", [(0.1, 1e-31), (0.1, 2e30), (1e38, 1e-3)])
+def test_caps_whose_scores_leave_fp32(lib, pools, scale, softcap):
+    changes = dict(sc=ctypes.pointer(api._Scores(scale, softcap, None, None)))
+    refused(lib, "paged_chunk_attention", attention(pools), changes, INVALID)

@@ -89,6 +89,41 @@ def test_scores(kv, kw):
     check(c, q, out, lse, **b)
 
 
+@pytest.mark.parametrize("kw", [dict(softcap=8.0), dict(softcap=1.5), dict(softcap=1e-3), dict(softcap=1e5),
+                                dict(softcap=1e12), dict(scale=-0.2), dict(scale=0.0), dict(scale=-0.2, softcap=6.0),
+                                dict(slope=-0.05), dict(slope=8.0), dict(slope=0.5, softcap=30.0, window=90),
+                                dict(softcap=3.0, window=40, prefix=True), dict(slope=1.0, prefix=True)])
+@pytest.mark.parametrize("kv", [api.F16, api.Q8_0])
+def test_scores_at_their_ends(kv, kw):
+    """Caps near and far from the scores, scales that are not positive, biases that rise and fall steeply: chunks
+    of both halves of a tile and single tokens."""
+    rows = [(150, 700), (1, 650), (20, 20), (64, 300), (1, 1)]
+    c = R.Chunk(kv, 2, 4, rows, seed=13)
+    b = {k: v for k, v in kw.items() if k == "softcap"}
+    if "slope" in kw:
+        b["slopes"] = torch.tensor([kw["slope"] * 0.9 ** h for h in range(c.n_q)], device=c.device)
+    if kw.get("prefix"):
+        b["prefix_lens"] = torch.tensor([690, 0, 20, 128, 5], dtype=torch.int32, device=c.device)
+    a, scale = dict(b), kw.get("scale", SCALE)
+    if "window" in kw:
+        c.pool.set_window(0, kw["window"])
+        b["window"] = kw["window"]
+    q = c.normal(c.tokens, c.n_q, 128, dtype=R.IO[kv])
+    lse = torch.empty(c.tokens, c.n_q, device=c.device)
+    out = api.paged_chunk_attention(c.pool, 0, q, c.cu, c.bt, c.lens, scale, lse=lse, **a)
+    want, tol, wl, lt = R.attention(c, q, scale, **b)
+    assert ((out.double() - want).abs() <= tol).all(), float(((out.double() - want).abs() - tol).max())
+    assert ((lse.double() - wl).abs() <= lt).all(), float(((lse.double() - wl).abs() - lt).max())
+    got = torch.zeros(len(rows), 2, 700, device=c.device)
+    api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, scale, mass_out=got, **a)
+    want, tol = R.mass(c, q, lse, scale, torch.zeros_like(got), **b)
+    for i, (n, L) in enumerate(rows):
+        # a steep bias takes weights below fp32's normal numbers, where each of a token's n (n_q / n_kv) terms is
+        # lost: less than 2^-126 each
+        lost = n * (c.n_q // c.n_kv) * 2.0 ** -126
+        assert ((got[i, :, :L].double() - want[i, :, :L]).abs() <= tol[i, :, :L] + lost).all(), i
+
+
 def test_large_scores():
     """Scores of several hundred: the running maximum is raised by far more than exp's range."""
     c = R.Chunk(api.F16, 1, 4, [(140, 900)], seed=2, spread=30.0)
@@ -195,6 +230,34 @@ def test_streams_and_graph():
     want, tol = R.mass(c, q, lse2, SCALE, torch.zeros_like(mass))
     for i, (_, L) in enumerate(c.rows):
         assert ((mass[i, :, :L].double() - want[i, :, :L]).abs() <= tol[i, :, :L]).all()
+
+
+def test_scratch_belongs_to_the_calls_stream(monkeypatch):
+    """Scratch that a call makes for a stream of its own is not handed to the current stream while that one may
+    still use it."""
+    c = R.Chunk(api.F16, 2, 4, [(65, 500), (1, 900)], seed=6)
+    made = []
+    for name in ("WorkspaceChunk", "WorkspaceMass"):
+        def note(*a, make=getattr(api, name)):
+            made.append(make(*a))
+            return made[-1]
+        monkeypatch.setattr(api, name, note)
+    side = torch.cuda.Stream()
+    q, out, lse = run(c)
+    del made[:]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    _, out2, lse2 = run(c, q, stream=side)  # its outputs are filled before, on the current stream
+    mass = api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, stream=side,
+                                    mass_out=torch.zeros(2, 2, 900, device=c.device))
+    at, sizes = [w.tensor.data_ptr() for w in made], [w.nbytes for w in made]
+    assert len(at) == 2
+    del made[:]
+    for size in sizes:
+        assert torch.empty(size, dtype=torch.uint8, device=c.device).data_ptr() not in at
+    torch.cuda.synchronize()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2) and bool((mass[0, :, :500] > 0).all())
 
 
 # ------------------------------------------------------------------------ mass ----

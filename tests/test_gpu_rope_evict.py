@@ -239,6 +239,24 @@ def test_evict_clamps_and_reports():
     assert c.pool.read_status() == api.DEV_BAD_PAGE
 
 
+def test_evict_on_a_stream_of_its_own():
+    """The kept indices that the call makes are filled on its stream, not behind the current one's work."""
+    rows, budgets = [700, 300], [250, 300]
+    c, bt, lens, dst = evict_case(api.F16, rows, budgets, seed=3)
+    mass = torch.rand(2, c.n_kv, 700, generator=c.gen).to(c.device)
+    keep = torch.tensor(budgets, dtype=torch.int32, device=c.device)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # the current stream is busy
+    idx, new = api.kv_evict(c.pool, 0, mass, bt, lens, keep, dst, first=4, recent=16, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert new.tolist() == budgets
+    for h in range(c.n_kv):
+        assert idx[0, h, :250].tolist() == R.keep(mass[0, h].tolist(), 700, 250, 4, 16)
+        assert idx[1, h, :300].tolist() == list(range(300))
+
+
 # ---------------------------------------------------------------- all together ----
 @pytest.mark.parametrize("kv", [api.F16, api.BF16, api.Q8_0])
 def test_long_prompt_in_chunks_then_eviction_then_a_step(kv):
