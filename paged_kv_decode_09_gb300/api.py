@@ -9,7 +9,6 @@ missing library raises on first use.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -474,10 +473,13 @@ def _token_array(t, name, tokens, heads, dtype, pool):
     return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * HEAD_DIM
 
 
-def _made_on(stream):
-    """Tensors made within belong to the call's stream: filled in its order, and their memory is reused in
-    its order once they are gone."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _made(stream, make, *args, **kw):
+    """make(...), whose tensors belong to the call's stream: filled in its order, and their memory is reused
+    in its order once they are gone."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
 
 
 def _call(name, pool, stream, *args):
@@ -515,8 +517,7 @@ def kv_rope_append(pool: KVPool, layer: int, q, k, v, positions, inv_freq, secti
         qp, qs = _token_array(q, "q", tokens, None, dtype, pool)
         n_q = q.shape[1]
         if q_out is None:
-            with _made_on(stream):
-                q_out = torch.empty(tokens, n_q, HEAD_DIM, dtype=dtype, device=pool.device)
+            q_out = _made(stream, torch.empty, tokens, n_q, HEAD_DIM, dtype=dtype, device=pool.device)
         if not isinstance(q_out, torch.Tensor) or q_out.dtype not in _KIND:
             raise TypeError("q_out must be a float16, bfloat16 or float32 tensor")
         op, kind_out = _array(q_out, q_out.dtype, "q_out", (tokens, n_q, HEAD_DIM), pool), _KIND[q_out.dtype]
@@ -533,6 +534,7 @@ def kv_rope_append(pool: KVPool, layer: int, q, k, v, positions, inv_freq, secti
 
 
 _sm_counts = {}  # device index: SMs, the default chunks of a call
+_mass_bytes = {}  # chunks: bytes of a workspace
 
 
 def _default_chunks_chunk(pool, n_q_heads):
@@ -563,9 +565,12 @@ class WorkspaceMass:
 
     def __init__(self, pool: KVPool, n_q_heads: int, num_chunks: int = 0):
         self.num_chunks = num_chunks or _default_chunks_chunk(pool, n_q_heads)
-        self.nbytes = lib().paged_attention_mass_workspace_bytes(self.num_chunks)
-        if self.nbytes == 0:
-            raise PkvError(1, "paged_attention_mass_workspace_bytes", "invalid sizes")
+        self.nbytes = _mass_bytes.get(self.num_chunks)
+        if self.nbytes is None:
+            self.nbytes = lib().paged_attention_mass_workspace_bytes(self.num_chunks)
+            if self.nbytes == 0:
+                raise PkvError(1, "paged_attention_mass_workspace_bytes", "invalid sizes")
+            _mass_bytes[self.num_chunks] = self.nbytes
         self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=pool.device)
 
 
@@ -591,15 +596,13 @@ def paged_chunk_attention(pool: KVPool, layer: int, q, cu_seqlens, block_table, 
     qp, qs = _token_array(q, "q", None, None, dtype, pool)
     tokens, n_q = q.shape[0], q.shape[1]
     if out is None:
-        with _made_on(stream):
-            out = torch.empty(tokens, n_q, HEAD_DIM, dtype=dtype, device=pool.device)
+        out = _made(stream, torch.empty, tokens, n_q, HEAD_DIM, dtype=dtype, device=pool.device)
     op = _array(out, dtype, "out", (tokens, n_q, HEAD_DIM), pool)
     lp = _optional(lse, torch.float32, "lse", (tokens, n_q), pool)
     sc = _Scores(scale, softcap, _optional(slopes, torch.float32, "slopes", (n_q,), pool),
                  _optional(prefix_lens, torch.int32, "prefix_lens", (rows,), pool))
     if workspace is None:
-        with _made_on(stream):
-            workspace = WorkspaceChunk(pool, n_q)
+        workspace = _made(stream, WorkspaceChunk, pool, n_q)
     _call("paged_chunk_attention", pool, stream, pool.handle, layer, qp, qs, _KIND[dtype],
           _array(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), pool), tokens, bt, stride,
           _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows, n_q, ctypes.addressof(sc), op, lp,
@@ -630,8 +633,7 @@ def paged_attention_mass(pool: KVPool, layer: int, q, lse, cu_seqlens, block_tab
     sc = _Scores(scale, softcap, _optional(slopes, torch.float32, "slopes", (n_q,), pool),
                  _optional(prefix_lens, torch.int32, "prefix_lens", (rows,), pool))
     if workspace is None:
-        with _made_on(stream):
-            workspace = WorkspaceMass(pool, n_q)
+        workspace = _made(stream, WorkspaceMass, pool, n_q)
     _call("paged_attention_mass", pool, stream, pool.handle, layer, qp, qs, _KIND[dtype], lp,
           _array(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), pool), tokens, bt, stride,
           _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows, n_q, ctypes.addressof(sc),
@@ -650,13 +652,12 @@ def kv_evict(pool: KVPool, layer: int, mass, block_table, seq_lens, keep_lens, d
     if not isinstance(mass, torch.Tensor) or mass.dim() != 3 or mass.shape[:2] != (rows, pool.n_kv):
         raise ValueError("mass must be a tensor [rows][n_kv][stride]")
     if keep_idx is None:
-        with _made_on(stream):
-            keep_idx = torch.full((rows, pool.n_kv, PAGE * dst_stride), -1, dtype=torch.int32, device=pool.device)
+        keep_idx = _made(stream, torch.full, (rows, pool.n_kv, PAGE * dst_stride), -1, dtype=torch.int32,
+                         device=pool.device)
     if not isinstance(keep_idx, torch.Tensor) or keep_idx.dim() != 3 or keep_idx.shape[:2] != (rows, pool.n_kv):
         raise ValueError("keep_idx must be a tensor [rows][n_kv][stride]")
     if new_lens is None:
-        with _made_on(stream):
-            new_lens = torch.empty_like(seq_lens)
+        new_lens = _made(stream, torch.empty_like, seq_lens)
     shape = keep_idx.shape
     _call("kv_evict", pool, stream, pool.handle, layer, _array(mass, torch.float32, "mass", mass.shape, pool),
           mass.shape[2], bt, stride, _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows,
