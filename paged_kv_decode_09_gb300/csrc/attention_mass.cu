@@ -16,8 +16,12 @@
 // issues the products, 10 copies K pages, 11 copies queries and stages their
 // lse; with q8_0, 12-15 split the codes instead of warp 10.  Each half has two
 // score buffers (all 512 columns of tensor memory), so that the products run
-// ahead of the exponentials, which bound the kernel: 32768 of them a block
-// against 512 cycles of products.
+// ahead of the exponentials.  A block of 256 x 128 takes 1024 cycles of
+// products and as many of exponentials (four cycles a warp's row each), and in
+// fact some 2500: two warps a scheduler take 450 cycles for a group of 32
+// columns, four warps a scheduler (the columns shared out) no less in all.  Two
+// chunks of 1800 tokens over 5600 and 4500: 158 us, 775 TFLOP/s; the last 32
+// queries of four rows of 5K to 23K tokens, which K's bytes bound (15 us): 28.5.
 //
 // The work is the line of (KV head, tile, block) units of chunk_plan.cuh; a
 // tile cut by a boundary leaves its 256 partial sums in the workspace, which
@@ -515,9 +519,9 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.0f, 0.0f);
           // the weights of columns 32 q ..: 2^(c1 s - lse2).  The masked form is
-          // code of its own: a test per column group would cut the arithmetic
-          // into pieces too short to hide each other's latency (3500 cycles a
-          // block instead of 1400).
+          // code of its own: a test per column would cut the arithmetic into
+          // pieces too short to hide each other's latency (two chunks of 1800
+          // tokens 223 us instead of 163).
           auto weigh = [&](float (&v)[32], int q) {
             float2 mul = make_float2(c1, c1);
             float cq[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // GEN 1: the factor is q(v^2)

@@ -24,7 +24,8 @@
 // Q, 9 issues the products, 10 copies K and V pages (one tensor copy each)
 // into a ring of five 32 KiB slots, 11 mends V blocks that hold tokens no
 // query of the tile attends to; with q8_0, 10 copies codes and scales into a
-// ring of their own, and 12-15 split them into the ring of slots.  Hand-overs by shared-memory barriers:
+// ring of their own, and 12-15 split them into the ring of slots.  Hand-overs
+// by shared-memory barriers:
 //   dfull, dempty[x]  descriptor x of a piece (a tile's blocks in this range)
 //   qfull[m], qempty  Q_m landed; the piece's last scores are computed
 //   full, empty[s]    K or V block in ring slot s
@@ -37,6 +38,19 @@
 //                     read them and O_1
 // Every wait is bounded; a warp that gives up sets the abort flag, which ends
 // the other waits, and its copies and products are awaited before the CTA ends.
+//
+// What bounds it: the products of a block of 256 x 128 take 2048 cycles, a block
+// some 3200.  A half's softmax (four groups of 32 columns, 400 to 500 cycles
+// each while the other half's warps compete for the schedulers) and its own two
+// products follow one another, and there is no tensor memory left for a second
+// S_m.  Scores in steps of 64 tokens, each computed while the step before is in
+// its softmax, take that chain apart, but the scores' products then cost half
+// as much again and the steps their own hand-overs: 381 us instead of 376.
+// 8191 tokens of 32 heads in bf16 376 us, 1460 TFLOP/s; with a window of 4096
+// over rows of 14K to 16K 195 us, 1230 TFLOP/s; 2048 tokens over 32049 in q8_0
+// 1.40 ms (twice the products; 745 TFLOP/s of useful work).  Single tokens of 8
+// rows of 1K to 6K are bound by K and V's bytes: 22.4 us, 4.1 TB/s, of which
+// some 10 are the launches, the plan, the last blocks and the merge.
 //
 // The work of the batch is a line of (KV head, tile, block) units, cut into
 // equal ranges, one per CTA (chunk_plan.cuh).  A tile that crosses a boundary
