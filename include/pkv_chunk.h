@@ -97,7 +97,8 @@ typedef struct pkv_scores {
  * (the chunk's K and V stored before, by kv_rope_append or kv_append):
  *     out[j][g] = sum_t softmax_t(s) V[h][t],   lse[j][g] = log sum_t exp(s)
  *   q      [total_tokens][n_q_heads][128] of q_dtype, any token stride
- *   out    contiguous [total_tokens][n_q_heads][128] of q_dtype
+ *   out    contiguous [total_tokens][n_q_heads][128] of q_dtype; it must not
+ *          overlap q
  *   lse    fp32 [total_tokens][n_q_heads], or NULL
  * q_dtype is f16 on f16 and q8_0 pools and bf16 on bf16 pools; f32 pools are
  * refused (PKV_ERR_UNSUPPORTED; paged_decode_attention_mq serves them).

@@ -215,6 +215,8 @@ pkv_status paged_chunk_attention(const pkv_pool* pool, int layer, const void* q,
   if (!workspace || workspace_bytes < need)
     return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   if (!aligned(workspace, 256)) return fail(PKV_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  // a row that is computed again reads its query after others are written
+  if (out == q) return fail(PKV_ERR_INVALID_ARG, "out must not be q");
   a.rows = rows_of(cu_seqlens, seq_lens, block_table, bt_stride, num_rows, total_tokens);
   a.q = static_cast<const uint8_t*>(q);
   a.q_stride = q_stride;

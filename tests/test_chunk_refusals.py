@@ -161,3 +161,8 @@ def test_evict(lib, pools, changes, status):
 def test_caps_whose_scores_leave_fp32(lib, pools, scale, softcap):
     changes = dict(sc=ctypes.pointer(api._Scores(scale, softcap, None, None)))
     refused(lib, "paged_chunk_attention", attention(pools), changes, INVALID)
+
+
+def test_out_is_not_q(lib, pools):
+    refused(lib, "paged_chunk_attention", attention(pools), dict(out=FAKE), INVALID)
+    assert b"out" in lib.pkv_last_error_message()
