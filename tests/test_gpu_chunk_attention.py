@@ -232,6 +232,52 @@ def test_streams_and_graph():
         assert ((mass[i, :, :L].double() - want[i, :, :L]).abs() <= tol[i, :, :L]).all()
 
 
+@pytest.mark.parametrize("kv", [api.F16, api.Q8_0])
+def test_replayed_with_other_lengths(kv):
+    """A captured call follows the lengths that the device holds when it is replayed: other rows, fewer tokens, a
+    row without any."""
+    c = R.Chunk(kv, 2, 4, [(65, 500), (1, 900), (200, 260)], seed=6)
+    ws, wm = api.WorkspaceChunk(c.pool, c.n_q), api.WorkspaceMass(c.pool, c.n_q)
+    q, out, lse = run(c, workspace=ws)
+    mass = torch.zeros(3, 2, 1000, device=c.device)
+    api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, mass_out=mass, workspace=wm)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.paged_chunk_attention(c.pool, 0, q, c.cu, c.bt, c.lens, SCALE, out=out, lse=lse, workspace=ws)
+        api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, mass_out=mass, workspace=wm)
+    for rows in ([(1, 120), (150, 900), (0, 10)], [(266, 400), (0, 0), (0, 260)], [(1, 1), (1, 900), (1, 2)]):
+        c.rows = rows
+        c.cu.copy_(torch.tensor([0] + [n for n, _ in rows]).cumsum(0))
+        c.lens.copy_(torch.tensor([L for _, L in rows]))
+        mass.fill_(-1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(c, q, out, lse)
+        want, tol = R.mass(c, q, lse, SCALE, torch.zeros_like(mass))
+        for i, (_, L) in enumerate(rows):
+            assert ((mass[i, :, :L].double() - want[i, :, :L]).abs() <= tol[i, :, :L]).all()
+            assert (mass[i, :, L:] == -1).all()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace, give the bits that they give alone."""
+    c = R.Chunk(api.BF16, 2, 4, [(65, 500), (1, 4000), (300, 1500)] + [(1, 700)] * 20, seed=16)
+    q, out, lse = run(c)
+    mass = api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE,
+                                    mass_out=torch.zeros(23, 2, 4000, device=c.device))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [(api.WorkspaceChunk(c.pool, c.n_q), api.WorkspaceMass(c.pool, c.n_q)) for _ in streams]
+    outs = [(torch.zeros_like(out), torch.zeros_like(lse), torch.zeros_like(mass)) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, (ws, wm), (o, l, m) in zip(streams, spaces, outs):
+            api.paged_chunk_attention(c.pool, 0, q, c.cu, c.bt, c.lens, SCALE, out=o, lse=l, workspace=ws, stream=st)
+            api.paged_attention_mass(c.pool, 0, q, l, c.cu, c.bt, c.lens, SCALE, mass_out=m, workspace=wm, stream=st)
+    torch.cuda.synchronize()
+    for o, l, m in outs:
+        assert torch.equal(o, out) and torch.equal(l, lse) and torch.equal(m, mass)
+
+
 def test_scratch_belongs_to_the_calls_stream(monkeypatch):
     """Scratch that a call makes for a stream of its own is not handed to the current stream while that one may
     still use it."""
