@@ -15,7 +15,7 @@
 // shared memory holds re-read their weights (from L2) in every pass.  Each loop
 // runs once over the keys, from a cold instruction cache: they are loops of a
 // few instructions (with the keys in registers and the loops unrolled, the code
-// took 32 us to fetch, whatever the rows' lengths).  19 us for 32768 tokens a
+// took 32 us to fetch, whatever the rows' lengths).  18 us for 32768 tokens a
 // row, 7 for 2048; a cluster of two CTAs a row and head gains one of them, one
 // of four loses nine to its meetings.
 //
@@ -23,7 +23,7 @@
 // a CTA takes 64 kept tokens of a head and moves their K and V in 16-byte
 // pieces.  Bound by memory: the bytes are the kept K and V, read and written
 // once; the weights of the whole row are a few percent of them.  Eight rows to
-// 4096 tokens of 8 heads each, 273 MB: 40 us, 6.8 TB/s; with the selection 59.
+// 4096 tokens of 8 heads each, 273 MB: 40 us, 6.8 TB/s; with the selection 58.
 #include <atomic>
 #include <cstdint>
 
@@ -91,7 +91,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     return t < first || t >= L - recent ? 0xFFFFFFFFu : key_of(x);
   };
   auto key = [&](int t) { return CACHED ? keys[t] : fetch(t); };
-  if constexpr (CACHED) {
+  uint32_t* mine = hist[warp % kCopies];
+  auto clear = [&] {
+#pragma unroll 1
+    for (int e = tid; e < kCopies * kBins / 4; e += kSelThreads)
+      reinterpret_cast<uint4*>(hist)[e] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+  };
+  clear();
+  if constexpr (CACHED) {  // the keys, and the first digit's histogram with them
 #pragma unroll 1
     for (int t0 = 0; t0 < L; t0 += 8 * kSelThreads) {  // eight loads in flight
       float x[8];
@@ -100,7 +108,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int t = t0 + u * kSelThreads + tid;
-        if (t < L) keys[t] = t < first || t >= L - recent ? 0xFFFFFFFFu : key_of(x[u]);
+        if (t < L) {
+          const uint32_t y = t < first || t >= L - recent ? 0xFFFFFFFFu : key_of(x[u]);
+          keys[t] = y;
+          atomicAdd(&mine[y >> 21], 1u);
+        }
       }
     }
   }
@@ -110,15 +122,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t digit = pass == 2 ? 1023u : 2047u;
-#pragma unroll 1
-    for (int e = tid; e < kCopies * kBins / 4; e += kSelThreads)
-      reinterpret_cast<uint4*>(hist)[e] = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-    uint32_t* mine = hist[warp % kCopies];
+    if (pass > 0) clear();
+    if (!CACHED || pass > 0) {
 #pragma unroll 4
-    for (int t = tid; t < L; t += kSelThreads) {
-      const uint32_t x = key(t);
-      if ((x & mask) == T) atomicAdd(&mine[(x >> shift) & digit], 1u);
+      for (int t = tid; t < L; t += kSelThreads) {
+        const uint32_t x = key(t);
+        if ((x & mask) == T) atomicAdd(&mine[(x >> shift) & digit], 1u);
+      }
     }
     __syncthreads();
     // a thread's bins, from the top: 2 consecutive ones
