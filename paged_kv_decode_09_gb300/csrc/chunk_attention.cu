@@ -50,7 +50,8 @@
 // over rows of 14K to 16K 195 us, 1230 TFLOP/s; 2048 tokens over 32049 in q8_0
 // 1.40 ms (twice the products; 745 TFLOP/s of useful work).  Single tokens of 8
 // rows of 1K to 6K are bound by K and V's bytes: 22.4 us, 4.1 TB/s, of which
-// some 10 are the launches, the plan, the last blocks and the merge.
+// some 10 are the launches, the plan, the last blocks and the merge.  The CTAs
+// of the prompt are busy for 351 to 364 us, 356 in the mean.
 //
 // The work of the batch is a line of (KV head, tile, block) units, cut into
 // equal ranges, one per CTA (chunk_plan.cuh).  A tile that crosses a boundary
@@ -90,7 +91,7 @@ constexpr int kAttnThreads = DT == PKV_KV_Q8_0 ? 512 : kPlanThreads;
 #define PKV_CHUNK_SMALL_COST 10
 #endif
 #ifndef PKV_CHUNK_SNAP
-#define PKV_CHUNK_SNAP 2
+#define PKV_CHUNK_SNAP 1
 #endif
 // What a tile costs besides its blocks, and how far from a tile's end a
 // boundary moves there, in blocks (chunk_plan).
