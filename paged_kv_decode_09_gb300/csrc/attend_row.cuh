@@ -61,7 +61,7 @@ __device__ __forceinline__ void attend_row(const PoolView& pool, const ChunkRows
       }
       r = (static_cast<long long>(pg) * pool.n_kv + h) * kPage + t % kPage;
       float dot = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
       for (int vec = 0; vec < kD / 8; ++vec) {
         float x[8], y[8];
         load_kv8<DT>(pool.k_data, pool.k_scales, r, vec, x);
@@ -86,6 +86,7 @@ __device__ __forceinline__ void attend_row(const PoolView& pool, const ChunkRows
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] *= al;
     const int n = min(32, t1 - base);
+#pragma unroll 8
     for (int u = 0; u < n; ++u) {
       const float pu = __shfl_sync(kFull, p, u);
       const long long ru = __shfl_sync(kFull, r, u);

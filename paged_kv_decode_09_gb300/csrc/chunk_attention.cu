@@ -60,9 +60,12 @@
 //
 // A token that some rows of a tile attend to and others do not gets weight 0
 // in the latter, but 0 times a value that is not finite is not 0.  Warp 11
-// looks for such values in the blocks that are masked for part of the tile;
-// where it finds one, rows that end up not finite are computed again from the
-// tokens they attend to alone (attend_row).
+// looks for such values in the blocks that are masked for part of the tile.
+// Where it finds one, the rows of the CTA's range that ended up not finite are
+// computed again from the tokens they attend to alone (mend_rows), after the
+// pipeline has drained: a row takes a warp 5.6 us per 32 tokens (7.3 with four
+// loads in flight instead of eight), so that inside the pipeline a tile of a
+// row of 150K tokens would run the other warps' waits out of their limit.
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -151,11 +154,11 @@ static_assert(sizeof(Piece) == 64, "");
 struct Tail {
   uint64_t bars[kNumBars];
   Piece piece[kDescs];
-  int bad[kDescs];  // a masked V block of the piece holds a value that is not finite
-  volatile int ctl[2];
+  volatile int ctl[2];  // abort; a masked V block held a value that is not finite
   uint32_t tmem;
+  int tiles;           // of the batch
   float2 half[kTileRows / 2];  // half 1's maximum and sum of each row
-  Place bounds[2];
+  Place bounds[2];     // the CTA's range
   PlanScratch scratch;
 };
 constexpr size_t kSmemBytes = 1024 + kTail + sizeof(Tail);
@@ -236,6 +239,12 @@ struct Io {
       return *reinterpret_cast<const uint32_t*>(&h);
     }
   }
+  static __device__ __forceinline__ float2 values(uint32_t w) {
+    if constexpr (kType == PKV_KV_BF16)
+      return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else
+      return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
   static __device__ __forceinline__ uint32_t pack(float x, float y) {
     if constexpr (kType == PKV_KV_BF16) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
@@ -247,10 +256,33 @@ struct Io {
   }
 };
 
+// Blocks [b0, b1) of tile g, where the walk of this CTA's range stands.
+template <int DT>
+__device__ __forceinline__ Piece piece_of(const Walk<QueryTiles<DT>>& w, const TileGeom& g, int b0, int b1) {
+  Piece d;
+  d.i = w.at.i;
+  d.h = w.at.h;
+  d.tok = w.r.start + w.at.t * w.geo.QT;
+  d.nq = g.nq;
+  d.P0 = g.P0;
+  d.L = w.r.L;
+  d.F = w.F;
+  d.kb = g.kb + b0;
+  d.nb = b1 - b0;
+  d.t_lo = g.t_lo;
+  d.t_hi = g.t_hi;
+  d.full_lo = seen_from(g.P0 + g.nq - 1, w.geo.W);
+  d.full_hi = seen_to(g.P0, w.r.L, w.F);
+  d.slot = b0 > 0 ? 2 * static_cast<int>(blockIdx.x) : b1 < g.nb ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
+  d.last = 0;
+  d.pad = 0;
+  return d;
+}
+
 // ---------------------------------------------------- a row, once more ----
 // Row r of a piece computed by the whole warp from the tokens it attends to.
 template <int DT>
-__device__ __noinline__ void redo_row(const ChunkAttnArgs& a, const Piece& p, int r) {
+__device__ __forceinline__ void redo_row(const ChunkAttnArgs& a, const Piece& p, int r) {
   const int lane = threadIdx.x & 31;
   const int G = a.n_q / a.pool.n_kv;
   const int j = r / G, g = p.h * G + r % G, P = p.P0 + j;
@@ -268,6 +300,41 @@ __device__ __noinline__ void redo_row(const ChunkAttnArgs& a, const Piece& p, in
     const long long to = (static_cast<long long>(p.tok + j) * a.n_q + g) * kD + 4 * lane;
     *reinterpret_cast<uint2*>(a.out + to * 2) =
         make_uint2(Io<DT>::pack(acc[0] * inv, acc[1] * inv), Io<DT>::pack(acc[2] * inv, acc[3] * inv));
+  }
+}
+
+// The rows of the range [begin, end) that were stored as not finite, computed
+// again, a row by each of the first kMendWarps warps (all of them call it,
+// behind a barrier after the range's last store).
+constexpr int kMendWarps = 8;
+template <int DT>
+__device__ __noinline__ void mend_rows(const ChunkAttnArgs& a, const Place& begin, const Place& end, int T) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.n_q / a.pool.n_kv;
+  const QueryTiles<DT> geo{kTileRows / G, a.pool.window};
+  Walk<QueryTiles<DT>> w(a.rows, geo, a.sc.prefix_lens, T, begin, end);
+  while (w.more()) {
+    const TileGeom g = geo.tile(w.r, w.F, w.at.t);
+    const Piece d = piece_of<DT>(w, g, w.from(), w.to(g.nb));
+#pragma unroll 1
+    for (int r = warp; r < d.nq * G; r += kMendWarps) {
+      float x[4];  // four dims of the row
+      if (d.slot >= 0) {
+        const float4 v = slot_acc(a, d.slot)[lane * kTileRows + r];
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+      } else {
+        const long long row = static_cast<long long>(d.tok + r / G) * a.n_q + d.h * G + r % G;
+        const uint2 v = *reinterpret_cast<const uint2*>(a.out + (row * kD + 4 * lane) * 2);
+        const float2 lo = Io<DT>::values(v.x), hi = Io<DT>::values(v.y);
+        x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+      }
+      float watch = 0.0f;  // NaN once a value is not finite
+#pragma unroll
+      for (int e = 0; e < 4; ++e) watch = fmaf(x[e], 0.0f, watch);
+      if (__any_sync(kFull, watch != 0.0f)) redo_row<DT>(a, d, r);
+    }
+    if (w.ends_here()) break;
+    w.next();
   }
 }
 
@@ -344,6 +411,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     prefetch_tensormap(&maps.vp);
     prefetch_tensormap(&qmap);
     tail.ctl[0] = 0;
+    tail.ctl[1] = 0;
   }
   if (tid < kNumBars) {
     const int b = tid;
@@ -385,7 +453,10 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   if (warp == 8) {  // before the test hook: the merge reads every range's record
     if (small)
       T = chunk_plan_warp(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, kSplitSnap<DT>, begin, end);
-    if (lane == 0) {  // the boundary at this range's start, for the merge
+    if (lane == 0) {  // the range, for mend_rows, and the boundary at its start, for the merge
+      tail.tiles = T;
+      tail.bounds[0] = begin;
+      tail.bounds[1] = end;
       Rec x{};
       x.inside = begin.h < a.pool.n_kv && begin.off > 0;
       if (x.inside) {
@@ -467,7 +538,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
             *reinterpret_cast<uint4*>(hi + kPart + o0) = l0;
             *reinterpret_cast<uint4*>(hi + kPart + o1) = l1;
           }
-          if (v == 1 && mend && odd) *(volatile int*)&tail.bad[x] = 1;
+          if (v == 1 && mend && odd) ctl[1] = 1;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
@@ -500,23 +571,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       const int tok = r.start + c.t * QT;
       if (p >= kDescs && !(ok = wait(kBDescEmpty + x, p / kDescs - 1))) break;
       if (lane == 0) {
-        Piece& d = tail.piece[x];
-        d.i = c.i;
-        d.h = c.h;
-        d.tok = tok;
-        d.nq = g.nq;
-        d.P0 = g.P0;
-        d.L = r.L;
-        d.F = w.F;
-        d.kb = g.kb + b0;
-        d.nb = b1 - b0;
-        d.t_lo = g.t_lo;
-        d.t_hi = g.t_hi;
-        d.full_lo = seen_from(g.P0 + g.nq - 1, a.pool.window);
-        d.full_hi = seen_to(g.P0, r.L, w.F);
-        d.slot = b0 > 0 ? 2 * static_cast<int>(blockIdx.x) : b1 < g.nb ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
-        d.last = 0;
-        tail.bad[x] = 0;
+        tail.piece[x] = piece_of<DT>(w, g, b0, b1);
         mbar_arrive(bar(kBDesc + x));
       }
       __syncwarp();
@@ -733,7 +788,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
           }
           bits = *reinterpret_cast<const uint32_t*>(&acc);
         }
-        if (__any_sync(kFull, (bits & 0x7FFF7FFFu) != 0u) && lane == 0) *(volatile int*)&tail.bad[x] = 1;
+        if (__any_sync(kFull, (bits & 0x7FFF7FFFu) != 0u) && lane == 0) ctl[1] = 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the zeroed rows
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBFull + s));
@@ -1103,7 +1158,6 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
           f0 *= inv;
           f1 *= inv;
           const long long row = static_cast<long long>(d.tok + jq) * a.n_q + g;
-          float watch = 0.0f;  // NaN once a value is not finite
 #pragma unroll 1
           for (int e = 0; e < 4; ++e) {
             float o[32];
@@ -1118,8 +1172,6 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
 #pragma unroll
               for (int u = 0; u < 32; ++u) o[u] = fmaf(f1, o1[u], o[u]);
             }
-#pragma unroll
-            for (int u = 0; u < 32; ++u) watch = fmaf(o[u], 0.0f, watch);
             if (valid) {
               if (d.slot >= 0) {
                 float4* acc = slot_acc(a, d.slot) + r;
@@ -1142,15 +1194,6 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
             else if (a.lse)
               a.lse[row] = (sub + log2f(l)) * kLn2;
           }
-          if (*(volatile int*)&tail.bad[x]) {
-            unsigned again = __ballot_sync(kFull, valid && watch != 0.0f);
-            __syncwarp();  // this warp's stores above come first
-            while (again) {
-              const int u = __ffs(again) - 1;
-              again &= again - 1;
-              redo_row<DT>(a, d, r - lane + u);
-            }
-          }
         }
         if (join && m == 0) {
           tc::fence_before();
@@ -1169,6 +1212,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     tc::fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
+  // (the warps with registers for it; a range that was given up has stored nothing to go by)
+  if (warp < kMendWarps && ctl[1] && !ctl[0]) mend_rows<DT>(a, tail.bounds[0], tail.bounds[1], tail.tiles);
 }
 
 // ---------------------------------------------------------------- merge ----
