@@ -10,7 +10,9 @@
 // weights: no exchange between threads, and a fixed order of additions.  The
 // K of 256 tokens of one (row, KV head) (a tile, in two halves m of 128) stay
 // in shared memory while the row's queries stream past, 128 rows a block.
-// q8_0 keys enter as two f16 parts, hi and lo (q8_tiles.cuh), two products.
+// q8_0 keys enter as two f16 parts, hi and lo (q8_tiles.cuh), two products; a
+// token with a block's scale of 512 or more enters times 2^-7, which keeps its
+// values in f16's range, and its scores are multiplied back.
 //
 // Warps: 0-3 and 4-7 sum the weights of half 0 and 1, 8 walks the work, 9
 // issues the products, 10 copies K pages, 11 copies queries and stages their
@@ -87,6 +89,7 @@ struct Tail {
   Place bounds[2];
   PlanScratch scratch;
   int tile_start[PKV_MAX_ROWS + 1];
+  float back[kDescs][kMassTok];  // q8_0: what a token's scores are multiplied by
 };
 constexpr size_t kSmemBytes = 1024 + kMassTail + sizeof(Tail);
 static_assert(kSmemBytes <= 232448, "");
@@ -344,7 +347,11 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
           uint8_t* hi = smem + s * kKBytes;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const __half2 s2 = __half2half2(sc[e]);
+            // the 8 lanes of a token agree
+            const unsigned large =
+                (__ballot_sync(kFull, (__half_as_ushort(sc[e]) & 0x7FFFu) >= kLargeScale) >> (lane & 24)) & 0xFFu;
+            const __half2 s2 = __hmul2(__half2half2(sc[e]), __float2half2_rn(large ? 0.0078125f : 1.0f));
+            if (col == 0) tail.back[x][128 * m + 16 * e + row] = large ? 128.0f : 1.0f;
             uint4 h0, l0, h1, l1;
             q8_split8(make_uint2(code[e].x, code[e].y), s2, h0, l0);
             q8_split8(make_uint2(code[e].z, code[e].w), s2, h1, l1);
@@ -502,6 +509,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) slope2[e] = __ldg(a.sc.slopes + d.h * G + (e & (G - 1))) * kLog2e;
       }
+      float c1t = c1;                 // GEN 0: with the token's `back` in it
       float sum = 0.0f, lost = 0.0f;  // the sum over blocks and its rounding error so far
       for (int b = 0; b < d.nb; ++b, ++gq) {
         const int s = gq % kLseSlots;
@@ -511,6 +519,10 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
         if (mine) {
           if (!(ok = wait(kBS + 2 * m + (used & 1), used >> 1))) break;
           tc::fence_after();
+          // written before the keys, which the scores come from
+          const float back = kQ8 && (GEN != 0 || b == 0) ? *(volatile float*)&tail.back[x][t - d.t0] : 1.0f;
+          if (kQ8 && GEN == 0 && b == 0) c1t = c1 * back;
+          const bool scaled = kQ8 && GEN != 0 && __any_sync(kFull, back != 1.0f);
           const uint32_t tS = tmem + lanes + 256 * m + 128 * (used & 1);
           const int j = (d.b0 + b) * QT;
           const int from = min(128, max(0, (jlo - j) * G)), to = min(128, max(0, (jhi - j) * G));
@@ -523,8 +535,13 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
           // pieces too short to hide each other's latency (two chunks of 1800
           // tokens 223 us instead of 163).
           auto weigh = [&](float (&v)[32], int q) {
-            float2 mul = make_float2(c1, c1);
+            const float c = kQ8 && GEN == 0 ? c1t : c1;
+            float2 mul = make_float2(c, c);
             float cq[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // GEN 1: the factor is q(v^2)
+            if (kQ8 && GEN != 0 && __builtin_expect(scaled, 0)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] *= back;
+            }
             if constexpr (GEN == 1) {
               if (__builtin_expect(cap.beyond(v), 0)) {
                 cap32(v, tS + 32 * q, cap_k, cap2);

@@ -61,7 +61,9 @@
 // A token that some rows of a tile attend to and others do not gets weight 0
 // in the latter, but 0 times a value that is not finite is not 0.  Warp 11
 // looks for such values in the blocks that are masked for part of the tile.
-// Where it finds one, the rows of the CTA's range that ended up not finite are
+// With q8_0, a block's scale of 512 or more may take a value out of f16's range
+// (q8_tiles.cuh): scores or outputs of the rows that meet it are not finite.
+// Where there is either, the rows of the CTA's range that ended up not finite are
 // computed again from the tokens they attend to alone (mend_rows), after the
 // pipeline has drained: a row takes a warp 5.6 us per 32 tokens (7.3 with four
 // loads in flight instead of eight), so that inside the pipeline a tile of a
@@ -154,7 +156,7 @@ static_assert(sizeof(Piece) == 64, "");
 struct Tail {
   uint64_t bars[kNumBars];
   Piece piece[kDescs];
-  volatile int ctl[2];  // abort; a masked V block held a value that is not finite
+  volatile int ctl[2];  // abort; there may be rows to compute again
   uint32_t tmem;
   int tiles;           // of the batch
   float2 half[kTileRows / 2];  // half 1's maximum and sum of each row
@@ -300,6 +302,7 @@ __device__ __forceinline__ void redo_row(const ChunkAttnArgs& a, const Piece& p,
     const long long to = (static_cast<long long>(p.tok + j) * a.n_q + g) * kD + 4 * lane;
     *reinterpret_cast<uint2*>(a.out + to * 2) =
         make_uint2(Io<DT>::pack(acc[0] * inv, acc[1] * inv), Io<DT>::pack(acc[2] * inv, acc[3] * inv));
+    if (a.lse && lane == 0) a.lse[static_cast<long long>(p.tok + j) * a.n_q + g] = (m + log2f(l)) * kLn2;
   }
 }
 
@@ -515,14 +518,16 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                               row * (kD / kQBlock) + (col >> 1);
           uint4 code[kPages];
           __half2 sc[kPages];
-          bool odd = false;
+          bool odd = false, large = false;
 #pragma unroll
           for (int e = 0; e < kPages; ++e) {  // token `row` of page e; 0 where no query of the tile attends
             const int t = t0 + e * kPage + row;
             const bool in = t >= d.t_lo && t < d.t_hi;
             code[e] = *reinterpret_cast<const uint4*>(raw + e * (kPage * kD));
             const __half f = in ? rsc[e * kPage * (kD / kQBlock)] : __float2half_rn(0.0f);
-            odd = odd || !(fabsf(__half2float(f)) <= 65504.0f);
+            const unsigned bits = __half_as_ushort(f) & 0x7FFFu;
+            odd = odd || bits >= kNotFinite;
+            large = large || (bits >= kLargeScale && bits < kNotFinite);
             sc[e] = __half2half2(f);
           }
           if (gs >= kS && !(ok = wait(kBEmpty + s, gs / kS - 1))) break;
@@ -538,7 +543,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
             *reinterpret_cast<uint4*>(hi + kPart + o0) = l0;
             *reinterpret_cast<uint4*>(hi + kPart + o1) = l1;
           }
-          if (v == 1 && mend && odd) ctl[1] = 1;
+          if (large || (v == 1 && mend && odd)) ctl[1] = 1;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {

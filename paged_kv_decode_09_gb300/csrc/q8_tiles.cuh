@@ -5,6 +5,10 @@
 // f16(scale * code) and lo = f16(scale * code - hi), exact but for lo's own
 // rounding (2^-22 of the value; values near f16's smallest keep its absolute
 // spacing), and a product takes both parts into the same accumulators.
+//
+// A scale below 512 keeps every value (128 codes of 511.75 are 65504) in f16's
+// range.  Beyond, hi is infinite and lo its opposite, and products that meet
+// them are NaN: the caller looks for such scales.
 #pragma once
 
 #include <cstdint>
@@ -12,6 +16,10 @@
 #include "pkv_device.cuh"
 
 namespace pkv {
+
+// Magnitudes of a scale's 16 bits: 512, and the smallest that is not finite.
+constexpr unsigned kLargeScale = 0x6000u;
+constexpr unsigned kNotFinite = 0x7C00u;
 
 // 8 codes (offset-binary bytes) times their block's scale (both halves of s):
 // the hi and lo parts of 8 dims.

@@ -11,6 +11,9 @@ from paged_kv_decode_09_gb300 import api
 pytestmark = pytest.mark.gpu
 
 SCALE = 1.0 / math.sqrt(128)
+ROWS = [(150, 340), (1, 70), (3, 50)]
+AT = (250, 33, 49)  # a token of each row: inside the chunk, before the only query, the last one
+KW = [{}, {"softcap": 30.0}, {"slope": 0.01}, {"slope": 0.01, "softcap": 30.0}]
 
 
 def test_rows_computed_again_do_not_stop_the_rest():
@@ -31,3 +34,104 @@ def test_rows_computed_again_do_not_stop_the_rest():
     c.pool.v_data[0, c.bt[0, (L - 1) // 16].long(), :, (L - 1) % 16, 5] = 0
     want, tol, wl, lt = R.attention(c, q, SCALE)
     assert ((out.double() - want).abs() <= tol)[:-1].all() and ((lse.double() - wl).abs() <= lt).all()
+
+
+# ------------------------------------------------------- q8_0: a block's scale may be any f16 ----
+def put(c, which, scale, code, block=1, dim=37):
+    """Token AT of each row: one 32-wide block of K or V is `code` in one dim and 0 in the others, under `scale`."""
+    for i, t in enumerate(AT):
+        page = c.bt[i, t // 16].long()
+        data, scales = getattr(c.pool, which + "_data")[0], getattr(c.pool, which + "_scales")[0]
+        data[page, :, t % 16, 32 * block:32 * block + 32] = 128
+        data[page, :, t % 16, dim] = 128 + code
+        scales[page, :, t % 16, block] = scale
+
+
+def queries(c, which):
+    q = c.normal(c.tokens, c.n_q, 128, dtype=torch.float16)
+    if which == "k":
+        q[..., 37] *= 2.0 ** -12  # scores of the size of the others
+    return q
+
+
+def zero_key(c):
+    """K of the tokens AT is 0: their weights stay far from 1, and V times weight within f16's range."""
+    for i, t in enumerate(AT):
+        c.pool.k_data[0][c.bt[i, t // 16].long(), :, t % 16] = 128
+
+
+def scores_of(c, kw):
+    a = {k: v for k, v in kw.items() if k == "softcap"}
+    if "slope" in kw:
+        a["slopes"] = torch.full((c.n_q,), kw["slope"], device=c.device)
+    return a
+
+
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("chunks", [1, 152])
+@pytest.mark.parametrize("kw", KW)
+@pytest.mark.parametrize("scale,code", [(511.5, -128), (512.0, 127), (600.0, -127), (-600.0, 127), (60000.0, 2)])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_large_q8_0_values(which, scale, code, kw, chunks, window):
+    """Stored values around and beyond f16's 65504, for queries that see them and queries that do not."""
+    c = R.Chunk(api.Q8_0, 2, 4, ROWS, seed=21)
+    c.pool.set_window(0, window)
+    q = queries(c, which)
+    if which == "v":
+        zero_key(c)
+    put(c, which, scale, code)
+    a = scores_of(c, kw)
+    out, lse = torch.empty(c.tokens, c.n_q, 128, dtype=torch.float16, device=c.device), \
+        torch.empty(c.tokens, c.n_q, device=c.device)
+    api.paged_chunk_attention(c.pool, 0, q, c.cu, c.bt, c.lens, SCALE, out=out, lse=lse,
+                              workspace=api.WorkspaceChunk(c.pool, c.n_q, chunks), **a)
+    want, tol, wl, lt = R.attention(c, q, SCALE, window=window, **a)
+    assert want.abs().max() < 65000
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    assert ((out.double() - want).abs() <= tol).all(), float(((out.double() - want).abs() - tol).max())
+    assert ((lse.double() - wl).abs() <= lt).all()
+    assert c.pool.read_status() == 0
+
+
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("kw", KW)
+@pytest.mark.parametrize("scale,code", [(511.5, -128), (512.0, 127), (600.0, -127), (-600.0, 127), (60000.0, 2)])
+def test_mass_of_large_q8_0_keys(scale, code, kw, window):
+    c = R.Chunk(api.Q8_0, 2, 4, ROWS, seed=22)
+    c.pool.set_window(0, window)
+    q = queries(c, "k")
+    put(c, "k", scale, code)
+    a = scores_of(c, kw)
+    lse = R.attention(c, q, SCALE, window=window, **a)[2].float()
+    before = torch.rand(3, 2, 340, device=c.device)
+    got = api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, mass_in=before,
+                                   mass_out=torch.empty_like(before), **a)
+    want, tol = R.mass(c, q, lse, SCALE, before, window=window, **a)
+    for i, (_, L) in enumerate(c.rows):
+        assert ((got[i, :, :L].double() - want[i, :, :L]).abs() <= tol[i, :, :L]).all(), i
+    assert c.pool.read_status() == 0
+
+
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("kw", KW)
+@pytest.mark.parametrize("scale,code", [(math.nan, 1), (math.inf, -3), (600.0, 127)])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_unseen_q8_0_values_never_reach_an_output(which, scale, code, kw, window):
+    """Queries before the token, and queries whose window has passed it, are as without it."""
+    c = R.Chunk(api.Q8_0, 2, 4, ROWS, seed=23)
+    c.pool.set_window(0, window)
+    q, a = queries(c, which), scores_of(c, kw)
+    if which == "v":
+        zero_key(c)
+    want, tol, wl, lt = R.attention(c, q, SCALE, window=window, **a)
+    put(c, which, scale, code)
+    lse = torch.empty(c.tokens, c.n_q, device=c.device)
+    out = api.paged_chunk_attention(c.pool, 0, q, c.cu, c.bt, c.lens, SCALE, lse=lse, **a)
+    for i, (n, L) in enumerate(ROWS):
+        s = int(c.cu[i])
+        pos = torch.arange(L - n, L, device=c.device)
+        sees = (pos >= AT[i]) & ((pos < AT[i] + window) | (window == 0))
+        off = s + torch.nonzero(~sees).flatten()
+        assert ((out.double() - want).abs() <= tol)[off].all() and ((lse.double() - wl).abs() <= lt)[off].all(), i
+        if not math.isfinite(scale):
+            assert not torch.isfinite(out[s + torch.nonzero(sees).flatten()][..., 37]).any()
