@@ -10,9 +10,13 @@
 // weights: no exchange between threads, and a fixed order of additions.  The
 // K of 256 tokens of one (row, KV head) (a tile, in two halves m of 128) stay
 // in shared memory while the row's queries stream past, 128 rows a block.
-// q8_0 keys enter as two f16 parts, hi and lo (q8_tiles.cuh), two products; a
-// token with a block's scale of 512 or more enters times 2^-7, which keeps its
-// values in f16's range, and its scores are multiplied back.
+// q8_0 keys enter as two f16 parts, hi and lo (q8_tiles.cuh), two products.  A
+// token with a value beyond f16's range gets a sum that is not a number; it is
+// left out, and summed in fp32 after the pipeline has drained (mend_tokens).
+// Such tokens are rare, and looking for them earlier costs every call: votes of
+// the splitting warps 49 -> 51.5 us for the last queries' call, a warp of its own
+// 58.7; scaling them down for the products and their scores back up 186 -> 194
+// for whole chunks.
 //
 // Warps: 0-3 and 4-7 sum the weights of half 0 and 1, 8 walks the work, 9
 // issues the products, 10 copies K pages, 11 copies queries and stages their
@@ -30,8 +34,10 @@
 // the second kernel adds in order.
 #include <atomic>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 
+#include "attend_row.cuh"
 #include "chunk_device.cuh"
 #include "chunk_plan.cuh"
 #include "q8_tiles.cuh"
@@ -82,16 +88,17 @@ static_assert(sizeof(Piece) == 64, "");
 struct Tail {
   uint64_t bars[kNumBars];
   Piece piece[kDescs];
-  float lse2[kLseSlots][128];  // minus the lse of a block's rows in base 2, -inf: not counted
+  alignas(16) float lse2[kLseSlots][128];  // minus the lse of a block's rows in base 2, -inf: not counted
   int odd[kLseSlots];          // the block has a row that is not counted
-  volatile int ctl[2];
+  volatile int ctl[2];  // abort; q8_0: sums were left out
   uint32_t tmem;
-  Place bounds[2];
+  int tiles;        // of the batch
+  Place bounds[2];  // the CTA's range
   PlanScratch scratch;
   int tile_start[PKV_MAX_ROWS + 1];
-  float back[kDescs][kMassTok];  // q8_0: what a token's scores are multiplied by
 };
 constexpr size_t kSmemBytes = 1024 + kMassTail + sizeof(Tail);
+static_assert(offsetof(Tail, lse2) % 16 == 0 && kMassTail % 16 == 0, "read four at a time");
 static_assert(kSmemBytes <= 232448, "");
 
 // Tokens t * 256 .. of a row, and the blocks of the queries that attend to
@@ -138,6 +145,100 @@ __device__ __forceinline__ float* slot_sums(const MassArgs& a, int slot) {
 template <int DT>
 constexpr int kMassThreads = DT == PKV_KV_Q8_0 ? 512 : 384;
 
+// The partial slot of blocks [from, to) of a tile's in this CTA's range, -1: all.
+__device__ __forceinline__ int slot_of(int from, int to, int blocks) {
+  const int cta = static_cast<int>(blockIdx.x);
+  return from > 0 ? 2 * cta : to < blocks ? 2 * cta + 1 : -1;
+}
+
+// The sum of token t of row i (of L tokens, n of them new) and KV head h, over
+// a whole tile or the part of it in `slot`.
+__device__ __forceinline__ void store_sum(const MassArgs& a, int slot, int i, int h, int t, int L, int n, float sum) {
+  if (slot >= 0) {
+    slot_sums(a, slot)[t % kMassTok] = sum;
+  } else {
+    const long long at = (static_cast<long long>(i) * a.pool.n_kv + h) * a.mass_stride + t;
+    a.mass_out[at] = (a.mass_in && t < L - n ? a.mass_in[at] : 0.0f) + sum;
+  }
+}
+
+// Token t of row i as a row of 128 dims in the pool's layer, for KV head h.
+__device__ __forceinline__ long long token_row(const MassArgs& a, int i, int h, int t) {
+  int pg = __ldg(a.rows.block_table + static_cast<long long>(i) * a.rows.bt_stride + t / kPage);
+  if (pg < 0 || pg >= a.pool.num_pages) pg = 0;  // as the products read it
+  return (static_cast<long long>(pg) * a.pool.n_kv + h) * kPage + t % kPage;
+}
+
+// Dims 4 u .. 4 u + 3 of a q8_0 token; one is beyond what q8_split8 takes (as
+// one that is not finite is).
+__device__ __forceinline__ bool key4(const MassArgs& a, long long row, int u, float (&k)[4]) {
+  const float scale = __half2float(__ldg(reinterpret_cast<const __half*>(a.pool.k_scales) + 4 * row + (u >> 3)));
+  const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(a.pool.k_data + row * kD) + u);
+  bool beyond = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    k[e] = scale * (static_cast<float>((codes >> (8 * e)) & 255u) - 128.0f);
+    beyond = beyond || !(fabsf(k[e]) < 65520.0f);
+  }
+  return beyond;
+}
+
+// A thread's token t has such a value: its sum is left to mend_tokens.  (Where no
+// query attends to the token its sum is 0, in both.)
+__device__ __noinline__ bool token_beyond(const MassArgs& a, int i, int h, int t) {
+  const long long row = token_row(a, i, h, t);
+  bool beyond = false;
+#pragma unroll 1
+  for (int u = 0; u < kD / 4; ++u) {
+    float k[4];
+    beyond = key4(a, row, u, k) || beyond;
+  }
+  return beyond;
+}
+
+// The sums of such tokens over the range [begin, end), in fp32 from the stored
+// codes: a token by each warp of the CTA (all of them call it), 4 dims a lane.
+__device__ __noinline__ void mend_tokens(const MassArgs& a, const TokenTiles& geo, const Place& begin,
+                                         const Place& end, int T) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int G = a.n_q / a.pool.n_kv;
+  Walk<TokenTiles> w(a.rows, geo, a.sc.prefix_lens, T, begin, end);
+  while (w.more()) {
+    const RowInfo& r = w.r;
+    const int i = w.at.i, h = w.at.h;
+    int b0, b1;
+    geo.range(r, w.F, w.at.t, b0, b1);
+    const int from = w.from(), to = w.to(b1 - b0), slot = slot_of(from, to, b1 - b0);
+    const int j0 = geo.first_query(r) + (b0 + from) * geo.QT, j1 = min(r.n, j0 + (to - from) * geo.QT);
+#pragma unroll 1
+    for (int t = w.at.t * kMassTok + warp; to > from && t < min(r.L, (w.at.t + 1) * kMassTok); t += warps) {
+      float k[4];
+      if (!__any_sync(kFull, key4(a, token_row(a, i, h, t), lane, k))) continue;
+      float sum = 0.0f, lost = 0.0f;
+#pragma unroll 1
+      for (int c = j0 * G; c < j1 * G; ++c) {
+        const int j = c / G, g = h * G + c % G, P = r.L - r.n + j;
+        const float lse = __ldg(a.lse + static_cast<long long>(r.start + j) * a.n_q + g);
+        if (t < seen_from(P, geo.W) || t >= seen_to(P, r.L, w.F) || !(fabsf(lse) <= 3.0e38f)) continue;
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(
+            a.q + ((r.start + j) * a.q_stride + static_cast<long long>(g) * kD + 4 * lane) * 2));
+        const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&q.x));
+        const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&q.y));
+        float dot = fmaf(hi.y, k[3], fmaf(hi.x, k[2], fmaf(lo.y, k[1], lo.x * k[0])));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+        const float s = score2(dot, a.sc.scale, a.sc.softcap, a.sc.slopes ? __ldg(a.sc.slopes + g) : 0.0f, abs(P - t));
+        const float y = exp2f(s - lse * kLog2e) - lost, z = sum + y;
+        lost = (z - sum) - y;
+        sum = z;
+      }
+      if (lane == 0) store_sum(a, slot, i, h, t, r.L, r.n, sum);
+    }
+    if (w.ends_here()) break;
+    w.next();
+  }
+}
+
 // GEN: 0 plain scores; 1 capped; 2 with a distance bias, capped or not.
 template <int DT, int GEN>
 __global__ void __launch_bounds__(kMassThreads<DT>, 1)
@@ -161,6 +262,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
     prefetch_tensormap(&maps.kp);
     prefetch_tensormap(&qmap);
     tail.ctl[0] = 0;
+    tail.ctl[1] = 0;
   }
   if (tid < kNumBars) {
     const int b = tid;
@@ -195,7 +297,10 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
   Place begin = tail.bounds[0], end = tail.bounds[1];  // of a small call: made by warp 8
   if (warp == 8) {  // before the test hook: the merge reads every range's record
     if (small) T = chunk_plan_warp(a.rows, a.pool.n_kv, geo, a.sc.prefix_lens, a.chunks, 1, begin, end);
-    if (lane == 0) {  // the boundary at this range's start, for the merge
+    if (lane == 0) {  // the range, for mend_tokens, and the boundary at its start, for the merge
+      tail.tiles = T;
+      tail.bounds[0] = begin;
+      tail.bounds[1] = end;
       Rec x{};
       x.inside = begin.h < a.pool.n_kv && begin.off > 0;
       if (x.inside) {
@@ -243,8 +348,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
         d.F = w.F;
         d.b0 = b0 + from;
         d.nb = to - from;
-        d.slot = from > 0 ? 2 * static_cast<int>(blockIdx.x)
-                 : to < b1 - b0 ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
+        d.slot = slot_of(from, to, b1 - b0);
         d.last = 0;
         mbar_arrive(bar(kBDesc + x));
       }
@@ -347,11 +451,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
           uint8_t* hi = smem + s * kKBytes;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            // the 8 lanes of a token agree
-            const unsigned large =
-                (__ballot_sync(kFull, (__half_as_ushort(sc[e]) & 0x7FFFu) >= kLargeScale) >> (lane & 24)) & 0xFFu;
-            const __half2 s2 = __hmul2(__half2half2(sc[e]), __float2half2_rn(large ? 0.0078125f : 1.0f));
-            if (col == 0) tail.back[x][128 * m + 16 * e + row] = large ? 128.0f : 1.0f;
+            const __half2 s2 = __half2half2(sc[e]);
             uint4 h0, l0, h1, l1;
             q8_split8(make_uint2(code[e].x, code[e].y), s2, h0, l0);
             q8_split8(make_uint2(code[e].z, code[e].w), s2, h1, l1);
@@ -509,7 +609,6 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) slope2[e] = __ldg(a.sc.slopes + d.h * G + (e & (G - 1))) * kLog2e;
       }
-      float c1t = c1;                 // GEN 0: with the token's `back` in it
       float sum = 0.0f, lost = 0.0f;  // the sum over blocks and its rounding error so far
       for (int b = 0; b < d.nb; ++b, ++gq) {
         const int s = gq % kLseSlots;
@@ -519,10 +618,6 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
         if (mine) {
           if (!(ok = wait(kBS + 2 * m + (used & 1), used >> 1))) break;
           tc::fence_after();
-          // written before the keys, which the scores come from
-          const float back = kQ8 && (GEN != 0 || b == 0) ? *(volatile float*)&tail.back[x][t - d.t0] : 1.0f;
-          if (kQ8 && GEN == 0 && b == 0) c1t = c1 * back;
-          const bool scaled = kQ8 && GEN != 0 && __any_sync(kFull, back != 1.0f);
           const uint32_t tS = tmem + lanes + 256 * m + 128 * (used & 1);
           const int j = (d.b0 + b) * QT;
           const int from = min(128, max(0, (jlo - j) * G)), to = min(128, max(0, (jhi - j) * G));
@@ -535,13 +630,8 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
           // pieces too short to hide each other's latency (two chunks of 1800
           // tokens 223 us instead of 163).
           auto weigh = [&](float (&v)[32], int q) {
-            const float c = kQ8 && GEN == 0 ? c1t : c1;
-            float2 mul = make_float2(c, c);
+            float2 mul = make_float2(c1, c1);
             float cq[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // GEN 1: the factor is q(v^2)
-            if (kQ8 && GEN != 0 && __builtin_expect(scaled, 0)) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] *= back;
-            }
             if constexpr (GEN == 1) {
               if (__builtin_expect(cap.beyond(v), 0)) {
                 cap32(v, tS + 32 * q, cap_k, cap2);
@@ -638,12 +728,10 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
       }
       if (!ok) break;
       if (mine && t < d.L) {
-        if (d.slot >= 0) {
-          slot_sums(a, d.slot)[t - d.t0] = sum;
-        } else {
-          const long long at = (static_cast<long long>(d.i) * a.pool.n_kv + d.h) * a.mass_stride + t;
-          a.mass_out[at] = (a.mass_in && t < d.L - d.n ? a.mass_in[at] : 0.0f) + sum;
-        }
+        if (kQ8 && __builtin_expect(!(fabsf(sum) <= 3.0e38f), 0) && token_beyond(a, d.i, d.h, t))
+          ctl[1] = 1;
+        else
+          store_sum(a, d.slot, d.i, d.h, t, d.L, d.n, sum);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
@@ -655,6 +743,9 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
   if (warp == 9) {
     tc::fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+  if constexpr (kQ8) {
+    if (ctl[1] && !ctl[0]) mend_tokens(a, geo, tail.bounds[0], tail.bounds[1], tail.tiles);
   }
 }
 
