@@ -62,7 +62,8 @@ enum : int {
   kBKEmpty = kBKFull + kKBufs,
   kBQFull = kBKEmpty + kKBufs,
   kBQEmpty = kBQFull + kQSlots,
-  kBLse = kBQEmpty + kQSlots,
+  kBQLand = kBQEmpty + kQSlots,  // queries that are cleared behind the row's
+  kBLse = kBQLand + 1,
   kBLseEmpty = kBLse + kLseSlots,
   kBS = kBLseEmpty + kLseSlots,  // [half][buffer]
   kBSFree = kBS + 4,
@@ -473,6 +474,8 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
   } else if (warp == 11) {
     // ---------------------------------------------------- queries and lse ----
     int gq = 0;
+    uint32_t landed = 0;   // blocks that were cleared
+    bool landing = false;  // the wait for one was given up
     bool ok = true;
     for (int p = 0; ok; ++p) {
       const int x = p % kDescs;
@@ -482,6 +485,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
       for (int b = 0; b < d.nb; ++b, ++gq) {
         const int s = gq % kQSlots;
         const int j = (d.b0 + b) * QT;  // first query of the block, from d.tok
+        const int own = (d.nq - j) * G;  // rows of the row's queries
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -489,9 +493,28 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
           v[e] = jj < d.nq ? __ldg(a.lse + static_cast<long long>(d.tok + jj) * a.n_q + d.h * G + c % G) : INFINITY;
         }
         if (gq >= kQSlots && !(ok = wait(kBQEmpty + s, gq / kQSlots - 1))) break;
+        // A cap's arithmetic is chosen by the scores of a block, so the rows behind
+        // (another row's queries, or tokens of no row) are cleared first.
+        const bool clear = GEN == 1 && own < 128;
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar(kBQFull + s), kBuf);
-          tc::load_rows(sbase + kQRing + s * kBuf, &qmap, d.h * G, d.tok + j, bar(kBQFull + s));
+          const uint32_t to = clear ? bar(kBQLand) : bar(kBQFull + s);
+          mbar_arrive_expect_tx(to, kBuf);
+          tc::load_rows(sbase + kQRing + s * kBuf, &qmap, d.h * G, d.tok + j, to);
+        }
+        if (clear) {
+          __syncwarp();
+          ok = wait(kBQLand, landed);
+          landing = !ok;
+          if (!ok) break;
+          ++landed;
+          uint8_t* rows = smem + kQRing + s * kBuf;  // 128 bytes of a row in either half
+          for (int e = 8 * own + lane; e < 8 * 128; e += 32) {
+            reinterpret_cast<uint4*>(rows)[e] = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4*>(rows + kBuf / 2)[e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBQFull + s));
         }
         bool odd = false;
 #pragma unroll
@@ -516,6 +539,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
       if (lane == 0) mbar_arrive(bar(kBDescEmpty + x));
     }
     const int zero = 0;  // the last copies land before the CTA ends
+    if (lane == 0 && landing) mbar_wait_bounded(bar(kBQLand), landed & 1u, &zero);
     if (lane == 0)
       for (int g = max(0, gq - kQSlots); g < gq; ++g)
         mbar_wait_bounded(bar(kBQFull + g % kQSlots), (g / kQSlots) & 1, &zero);
@@ -633,7 +657,7 @@ __global__ void __launch_bounds__(kMassThreads<DT>, 1)
             float2 mul = make_float2(c1, c1);
             float cq[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // GEN 1: the factor is q(v^2)
             if constexpr (GEN == 1) {
-              if (__builtin_expect(cap.beyond(v), 0)) {
+              if (__builtin_expect(cap.beyond(v, cap.limit(t < d.L)), 0)) {
                 cap32(v, tS + 32 * q, cap_k, cap2);
                 cq[0] = 1.0f;
               } else {

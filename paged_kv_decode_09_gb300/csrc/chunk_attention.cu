@@ -984,6 +984,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         for (int b = !kTurns || two ? 0 : m; b < d.nb; b += every, ++blocks, begun = true) {
           const int t0 = block(d.kb, d.nb, b) * N;
           const bool fast = __all_sync(kFull, t0 >= lo && t0 + N <= hi);
+          const float near = GEN == 1 ? cap.limit(valid, fast) : 0.0f;
           if (!(ok = wait(kBS + m, blocks))) break;
           tc::fence_after();
           if (any) {
@@ -1026,7 +1027,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
               float bias = 0.0f, step = 0.0f;  // of the group's first column; per column
               float cq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
               if constexpr (GEN == 1) {
-                if (__builtin_expect(cap.beyond(v, fast), 0)) {
+                if (__builtin_expect(cap.beyond(v, near), 0)) {
                   cap32(v, tS + 32 * group, cap_k, cap2);
                   cq[0] = 1.0f;
                 } else {

@@ -1,6 +1,8 @@
 // score32.cuh — capped scores, 32 at a time.
 #pragma once
 
+#include <cmath>
+
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -25,15 +27,21 @@ struct NearCap {
     }
     most = fabsf(k) > 1e-4f && fabsf(k) < 1e4f && fabsf(cap2) < 1e9f ? 0.35f / fabsf(k) : -1.0f;
   }
-  // a value of the warp is not near (or no k is), or `near` is not asked for
-  __device__ __forceinline__ bool beyond(const float (&v)[32], bool near = true) const {
+  // The largest magnitude that lets a lane take the near form, or the other
+  // always.  The two differ in their last bits, so what does not count towards a
+  // result must not choose between them: a lane of no row takes no part.
+  __device__ __forceinline__ float limit(bool live, bool near = true) const {
+    return !live ? INFINITY : near ? most : -1.0f;
+  }
+  // a value of the warp is beyond its lane's limit
+  static __device__ __forceinline__ bool beyond(const float (&v)[32], float limit) {
     float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
       m0 = tc::max3(m0, fabsf(v[e]), fabsf(v[e + 1]));
       m1 = tc::max3(m1, fabsf(v[e + 2]), fabsf(v[e + 3]));
     }
-    return __any_sync(kFull, fmaxf(m0, m1) > (near ? most : -1.0f));
+    return __any_sync(kFull, fmaxf(m0, m1) > limit);
   }
 };
 
@@ -43,8 +51,9 @@ constexpr float kTanhNear = 0.7f;
 // polynomial of degree 5 (1.4e-8).  A group with a value beyond takes
 // 1 - 2 / (1 + e^2z) for such values, which loses the low bits of small ones, in
 // a loop over 16 columns of tensor memory (tS: the columns that v was loaded
-// from, free to be written): few instructions, seldom run.  Not finite stays
-// not finite, or +-cap2.
+// from, free to be written): few instructions, seldom run.  A near value gets
+// the same bits there, whatever the others are.  Not finite stays not finite,
+// or +-cap2.
 __device__ __forceinline__ void cap32(float (&v)[32], uint32_t tS, float k, float cap2) {
   constexpr float kQ[6] = {1.0f, -0.333331257f, 0.133283168f, -0.0535204448f, 0.0200115982f, -0.00507791527f};
   float m0 = 0.0f, m1 = 0.0f;
@@ -65,11 +74,11 @@ __device__ __forceinline__ void cap32(float (&v)[32], uint32_t tS, float k, floa
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float x = __uint_as_float(w[e]), z = x * k, z2 = z * z;
-        float q = kQ[5];
+        float q = kc * kQ[5];
 #pragma unroll
-        for (int i = 4; i >= 0; --i) q = fmaf(q, z2, kQ[i]);
+        for (int i = 4; i >= 0; --i) q = fmaf(q, z2, kc * kQ[i]);
         const float t = 1.0f - __fdividef(2.0f, 1.0f + tc::ex2(z * 2.8853900817779268f));
-        w[e] = __float_as_uint(fabsf(z) <= kTanhNear ? x * kc * q : t * cap2);
+        w[e] = __float_as_uint(fabsf(z) <= kTanhNear ? x * q : t * cap2);
       }
       tc::st16(tS + c, w);
     }

@@ -135,3 +135,56 @@ def test_unseen_q8_0_values_never_reach_an_output(which, scale, code, kw, window
         assert ((out.double() - want).abs() <= tol)[off].all() and ((lse.double() - wl).abs() <= lt)[off].all(), i
         if not math.isfinite(scale):
             assert not torch.isfinite(out[s + torch.nonzero(sees).flatten()][..., 37]).any()
+
+
+# ------------------------------------------------------------------------ caps ----
+@pytest.mark.parametrize("kw", [{"softcap": 30.0}, {"slope": 0.02, "softcap": 30.0}])
+@pytest.mark.parametrize("kv", [api.F16, api.BF16, api.Q8_0])
+def test_capped_scores_do_not_depend_on_what_is_not_seen(kv, kw):
+    """Keys behind a row's end, keys that come after a query, and queries behind the last row may hold anything:
+    the same bits come out (a cap's arithmetic is chosen for groups of scores together)."""
+    rows = [(70, 250), (1, 301), (3, 77), (1, 1)]
+    c = R.Chunk(kv, 2, 4, rows, seed=24, behind=30)
+    a = scores_of(c, kw)
+    a["prefix_lens"] = torch.tensor([400, 0, 100, 9], dtype=torch.int32, device=c.device)
+    n = int(c.cu[-1])
+    q = c.normal(c.tokens, c.n_q, 128, dtype=R.IO[kv])
+    one = 128 + 127 if kv == api.Q8_0 else 1.0
+
+    def fill(big, last):
+        """Slots behind the rows' ends and queries behind the last row: 0, or far beyond the cap."""
+        for i, (_, L) in enumerate(rows):
+            page = c.bt[i, (L - 1) // 16].long()
+            c.pool.k_data[0, page, :, (L - 1) % 16 + 1:] = one
+            if kv == api.Q8_0:
+                c.pool.k_scales[0, page, :, (L - 1) % 16 + 1:] = 100.0 * big
+            else:
+                c.pool.k_data[0, page, :, (L - 1) % 16 + 1:] *= 1000.0 * big
+        q[n:] = 1000.0 * big
+        page = c.bt[0, 249 // 16].long()  # the last token of row 0's chunk
+        if last is not None:
+            c.pool.k_data[0, page, :, 249 % 16] = 128 if kv == api.Q8_0 else last
+
+    def both():
+        lse = torch.zeros(c.tokens, c.n_q, device=c.device)
+        out = torch.zeros_like(q)
+        api.paged_chunk_attention(c.pool, 0, q, c.cu, c.bt, c.lens, SCALE, out=out, lse=lse, **a)
+        mass = torch.zeros(4, 2, 310, device=c.device)
+        api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, mass_out=mass, last_queries=40, **a)
+        return out, lse, mass
+
+    fill(0.0, None)
+    want = both()
+    fill(1.0, None)
+    got = both()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    # no prefix: a key that only the last query of row 0 sees
+    a["prefix_lens"] = torch.zeros(4, dtype=torch.int32, device=c.device)
+    if kv != api.Q8_0:
+        fill(0.0, 0.0)
+        want = both()
+        fill(0.0, 500.0)
+        got = both()
+        for x, y in zip(got[:2], want[:2]):
+            assert torch.equal(x[:69], y[:69]) and torch.equal(x[70:], y[70:])
