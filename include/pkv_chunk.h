@@ -174,13 +174,14 @@ pkv_status paged_attention_mass(const pkv_pool *pool, int layer, const void *q, 
  *   keep_idx         int32 [num_rows][n_kv_heads][keep_stride]
  *   dst_mass         fp32 [num_rows][n_kv_heads][keep_stride] or NULL; not mass
  *   new_lens         int32 [num_rows], not seq_lens itself
- * keep_lens below 0 or above what keep_stride and dst_bt_stride hold, and rows
- * with L_i < 0 or beyond bt_stride or mass_stride, record PKV_DEV_BAD_LENGTH
- * and are clamped.  Entries and slots behind B_i are left as they are.  Block
- * table entries outside the pool record PKV_DEV_BAD_PAGE; that token is not
- * copied.  The kept tokens of different heads differ, so slots no longer are
- * positions: distance biases, windows and prefixes do not apply to an evicted
- * row; keys rotated before they were stored keep their angles.
+ * keep_lens below 0, a B_i above what keep_stride and dst_bt_stride hold, and
+ * rows with L_i < 0 or beyond bt_stride or mass_stride, record
+ * PKV_DEV_BAD_LENGTH and are clamped; keep_lens itself may be any budget.
+ * Entries and slots behind B_i are left as they are.  Block table entries
+ * outside the pool record PKV_DEV_BAD_PAGE; that token is not copied.  The kept
+ * tokens of different heads differ, so slots no longer are positions: distance
+ * biases, windows and prefixes do not apply to an evicted row; keys rotated
+ * before they were stored keep their angles.
  * Two launches. */
 pkv_status kv_evict(const pkv_pool *pool, int layer, const float *mass, int mass_stride,
                     const int32_t *block_table, int bt_stride, const int32_t *seq_lens,

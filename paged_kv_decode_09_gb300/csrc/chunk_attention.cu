@@ -89,21 +89,10 @@ template <int DT>
 constexpr int kBlockTok = DT == PKV_KV_Q8_0 ? 64 : 128;  // cached tokens of a block
 template <int DT>
 constexpr int kAttnThreads = DT == PKV_KV_Q8_0 ? 512 : kPlanThreads;
-#ifndef PKV_CHUNK_TILE_COST
-#define PKV_CHUNK_TILE_COST 3
-#endif
-#ifndef PKV_CHUNK_SMALL_COST
-#define PKV_CHUNK_SMALL_COST 10
-#endif
-#ifndef PKV_CHUNK_SNAP
-#define PKV_CHUNK_SNAP 1
-#endif
-// What a tile costs besides its blocks, and how far from a tile's end a
-// boundary moves there, in blocks (chunk_plan).
+// How far from a tile's end a boundary moves there, in blocks (chunk_plan): with
+// q8_0's blocks of 64 tokens, from one block away; with blocks of 128, never.
 template <int DT>
-constexpr int kTileCost = PKV_CHUNK_TILE_COST * (128 / kBlockTok<DT>);
-template <int DT>
-constexpr int kSplitSnap = PKV_CHUNK_SNAP * (128 / kBlockTok<DT>);
+constexpr int kSplitSnap = 128 / kBlockTok<DT>;
 template <int DT>
 constexpr int kSlots = DT == PKV_KV_Q8_0 ? 4 : 5;    // ring slots
 constexpr int kMaxSlots = 5;
@@ -199,7 +188,7 @@ struct QueryTiles {
     return DT == PKV_KV_Q8_0 || 2 * (r.n - t * QT) > QT ? 4 : 2;
   }
   __device__ __forceinline__ int lead(int weight) const {
-    return (weight == 4 ? 4 * PKV_CHUNK_TILE_COST : PKV_CHUNK_SMALL_COST) * (128 / kBlockTok<DT>);
+    return (weight == 4 ? 12 : 10) * (128 / kBlockTok<DT>);
   }
 };
 

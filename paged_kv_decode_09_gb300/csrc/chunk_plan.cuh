@@ -56,14 +56,6 @@ __device__ __forceinline__ T cta_scan(T x, T* tmp, T& total) {
   return pre + v - x;
 }
 
-// The plan of the call, made by every CTA (all its threads, kPlanThreads or
-// more, call it; `tile_start` holds num_rows + 1 ints and may be reused afterwards).
-// The U units of the batch are cut into C = min(chunks, U / kMostWeight) ranges,
-// range k from floor(k U / C), so that no two boundaries fall on one block; a boundary less than `snap` blocks from an end of its tile
-// moves there, since a split tile costs a partial state and its merge.  Writes
-// the boundaries blockIdx.x and blockIdx.x + 1 to bounds[0], bounds[1], and
-// returns the number of tiles.  The threads share out the tiles in contiguous
-// runs, so that their work is the same whatever the rows' lengths.
 // The block that comes next at unit u of a tile.
 __device__ __forceinline__ int block_of(unsigned u, unsigned lead, unsigned w) {
   return u < lead ? 0 : static_cast<int>((u - lead) / w);
@@ -80,6 +72,17 @@ __device__ __forceinline__ int row_of_tile(const int* tile_start, int rows, int 
   }
   return lo;
 }
+
+// The plan of the call, made by every CTA (all its threads, kPlanThreads or
+// more, call it; `tile_start` holds num_rows + 1 ints and may be reused
+// afterwards).  The U units of the batch are cut into C = min(chunks, U /
+// kMostWeight) ranges, range k from floor(k U / C), so that no two boundaries
+// fall on one block.  A boundary less than `snap` blocks from an end of its tile
+// moves there, since a split tile costs a partial state and its merge (1: none
+// does, a boundary being at a block's start).  Writes the boundaries blockIdx.x
+// and blockIdx.x + 1 to bounds[0], bounds[1], and returns the number of tiles.
+// The threads share out the tiles in contiguous runs, so that their work is the
+// same whatever the rows' lengths.
 template <typename Geo>
 __device__ __forceinline__ int chunk_plan(const ChunkRows& rows, int n_kv, const Geo& geo, const int32_t* prefix_lens,
                                           int chunks, int snap, int* tile_start, PlanScratch* tmp, Place* bounds) {

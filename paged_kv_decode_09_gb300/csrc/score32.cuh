@@ -48,7 +48,7 @@ struct NearCap {
 constexpr float kTanhNear = 0.7f;
 
 // v = cap2 * tanh(k v) for any v, for the warp's 32 lanes: |k v| <= 0.7 by a
-// polynomial of degree 5 (1.4e-8).  A group with a value beyond takes
+// polynomial of degree 5 (off by 2.8e-8 of the value).  A group with a value beyond takes
 // 1 - 2 / (1 + e^2z) for such values, which loses the low bits of small ones, in
 // a loop over 16 columns of tensor memory (tS: the columns that v was loaded
 // from, free to be written): few instructions, seldom run.  A near value gets

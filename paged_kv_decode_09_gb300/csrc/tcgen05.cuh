@@ -202,18 +202,6 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const void* tmap, int y,
       : "memory");
 }
 
-__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // The long end of a wait: false once *abort is set or after kWaitLimitNs.
 __device__ __forceinline__ bool wait_on_here(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
   const unsigned long long t0 = global_ns();
