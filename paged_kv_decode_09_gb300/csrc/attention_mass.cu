@@ -215,24 +215,40 @@ __device__ __noinline__ void mend_tokens(const MassArgs& a, const TokenTiles& ge
     for (int t = w.at.t * kMassTok + warp; to > from && t < min(r.L, (w.at.t + 1) * kMassTok); t += warps) {
       float k[4];
       if (!__any_sync(kFull, key4(a, token_row(a, i, h, t), lane, k))) continue;
+      // 32 (query, head) columns at a time, whose loads go out together; lane u
+      // weighs column u and sums its own
       float sum = 0.0f, lost = 0.0f;
 #pragma unroll 1
-      for (int c = j0 * G; c < j1 * G; ++c) {
-        const int j = c / G, g = h * G + c % G, P = r.L - r.n + j;
-        const float lse = __ldg(a.lse + static_cast<long long>(r.start + j) * a.n_q + g);
-        if (t < seen_from(P, geo.W) || t >= seen_to(P, r.L, w.F) || !(fabsf(lse) <= 3.0e38f)) continue;
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(
-            a.q + ((r.start + j) * a.q_stride + static_cast<long long>(g) * kD + 4 * lane) * 2));
-        const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&q.x));
-        const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&q.y));
-        float dot = fmaf(hi.y, k[3], fmaf(hi.x, k[2], fmaf(lo.y, k[1], lo.x * k[0])));
+      for (int c0 = j0 * G; c0 < j1 * G; c0 += 32) {
+        const int c = c0 + lane, j = c / G, g = h * G + c % G, P = r.L - r.n + j;
+        float lse = INFINITY, mine = 0.0f;
+        if (c < j1 * G && t >= seen_from(P, geo.W) && t < seen_to(P, r.L, w.F))
+          lse = __ldg(a.lse + static_cast<long long>(r.start + j) * a.n_q + g);
+        const bool counts = fabsf(lse) <= 3.0e38f;
+        if (!__any_sync(kFull, counts)) continue;
+        const int n = min(32, j1 * G - c0);
+#pragma unroll 8
+        for (int u = 0; u < n; ++u) {
+          const int cu = c0 + u;
+          const uint2 q = __ldg(reinterpret_cast<const uint2*>(
+              a.q + ((r.start + cu / G) * a.q_stride + static_cast<long long>(h * G + cu % G) * kD + 4 * lane) * 2));
+          const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&q.x));
+          const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&q.y));
+          float dot = fmaf(hi.y, k[3], fmaf(hi.x, k[2], fmaf(lo.y, k[1], lo.x * k[0])));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-        const float s = score2(dot, a.sc.scale, a.sc.softcap, a.sc.slopes ? __ldg(a.sc.slopes + g) : 0.0f, abs(P - t));
-        const float y = exp2f(s - lse * kLog2e) - lost, z = sum + y;
-        lost = (z - sum) - y;
-        sum = z;
+          for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+          mine = u == lane ? dot : mine;
+        }
+        if (counts) {
+          const float s =
+              score2(mine, a.sc.scale, a.sc.softcap, a.sc.slopes ? __ldg(a.sc.slopes + g) : 0.0f, abs(P - t));
+          const float y = exp2f(s - lse * kLog2e) - lost, z = sum + y;
+          lost = (z - sum) - y;
+          sum = z;
+        }
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
       if (lane == 0) store_sum(a, slot, i, h, t, r.L, r.n, sum);
     }
     if (w.ends_here()) break;

@@ -63,11 +63,11 @@
 // looks for such values in the blocks that are masked for part of the tile.
 // With q8_0, a block's scale of 512 or more may take a value out of f16's range
 // (q8_tiles.cuh): scores or outputs of the rows that meet it are not finite.
-// Where there is either, the rows of the CTA's range that ended up not finite are
+// Where there is either, the rows of the piece that ended up not finite are
 // computed again from the tokens they attend to alone (mend_rows), after the
-// pipeline has drained: a row takes a warp 5.6 us per 32 tokens (7.3 with four
-// loads in flight instead of eight), so that inside the pipeline a tile of a
-// row of 150K tokens would run the other warps' waits out of their limit.
+// pipeline has drained: a query takes a warp microseconds per 32 tokens, so that
+// inside the pipeline a tile of a long row would run the other warps' waits out
+// of their limit.
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -107,6 +107,7 @@ constexpr uint32_t kRawScaleBytes = 64 * (kD / kQBlock) * 2;
 constexpr uint32_t kTail = kRing + kMaxSlots * kHalf;   // barriers and descriptors
 static_assert(kRawScales + kRaws * kRawScaleBytes <= kTail, "");
 constexpr int kDescs = 4;
+constexpr int kMendBits = 1024;                      // pieces of a range told apart by mend_rows
 constexpr uint32_t kTmemS = 0, kTmemO = 256;         // S_m at 128 m, O_m at 256 + 128 m
 
 // barriers
@@ -148,6 +149,7 @@ struct Tail {
   volatile int ctl[2];  // abort; there may be rows to compute again
   uint32_t tmem;
   int tiles;           // of the batch
+  uint32_t notes[kMendBits / 32];  // the pieces with such rows (note_piece)
   float2 half[kTileRows / 2];  // half 1's maximum and sum of each row
   Place bounds[2];     // the CTA's range
   PlanScratch scratch;
@@ -270,60 +272,72 @@ __device__ __forceinline__ Piece piece_of(const Walk<QueryTiles<DT>>& w, const T
   return d;
 }
 
-// ---------------------------------------------------- a row, once more ----
-// Row r of a piece computed by the whole warp from the tokens it attends to.
-template <int DT>
-__device__ __forceinline__ void redo_row(const ChunkAttnArgs& a, const Piece& p, int r) {
-  const int lane = threadIdx.x & 31;
-  const int G = a.n_q / a.pool.n_kv;
-  const int j = r / G, g = p.h * G + r % G, P = p.P0 + j;
-  const int t0 = max(seen_from(P, a.pool.window), p.kb * kBlockTok<DT>);
-  const int t1 = min(seen_to(P, p.L, p.F), (p.kb + p.nb) * kBlockTok<DT>);
-  const float slope = a.sc.slopes ? __ldg(a.sc.slopes + g) : 0.0f;
-  float m, l, acc[4];
-  attend_row<DT>(a.pool, a.rows, a.sc, p.i, p.h, slope, P,
-                 a.q + ((p.tok + j) * a.q_stride + static_cast<long long>(g) * kD) * 2, t0, t1, m, l, acc);
-  if (p.slot >= 0) {
-    slot_acc(a, p.slot)[lane * kTileRows + r] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    if (lane == 0) slot_ml(a, p.slot)[r] = make_float2(m, l);
-  } else {
-    const float inv = 1.0f / l;
-    const long long to = (static_cast<long long>(p.tok + j) * a.n_q + g) * kD + 4 * lane;
-    *reinterpret_cast<uint2*>(a.out + to * 2) =
-        make_uint2(Io<DT>::pack(acc[0] * inv, acc[1] * inv), Io<DT>::pack(acc[2] * inv, acc[3] * inv));
-    if (a.lse && lane == 0) a.lse[static_cast<long long>(p.tok + j) * a.n_q + g] = (m + log2f(l)) * kLn2;
-  }
+// ------------------------------------------------- queries, once more ----
+// The pieces of the range with something to mend: a bit each, those from the last
+// bit on together.
+__device__ __forceinline__ void note_piece(uint32_t* notes, int p) {
+  const int b = min(p, kMendBits - 1);
+  atomicOr(notes + b / 32, 1u << (b % 32));
 }
 
-// The rows of the range [begin, end) that were stored as not finite, computed
-// again, a row by each of the first kMendWarps warps (all of them call it,
-// behind a barrier after the range's last store).
+// The rows of the noted pieces of the range [begin, end) that were stored as not
+// finite, computed again in fp32 from the tokens they attend to: a query by each
+// of the first kMendWarps warps (all of them call it, behind a barrier after the
+// range's last store).
 constexpr int kMendWarps = 8;
 template <int DT>
-__device__ __noinline__ void mend_rows(const ChunkAttnArgs& a, const Place& begin, const Place& end, int T) {
+__device__ __noinline__ void mend_rows(const ChunkAttnArgs& a, const uint32_t* notes, const Place& begin,
+                                       const Place& end, int T) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.n_q / a.pool.n_kv;
   const QueryTiles<DT> geo{kTileRows / G, a.pool.window};
   Walk<QueryTiles<DT>> w(a.rows, geo, a.sc.prefix_lens, T, begin, end);
-  while (w.more()) {
+  for (int p = 0; w.more(); ++p) {
     const TileGeom g = geo.tile(w.r, w.F, w.at.t);
     const Piece d = piece_of<DT>(w, g, w.from(), w.to(g.nb));
+    const int bit = min(p, kMendBits - 1);
+    const int queries = notes[bit / 32] >> (bit % 32) & 1u ? d.nq : 0;
 #pragma unroll 1
-    for (int r = warp; r < d.nq * G; r += kMendWarps) {
-      float x[4];  // four dims of the row
-      if (d.slot >= 0) {
-        const float4 v = slot_acc(a, d.slot)[lane * kTileRows + r];
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-      } else {
-        const long long row = static_cast<long long>(d.tok + r / G) * a.n_q + d.h * G + r % G;
-        const uint2 v = *reinterpret_cast<const uint2*>(a.out + (row * kD + 4 * lane) * 2);
-        const float2 lo = Io<DT>::values(v.x), hi = Io<DT>::values(v.y);
-        x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
-      }
-      float watch = 0.0f;  // NaN once a value is not finite
+    for (int j = warp; j < queries; j += kMendWarps) {
+      const long long row = static_cast<long long>(d.tok + j) * a.n_q + d.h * G;  // of its first head
+      unsigned bad = 0;  // heads
+#pragma unroll 1
+      for (int u = 0; u < G; ++u) {
+        float x[4];  // four dims of the row
+        if (d.slot >= 0) {
+          const float4 v = slot_acc(a, d.slot)[lane * kTileRows + j * G + u];
+          x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(a.out + ((row + u) * kD + 4 * lane) * 2);
+          const float2 lo = Io<DT>::values(v.x), hi = Io<DT>::values(v.y);
+          x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+        }
+        float watch = 0.0f;  // NaN once a value is not finite
 #pragma unroll
-      for (int e = 0; e < 4; ++e) watch = fmaf(x[e], 0.0f, watch);
-      if (__any_sync(kFull, watch != 0.0f)) redo_row<DT>(a, d, r);
+        for (int e = 0; e < 4; ++e) watch = fmaf(x[e], 0.0f, watch);
+        bad |= __any_sync(kFull, watch != 0.0f) ? 1u << u : 0u;
+      }
+      if (!bad) continue;
+      const int P = d.P0 + j;
+      const int t0 = max(seen_from(P, a.pool.window), d.kb * kBlockTok<DT>);
+      const int t1 = min(seen_to(P, d.L, d.F), (d.kb + d.nb) * kBlockTok<DT>);
+      float m[4], l[4], acc[4][4];
+      attend_query<DT>(a.pool, a.rows, a.sc, d.i, d.h, G, P,
+                       a.q + ((d.tok + j) * a.q_stride + static_cast<long long>(d.h) * G * kD) * 2, t0, t1, m, l, acc);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (!(bad >> u & 1u)) continue;
+        if (d.slot >= 0) {
+          const int r = j * G + u;
+          slot_acc(a, d.slot)[lane * kTileRows + r] = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+          if (lane == 0) slot_ml(a, d.slot)[r] = make_float2(m[u], l[u]);
+        } else {
+          const float inv = 1.0f / l[u];
+          *reinterpret_cast<uint2*>(a.out + ((row + u) * kD + 4 * lane) * 2) = make_uint2(
+              Io<DT>::pack(acc[u][0] * inv, acc[u][1] * inv), Io<DT>::pack(acc[u][2] * inv, acc[u][3] * inv));
+          if (a.lse && lane == 0) a.lse[row + u] = (m[u] + log2f(l[u])) * kLn2;
+        }
+      }
     }
     if (w.ends_here()) break;
     w.next();
@@ -405,6 +419,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     tail.ctl[0] = 0;
     tail.ctl[1] = 0;
   }
+  if (tid < kMendBits / 32) tail.notes[tid] = 0;
   if (tid < kNumBars) {
     const int b = tid;
     int count = 1;
@@ -532,7 +547,10 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
             *reinterpret_cast<uint4*>(hi + kPart + o0) = l0;
             *reinterpret_cast<uint4*>(hi + kPart + o1) = l1;
           }
-          if (large || (v == 1 && mend && odd)) ctl[1] = 1;
+          if (large || (v == 1 && mend && odd)) {
+            ctl[1] = 1;
+            note_piece(tail.notes, p);
+          }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
@@ -782,7 +800,10 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
           }
           bits = *reinterpret_cast<const uint32_t*>(&acc);
         }
-        if (__any_sync(kFull, (bits & 0x7FFF7FFFu) != 0u) && lane == 0) ctl[1] = 1;
+        if (__any_sync(kFull, (bits & 0x7FFF7FFFu) != 0u) && lane == 0) {
+          ctl[1] = 1;
+          note_piece(tail.notes, p);
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the zeroed rows
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBFull + s));
@@ -1208,7 +1229,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
   // (the warps with registers for it; a range that was given up has stored nothing to go by)
-  if (warp < kMendWarps && ctl[1] && !ctl[0]) mend_rows<DT>(a, tail.bounds[0], tail.bounds[1], tail.tiles);
+  if (warp < kMendWarps && ctl[1] && !ctl[0]) mend_rows<DT>(a, tail.notes, tail.bounds[0], tail.bounds[1], tail.tiles);
 }
 
 // ---------------------------------------------------------------- merge ----

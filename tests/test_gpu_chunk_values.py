@@ -18,8 +18,8 @@ KW = [{}, {"softcap": 30.0}, {"slope": 0.01}, {"slope": 0.01, "softcap": 30.0}]
 
 def test_rows_computed_again_do_not_stop_the_rest():
     """A value that is not finite in the last token of a long row: the 252 (query, head) rows of the tile that do
-    not attend to it are computed again, two KV heads by one CTA.  That takes longer than a wait's limit (a second):
-    no wait may stand behind it."""
+    not attend to it are computed again, two KV heads by one CTA.  Row by row in the middle of the pipeline that
+    took 1.5 seconds a head, beyond the limit of the waits behind it (a second)."""
     n, L = 64, 200_000
     c = R.Chunk(api.F16, 2, 4, [(n, L)], seed=31)
     c.pool.v_data[0, c.bt[0, (L - 1) // 16].long(), :, (L - 1) % 16, 5] = math.inf
