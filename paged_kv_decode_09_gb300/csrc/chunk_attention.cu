@@ -46,11 +46,13 @@
 // S_m.  Scores in steps of 64 tokens, each computed while the step before is in
 // its softmax, take that chain apart, but the scores' products then cost half
 // as much again and the steps their own hand-overs: 381 us instead of 376.
-// 8191 tokens of 32 heads in bf16 376 us, 1460 TFLOP/s; with a window of 4096
-// over rows of 14K to 16K 195 us, 1230 TFLOP/s; 2048 tokens over 32049 in q8_0
-// 1.40 ms (twice the products; 745 TFLOP/s of useful work).  Single tokens of 8
-// rows of 1K to 6K are bound by K and V's bytes: 22.4 us, 4.1 TB/s, of which
-// some 10 are the launches, the plan, the last blocks and the merge.  The CTAs
+// 8191 tokens of 32 heads in bf16 371 us, 1480 TFLOP/s; with a window of 4096
+// over rows of 14K to 16K 194 us, 1240 TFLOP/s; 2048 tokens over 32049 in q8_0
+// 1.38 ms (twice the products; 757 TFLOP/s of useful work).  Single tokens of 8
+// rows of 1K to 6K in f16 are bound by K and V's bytes: 22.2 us, 4.1 TB/s, of
+// which some 10 are the launches, the plan, the last blocks and the merge.  In
+// q8_0 they take 45.3 us for half the bytes: no turns, blocks of 64 tokens, and
+// the splitting of each block stands in its chain.  The CTAs
 // of the prompt are busy for 351 to 364 us, 356 in the mean.
 //
 // The work of the batch is a line of (KV head, tile, block) units, cut into
@@ -185,6 +187,8 @@ struct QueryTiles {
   // Units: 4 a block, 2 in a tile of up to 128 rows (half the arithmetic); 12
   // and 10 a tile.  A batch of two chunks and 30 single tokens takes 122 us, 142
   // at 3 units for the smaller blocks, 156 at 4.  q8_0 has no turns to gain by.
+  // (Measured on plain scores; with a cap or a bias a block costs up to half as
+  // much again.)
   static constexpr int kMostWeight = 4;
   __device__ __forceinline__ int weight(const RowInfo& r, int t) const {
     return DT == PKV_KV_Q8_0 || 2 * (r.n - t * QT) > QT ? 4 : 2;
