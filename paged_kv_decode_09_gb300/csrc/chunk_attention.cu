@@ -46,12 +46,12 @@
 // S_m.  Scores in steps of 64 tokens, each computed while the step before is in
 // its softmax, take that chain apart, but the scores' products then cost half
 // as much again and the steps their own hand-overs: 381 us instead of 376.
-// 8191 tokens of 32 heads in bf16 371 us, 1480 TFLOP/s; with a window of 4096
+// 8191 tokens of 32 heads in bf16 373 us, 1475 TFLOP/s; with a window of 4096
 // over rows of 14K to 16K 194 us, 1240 TFLOP/s; 2048 tokens over 32049 in q8_0
-// 1.38 ms (twice the products; 757 TFLOP/s of useful work).  Single tokens of 8
-// rows of 1K to 6K in f16 are bound by K and V's bytes: 22.2 us, 4.1 TB/s, of
+// 1.37 ms (twice the products; 761 TFLOP/s of useful work).  Single tokens of 8
+// rows of 1K to 6K in f16 are bound by K and V's bytes: 22.1 us, 4.2 TB/s, of
 // which some 10 are the launches, the plan, the last blocks and the merge.  In
-// q8_0 they take 45.3 us for half the bytes: no turns, blocks of 64 tokens, and
+// q8_0 they take 45.8 us for half the bytes: no turns, blocks of 64 tokens, and
 // the splitting of each block stands in its chain.  The CTAs
 // of the prompt are busy for 351 to 364 us, 356 in the mean.
 //

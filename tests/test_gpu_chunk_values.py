@@ -36,6 +36,28 @@ def test_rows_computed_again_do_not_stop_the_rest():
     assert ((out.double() - want).abs() <= tol)[:-1].all() and ((lse.double() - wl).abs() <= lt).all()
 
 
+@pytest.mark.parametrize("kv", [api.F16, api.BF16])
+def test_pieces_beyond_those_told_apart(kv):
+    """1400 pieces in one CTA's range, values that are not finite in the first and the last ones: the queries before
+    such a value are whole in every row."""
+    rows = [(2, 19 + i % 5) for i in range(700)]
+    c = R.Chunk(kv, 2, 2, rows, seed=32)
+    q = c.normal(c.tokens, c.n_q, 128, dtype=R.IO[kv])
+    want, tol, wl, lt = R.attention(c, q, SCALE)
+    bad = (0, 5, 350, 650, 698, 699)
+    for i in bad:
+        L = rows[i][1]
+        c.pool.v_data[0, c.bt[i, (L - 1) // 16].long(), :, (L - 1) % 16, 9] = math.nan
+    lse = torch.empty(c.tokens, c.n_q, device=c.device)
+    out = api.paged_chunk_attention(c.pool, 0, q, c.cu, c.bt, c.lens, SCALE, lse=lse,
+                                    workspace=api.WorkspaceChunk(c.pool, c.n_q, 1))
+    sees = torch.tensor([2 * i + 1 for i in bad], device=c.device)
+    assert torch.isnan(out[sees][..., 9]).all()
+    out[sees] = want[sees].to(out.dtype)
+    assert ((out.double() - want).abs() <= tol).all() and ((lse.double() - wl).abs() <= lt).all()
+    assert c.pool.read_status() == 0
+
+
 # ------------------------------------------------------- q8_0: a block's scale may be any f16 ----
 def put(c, which, scale, code, block=1, dim=37):
     """Token AT of each row: one 32-wide block of K or V is `code` in one dim and 0 in the others, under `scale`."""
@@ -109,6 +131,35 @@ def test_mass_of_large_q8_0_keys(scale, code, kw, window):
     want, tol = R.mass(c, q, lse, SCALE, before, window=window, **a)
     for i, (_, L) in enumerate(c.rows):
         assert ((got[i, :, :L].double() - want[i, :, :L]).abs() <= tol[i, :, :L]).all(), i
+    assert c.pool.read_status() == 0
+
+
+@pytest.mark.parametrize("group", [1, 2])
+def test_large_q8_0_values_of_other_groups(group):
+    """One and two query heads a KV head; every tenth token has values beyond f16's range, in K and in V."""
+    c = R.Chunk(api.Q8_0, 2, group, [(300, 900), (1, 77)], seed=25)
+    q = queries(c, "k")
+    for i, (_, L) in enumerate(c.rows):
+        t = torch.arange(3, L, 10, device=c.device)
+        page = c.bt[i][t // 16].long()
+        for name, scale in (("k", 700.0), ("v", -900.0)):
+            data, scales = getattr(c.pool, name + "_data")[0], getattr(c.pool, name + "_scales")[0]
+            data[page, :, t % 16, 32:64] = 128
+            data[page, :, t % 16, 37] = 128 + 100
+            scales[page, :, t % 16, 1] = scale
+    lse = torch.empty(c.tokens, c.n_q, device=c.device)
+    out = api.paged_chunk_attention(c.pool, 0, q, c.cu, c.bt, c.lens, SCALE, lse=lse)
+    want, tol, wl, lt = R.attention(c, q, SCALE)
+    over = want.abs() - tol >= 65520  # infinite in f16
+    assert (out[over].double() == want[over].sign() * math.inf).all()
+    held = want.abs() + tol < 65504
+    assert ((out.double() - want).abs() <= tol)[held].all() and ((lse.double() - wl).abs() <= lt).all()
+    assert held.float().mean() > 0.99
+    mass = torch.rand(2, 2, 900, device=c.device)
+    want, tol = R.mass(c, q, lse, SCALE, mass)
+    api.paged_attention_mass(c.pool, 0, q, lse, c.cu, c.bt, c.lens, SCALE, mass_in=mass)  # in place
+    for i, (_, L) in enumerate(c.rows):
+        assert ((mass[i, :, :L].double() - want[i, :, :L]).abs() <= tol[i, :, :L]).all(), i
     assert c.pool.read_status() == 0
 
 
