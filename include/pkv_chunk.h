@@ -106,8 +106,9 @@ typedef struct pkv_scores {
  * q_dtype before they meet V, and the output once.  Skipped rows get zeros
  * and an lse of -inf (rows with invalid cu_seqlens get nothing).  Values of
  * tokens a query does not attend to never reach its output, whatever they
- * are.  Queries that attend to a q8_0 value beyond f16's 65504, or share a tile
- * with one that attends to a value that is not finite, take a slower path.  A
+ * are.  Queries that meet a q8_0 value beyond f16's 65504, and those that share
+ * a tile with one that attends to a value that is not finite, take a slow path
+ * (a hundred times the time, in fp32).  A
  * block-table entry outside the pool records PKV_DEV_BAD_PAGE and page
  * 0 is read instead.
  *   workspace  paged_chunk_workspace_bytes(pool, n_q_heads, num_chunks) bytes,

@@ -52,8 +52,8 @@
 // rows of 1K to 6K in f16 are bound by K and V's bytes: 22.1 us, 4.2 TB/s, of
 // which some 10 are the launches, the plan, the last blocks and the merge.  In
 // q8_0 they take 45.8 us for half the bytes: no turns, blocks of 64 tokens, and
-// the splitting of each block stands in its chain.  The CTAs
-// of the prompt are busy for 351 to 364 us, 356 in the mean.
+// the splitting of each block stands in its chain.  The CTAs of the prompt are
+// busy for 351 to 364 us, 356 in the mean.
 //
 // The work of the batch is a line of (KV head, tile, block) units, cut into
 // equal ranges, one per CTA (chunk_plan.cuh).  A tile that crosses a boundary
