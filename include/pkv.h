@@ -74,6 +74,7 @@ extern "C" {
 #define PKV_HEAD_DIM 128
 #define PKV_Q8_BLOCK 32
 #define PKV_MAX_ROWS 2048 /* rows per call (per-CTA row tables live in shared memory) */
+#define PKV_MAX_SINKS (1 << 30) /* first tokens of a row that stay visible under a window */
 #define PKV_MAX_CHUNKS (1 << 24) /* work chunks per call (PKV_ERR_UNSUPPORTED above) */
 
 typedef enum pkv_status {
@@ -89,6 +90,7 @@ typedef enum pkv_status {
 #define PKV_DEV_BAD_PAGE 1u   /* block-table entry outside [0, num_pages): page 0 read instead, or write skipped */
 #define PKV_DEV_BAD_LENGTH 2u /* seq_lens[i] < 0 or > 16 * bt_stride: clamped */
 #define PKV_DEV_TIMEOUT 4u    /* a bounded wait on a shared-memory barrier gave up */
+#define PKV_DEV_BAD_TREE 8u   /* a parent or accepted leaf outside its row's tree: taken as -1 */
 
 /* How long (ns) a warp of the attention kernels waits on a shared-memory
  * barrier (a tile copy, a peer warp) before the kernel gives up. */
@@ -145,6 +147,20 @@ void kv_pool_destroy(pkv_pool *pool);
  * call is queued; kv_append is unaffected.  W < 0 -> PKV_ERR_INVALID_ARG. */
 pkv_status kv_pool_set_window(pkv_pool *pool, int layer, int window);
 pkv_status kv_pool_get_window(const pkv_pool *pool, int layer, int *window);
+
+/* Sinks of a layer: the first S tokens of a row that stay visible under the
+ * layer's window.  With window W > 0 and S > 0, a query at position P attends to
+ * t <= P with t > P - W or t < S; the pages between the sinks and the window are
+ * not read, and their block-table entries may be anything.  Without a window
+ * sinks change nothing.  S = 0 (the default) is none; S outside [0,
+ * PKV_MAX_SINKS] -> PKV_ERR_INVALID_ARG.  Host-side descriptor state, read when
+ * a call is queued.  paged_decode_attention, paged_decode_attention_static,
+ * pkv_decode_step, paged_chunk_attention and paged_tree_attention serve layers
+ * with sinks; the two-launch form (paged_decode_split), the several-query calls
+ * (paged_decode_attention_mq, pkv_decode_step_mq: take paged_chunk_attention) and
+ * paged_attention_mass return PKV_ERR_UNSUPPORTED on them. */
+pkv_status kv_pool_set_sinks(pkv_pool *pool, int layer, int sinks);
+pkv_status kv_pool_get_sinks(const pkv_pool *pool, int layer, int *sinks);
 
 /* Test hook, not part of the method: it lets the kernels' give-up path be
  * run on a real GPU, with no hang and no fault.  With stall_ns > 0, every

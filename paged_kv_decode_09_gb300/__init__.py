@@ -16,6 +16,7 @@ _API_NAMES = {
     "paged_decode_plan", "paged_decode_combine", "paged_decode_split", "decode_step", "workspace_bytes",
     "default_chunks", "status_string", "library_path", "Workspace", "BF16", "F32", "kv_rope_append",
     "paged_chunk_attention", "WorkspaceChunk", "paged_attention_mass", "WorkspaceMass", "kv_evict",
+    "paged_tree_attention", "kv_tree_commit",
 }
 
 

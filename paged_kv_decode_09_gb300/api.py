@@ -30,7 +30,7 @@ _lib = None
 
 STATUS_NAMES = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED",
                 3: "PKV_ERR_CAPACITY", 4: "PKV_ERR_WORKSPACE", 5: "PKV_ERR_CUDA"}
-DEV_BAD_PAGE, DEV_BAD_LENGTH, DEV_TIMEOUT = 1, 2, 4
+DEV_BAD_PAGE, DEV_BAD_LENGTH, DEV_TIMEOUT, DEV_BAD_TREE = 1, 2, 4, 8
 
 
 class PkvError(RuntimeError):
@@ -95,6 +95,11 @@ _SIGS = {
     "paged_attention_mass": ([_vp, _i, _vp, _ll, _i, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _i, _vp,
                               _vp, _i, _vp, _sz, _i, _vp], _i),
     "kv_evict": ([_vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp], _i),
+    "kv_pool_set_sinks": ([_vp, _i, _i], _i),
+    "kv_pool_get_sinks": ([_vp, _i, ctypes.POINTER(_i)], _i),
+    "paged_tree_attention": ([_vp, _i, _vp, _ll, _i, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp,
+                              _sz, _i, _vp], _i),
+    "kv_tree_commit": ([_vp, _i, _i, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp], _i),
     "pkv_status_string": ([_i], ctypes.c_char_p),
     "pkv_last_error_message": ([], ctypes.c_char_p),
 }
@@ -213,6 +218,15 @@ class KVPool:
         w = ctypes.c_int(0)
         _check(lib().kv_pool_get_window(self.handle, layer, ctypes.byref(w)), "kv_pool_get_window")
         return w.value
+
+    def set_sinks(self, layer: int, sinks: int):
+        """First tokens of a row that stay visible under the window of `layer` (0: none)."""
+        _check(lib().kv_pool_set_sinks(self.handle, layer, sinks), "kv_pool_set_sinks")
+
+    def sinks(self, layer: int) -> int:
+        n = ctypes.c_int(0)
+        _check(lib().kv_pool_get_sinks(self.handle, layer, ctypes.byref(n)), "kv_pool_get_sinks")
+        return n.value
 
     def read_status(self, stream=None) -> int:
         """Synchronise and return (and clear) the device status word."""
@@ -424,7 +438,7 @@ def paged_decode_combine(seq_lens, n_q_heads: int, n_kv_heads: int, bt_stride: i
     return out
 
 
-# ------------------------------------------------------------- long prompts ----
+# ------------------------------------------ long prompts and drafted trees ----
 # The kernels behind these calls take a few microseconds for a decode step, so their arguments are looked at
 # with few attribute reads; what does not fit is looked at again by _need, for its message.
 _KIND = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
@@ -584,12 +598,8 @@ def _q_type(pool):
     return torch.bfloat16 if pool.dtype == BF16 else torch.float16
 
 
-def paged_chunk_attention(pool: KVPool, layer: int, q, cu_seqlens, block_table, seq_lens, scale: float, *,
-                          softcap: float = 0.0, slopes=None, prefix_lens=None, out=None, lse=None,
-                          workspace: WorkspaceChunk | None = None, stream=None):
-    """Attention of a ragged chunk over the paged cache (paged_chunk_attention in pkv_chunk.h): q
-    [tokens][n_q][128] in bf16 for bf16 pools and f16 for f16 and q8_0 pools.  Returns out, like q; `lse`
-    (fp32 [tokens][n_q]) receives the log of the softmax denominators."""
+def _chunk_attention(name, pool, layer, q, parents, cu_seqlens, block_table, seq_lens, scale, softcap, slopes,
+                     prefix_lens, out, lse, workspace, stream):
     bt, stride = _table(block_table, "block_table", None, pool)
     rows = block_table.shape[0]
     dtype = _q_type(pool)
@@ -601,13 +611,61 @@ def paged_chunk_attention(pool: KVPool, layer: int, q, cu_seqlens, block_table, 
     lp = _optional(lse, torch.float32, "lse", (tokens, n_q), pool)
     sc = _Scores(scale, softcap, _optional(slopes, torch.float32, "slopes", (n_q,), pool),
                  _optional(prefix_lens, torch.int32, "prefix_lens", (rows,), pool))
+    tree = () if parents is None else (_array(parents, torch.int32, "parents", (tokens,), pool),)
     if workspace is None:
         workspace = _made(stream, WorkspaceChunk, pool, n_q)
-    _call("paged_chunk_attention", pool, stream, pool.handle, layer, qp, qs, _KIND[dtype],
+    _call(name, pool, stream, pool.handle, layer, qp, qs, _KIND[dtype], *tree,
           _array(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), pool), tokens, bt, stride,
           _array(seq_lens, torch.int32, "seq_lens", (rows,), pool), rows, n_q, ctypes.addressof(sc), op, lp,
           *_scratch(workspace, pool))
     return out
+
+
+def paged_chunk_attention(pool: KVPool, layer: int, q, cu_seqlens, block_table, seq_lens, scale: float, *,
+                          softcap: float = 0.0, slopes=None, prefix_lens=None, out=None, lse=None,
+                          workspace: WorkspaceChunk | None = None, stream=None):
+    """Attention of a ragged chunk over the paged cache (paged_chunk_attention in pkv_chunk.h): q
+    [tokens][n_q][128] in bf16 for bf16 pools and f16 for f16 and q8_0 pools.  Returns out, like q; `lse`
+    (fp32 [tokens][n_q]) receives the log of the softmax denominators."""
+    return _chunk_attention("paged_chunk_attention", pool, layer, q, None, cu_seqlens, block_table, seq_lens, scale,
+                            softcap, slopes, prefix_lens, out, lse, workspace, stream)
+
+
+def paged_tree_attention(pool: KVPool, layer: int, q, parents, cu_seqlens, block_table, seq_lens, scale: float, *,
+                         softcap: float = 0.0, out=None, lse=None, workspace: WorkspaceChunk | None = None,
+                         stream=None):
+    """Attention of a tree of drafted tokens per row over the paged cache (paged_tree_attention in
+    pkv_tree.h): the rows' new tokens are the trees, parents int32 [tokens] their parents within the row (-1:
+    the context).  The rest is paged_chunk_attention's."""
+    if parents is None:
+        raise TypeError("parents must be a torch.Tensor")
+    return _chunk_attention("paged_tree_attention", pool, layer, q, parents, cu_seqlens, block_table, seq_lens, scale,
+                            softcap, None, None, out, lse, workspace, stream)
+
+
+def kv_tree_commit(pool: KVPool, parents, leaves, cu_seqlens, block_table, seq_lens, *, first_layer: int = 0,
+                   num_layers: int | None = None, path=None, new_lens=None, stream=None):
+    """Keep the branch of each row's drafted tree that ends in token leaves[i] (-1: none) as the row's next
+    tokens (kv_tree_commit in pkv_tree.h), in all layers unless told otherwise.  `path` (int32 [rows][stride])
+    receives the branch's tokens.  Returns new_lens, int32 [rows]."""
+    bt, stride = _table(block_table, "block_table", None, pool)
+    rows = block_table.shape[0]
+    if not isinstance(parents, torch.Tensor) or parents.dim() != 1:
+        raise ValueError("parents must be a tensor [tokens]")
+    tokens = parents.shape[0]
+    if path is not None and (not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[0] != rows):
+        raise ValueError("path must be a tensor [rows][stride]")
+    lens = _array(seq_lens, torch.int32, "seq_lens", (rows,), pool)
+    if new_lens is None:
+        new_lens = _made(stream, torch.empty_like, seq_lens)
+    _call("kv_tree_commit", pool, stream, pool.handle, first_layer,
+          pool.num_layers - first_layer if num_layers is None else num_layers,
+          _array(parents, torch.int32, "parents", (tokens,), pool),
+          _array(leaves, torch.int32, "leaves", (rows,), pool),
+          _array(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), pool), tokens, bt, stride, lens, rows,
+          None if path is None else _array(path, torch.int32, "path", path.shape, pool),
+          1 if path is None else path.shape[1], _array(new_lens, torch.int32, "new_lens", (rows,), pool))
+    return new_lens
 
 
 def paged_attention_mass(pool: KVPool, layer: int, q, lse, cu_seqlens, block_table, seq_lens, scale: float, *,

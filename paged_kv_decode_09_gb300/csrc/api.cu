@@ -34,12 +34,16 @@ struct pkv_pool {
   std::atomic<int>* ready;   // [num_layers]: 1 once maps[layer] is valid
   std::mutex maps_mutex;
   int* window;               // [num_layers]: sliding window of the layer (0: none)
+  int* sinks;                // [num_layers]: first tokens that stay visible under it
   unsigned long long test_stall_ns = 0;  // test hook (kv_pool_set_test_stall); 0: off
   ~pkv_pool() {
     delete[] maps;
     delete[] ready;
     delete[] window;
+    delete[] sinks;
   }
+  // the sinks of a layer, where its window leaves any tokens out
+  int sinks_of(int layer) const { return window[layer] > 0 ? sinks[layer] : 0; }
 };
 
 namespace {
@@ -204,6 +208,9 @@ pkv_status attention_impl(const pkv_pool* pool, int layer, const float* q, const
     return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   if (!aligned(workspace, 256)) return fail(PKV_ERR_INVALID_ARG, "workspace not 256-byte aligned");
 
+  // paged_decode_combine plans the pieces again from the window alone
+  if (mode == Mode::kSplitOnly && pool->sinks_of(layer) > 0)
+    return fail(PKV_ERR_UNSUPPORTED, "layer %d has sinks: paged_decode_attention serves them", layer);
   const int g = n_q / pool->n_kv;
   const WsParts w = workspace_parts(workspace, workspace_bytes, num_rows, n_q, pool->n_kv, num_chunks);
   pkv::DecodeArgs a;
@@ -223,6 +230,7 @@ pkv_status attention_impl(const pkv_pool* pool, int layer, const float* q, const
   a.n_q = n_q;
   a.qscale = scale * 1.4426950408889634f;  // log2(e): base-2 softmax
   a.window = pool->window[layer];
+  a.sinks = pool->sinks_of(layer);
   a.q_len = 1;
   a.q0 = 0;
   a.nq = 1;
@@ -280,6 +288,8 @@ pkv_status attention_mq_impl(const pkv_pool* pool, int layer, const float* q, co
     return fail(PKV_ERR_INVALID_ARG, "q / out not 16-byte aligned");
   if (num_chunks < 0) return fail(PKV_ERR_INVALID_ARG, "num_chunks < 0");
   if (num_chunks > PKV_MAX_CHUNKS) return fail(PKV_ERR_UNSUPPORTED, "num_chunks > %d", PKV_MAX_CHUNKS);
+  if (pool->sinks_of(layer) > 0)
+    return fail(PKV_ERR_UNSUPPORTED, "layer %d has sinks: paged_chunk_attention serves several queries", layer);
   if (num_rows == 0) return PKV_OK;
   const int g = n_q / pool->n_kv;
   if (num_chunks == 0 && (s = default_chunks_mq(pool, g, q_len, num_rows, &num_chunks))) return s;
@@ -309,6 +319,7 @@ pkv_status attention_mq_impl(const pkv_pool* pool, int layer, const float* q, co
   a.n_q = n_q;
   a.qscale = scale * 1.4426950408889634f;  // log2(e): base-2 softmax
   a.window = pool->window[layer];
+  a.sinks = 0;
   a.q_len = q_len;
   a.vchunks = num_chunks;
   a.aligned_split = split_may_align(pool->dtype);
@@ -334,6 +345,7 @@ pkv_status attention_mq_impl(const pkv_pool* pool, int layer, const float* q, co
 
 namespace pkv {
 int pool_kv_heads(const pkv_pool* pool) { return pool ? pool->n_kv : 0; }
+int pool_layers(const pkv_pool* pool) { return pool ? pool->num_layers : 0; }
 pkv_status check_attention_args(const pkv_pool* pool, int layer, const float* q,
                                 const int32_t* block_table, int bt_stride,
                                 const int32_t* seq_lens, int num_rows, int n_q_heads,
@@ -353,9 +365,14 @@ pkv_status pool_layer_view(const pkv_pool* pool, int layer, PoolView* view) {
   view->n_kv = pool->n_kv;
   view->dtype = pool->dtype;
   view->window = pool->window[layer];
+  view->sinks = pool->sinks_of(layer);
   view->status = pool->status;
   view->test_stall_ns = pool->test_stall_ns;
   return PKV_OK;
+}
+void pool_layer_bytes(const pkv_pool* pool, size_t* data, size_t* scales) {
+  *data = pool->layer_data_bytes;
+  *scales = pool->layer_scale_bytes;
 }
 pkv_status pool_layer_maps(const pkv_pool* pool, int layer, const TileMaps** maps) {
   return layer_maps(pool, layer, maps);
@@ -416,6 +433,7 @@ pkv_status kv_pool_create(pkv_pool** out, int num_layers, int num_pages, int n_k
   p->maps = nullptr;
   p->ready = nullptr;
   p->window = nullptr;
+  p->sinks = nullptr;
   if (static_cast<long long>(num_pages) * n_kv_heads >= (1ll << 31)) {
     delete p;
     return fail(PKV_ERR_UNSUPPORTED, "num_pages * n_kv_heads must be below 2^31");
@@ -423,13 +441,15 @@ pkv_status kv_pool_create(pkv_pool** out, int num_layers, int num_pages, int n_k
   p->maps = new (std::nothrow) pkv::TileMaps[num_layers];
   p->ready = new (std::nothrow) std::atomic<int>[num_layers];
   p->window = new (std::nothrow) int[num_layers];
-  if (!p->maps || !p->ready || !p->window) {
+  p->sinks = new (std::nothrow) int[num_layers];
+  if (!p->maps || !p->ready || !p->window || !p->sinks) {
     delete p;
     return fail(PKV_ERR_INVALID_ARG, "out of host memory");
   }
   for (int l = 0; l < num_layers; ++l) {
     p->ready[l].store(0);
     p->window[l] = 0;
+    p->sinks[l] = 0;
   }
   *out = p;
   return PKV_OK;
@@ -450,6 +470,22 @@ pkv_status kv_pool_get_window(const pkv_pool* pool, int layer, int* window) {
   if (s) return s;
   if (!window) return fail(PKV_ERR_INVALID_ARG, "null window pointer");
   *window = pool->window[layer];
+  return PKV_OK;
+}
+
+pkv_status kv_pool_set_sinks(pkv_pool* pool, int layer, int sinks) {
+  pkv_status s = check_pool_layer(pool, layer);
+  if (s) return s;
+  if (sinks < 0 || sinks > PKV_MAX_SINKS) return fail(PKV_ERR_INVALID_ARG, "sinks outside [0, %d]", PKV_MAX_SINKS);
+  pool->sinks[layer] = sinks;
+  return PKV_OK;
+}
+
+pkv_status kv_pool_get_sinks(const pkv_pool* pool, int layer, int* sinks) {
+  pkv_status s = check_pool_layer(pool, layer);
+  if (s) return s;
+  if (!sinks) return fail(PKV_ERR_INVALID_ARG, "null sinks pointer");
+  *sinks = pool->sinks[layer];
   return PKV_OK;
 }
 

@@ -55,15 +55,23 @@ struct Stored8 {
   }
 };
 
+// The tokens that attend_query visits: t stands for token(t), which it reads
+// where seen(token).
+struct AllSeen {
+  static constexpr bool kAll = true;
+  __device__ __forceinline__ int token(int t) const { return t; }
+  __device__ __forceinline__ bool seen(int) const { return true; }
+};
+
 // The states of a query's G rows for KV head h (1, 2 or 4 query heads, which see
-// the same tokens) over [t0, t1) of row i, all attended: running maximum m and
-// sum l in base 2, and dims 4 lane .. + 3 of the unnormalised outputs.  q points
-// at the first row's 128 dims (f16 or bf16), the others follow.  The whole warp
-// must call it.
-template <int DT>
+// the same tokens) over [t0, t1) of row i, those of them that `see` lets through
+// (all, by default): running maximum m and sum l in base 2, and dims 4 lane .. +
+// 3 of the unnormalised outputs.  q points at the first row's 128 dims (f16 or
+// bf16), the others follow.  The whole warp must call it.
+template <int DT, typename See = AllSeen>
 __device__ __forceinline__ void attend_query(const PoolView& pool, const ChunkRows& rows, const ScoreArgs& sc, int i,
                                              int h, int G, int P, const uint8_t* q, int t0, int t1, float (&m)[4],
-                                             float (&l)[4], float (&acc)[4][4]) {
+                                             float (&l)[4], float (&acc)[4][4], const See& see = See()) {
   constexpr int kIo = DT == PKV_KV_BF16 ? PKV_KV_BF16 : PKV_KV_F16;
   const int lane = threadIdx.x & 31;
   const int32_t* bt = rows.block_table + static_cast<long long>(i) * rows.bt_stride;
@@ -76,8 +84,9 @@ __device__ __forceinline__ void attend_query(const PoolView& pool, const ChunkRo
     acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.0f;
   }
   for (int base = t0; base < t1; base += 32) {
-    const int t = base + lane;
-    const bool in = t < t1;
+    const int t = see.token(base + lane);
+    const bool in = base + lane < t1 && see.seen(t);
+    const unsigned ins = See::kAll ? kFull : __ballot_sync(kFull, in);
     long long r = 0;
     float s[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, w[4];
     if (in) {
@@ -142,6 +151,7 @@ __device__ __forceinline__ void attend_query(const PoolView& pool, const ChunkRo
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         if (u0 + u >= n) break;
+        if (!See::kAll && !(ins >> (u0 + u) & 1u)) continue;  // its value may be anything
         float x[4];
         v[u].values(lane & 1, x);
 #pragma unroll

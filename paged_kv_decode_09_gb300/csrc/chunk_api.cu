@@ -1,5 +1,5 @@
-// chunk_api.cu — the C entries of pkv_chunk.h: host-side validation and the
-// launches.  Nothing here allocates device memory or synchronises a stream.
+// chunk_api.cu — the C entries of pkv_chunk.h and pkv_tree.h: host-side
+// validation and the launches.  Nothing here allocates device memory or synchronises a stream.
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
@@ -91,7 +91,7 @@ pkv_status check_q_type(int pool_dtype, pkv_kv_dtype q_dtype) {
 
 pkv::ChunkRows rows_of(const int32_t* cu, const int32_t* seq_lens, const int32_t* bt, int bt_stride,
                        int num_rows, int total_tokens) {
-  return pkv::ChunkRows{cu, seq_lens, bt, bt_stride, num_rows, total_tokens};
+  return pkv::ChunkRows{cu, seq_lens, bt, bt_stride, num_rows, total_tokens, PKV_MAX_CHUNK_TOKENS};
 }
 
 pkv_status default_chunks(int* chunks) {
@@ -105,6 +105,54 @@ pkv_status default_chunks(int* chunks) {
 }
 
 constexpr int kMaxChunks = 4096;
+
+// paged_chunk_attention and paged_tree_attention.
+pkv_status chunk_attention(bool tree, const pkv_pool* pool, int layer, const void* q, long long q_stride,
+                           pkv_kv_dtype q_dtype, const int32_t* parents, const int32_t* cu_seqlens, int total_tokens,
+                           const int32_t* block_table, int bt_stride, const int32_t* seq_lens, int num_rows,
+                           int n_q_heads, const pkv_scores* scores, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, int num_chunks, void* stream) {
+  pkv::ChunkAttnArgs a;
+  pkv_status s = pkv::pool_layer_view(pool, layer, &a.pool);
+  if (s) return s;
+  if ((s = check_group(n_q_heads, a.pool.n_kv))) return s;
+  if ((s = check_q_type(a.pool.dtype, q_dtype))) return s;
+  if ((s = check_rows(num_rows, total_tokens, cu_seqlens, seq_lens, block_table, bt_stride))) return s;
+  if ((s = check_scores(scores))) return s;
+  if (tree && (scores->slopes || scores->prefix_lens))
+    return fail(PKV_ERR_UNSUPPORTED, "trees take no slopes and no prefix_lens");
+  if (num_chunks < 0) return fail(PKV_ERR_INVALID_ARG, "num_chunks < 0");
+  if (num_chunks > kMaxChunks) return fail(PKV_ERR_UNSUPPORTED, "num_chunks > %d", kMaxChunks);
+  if (num_rows == 0 || total_tokens == 0) return PKV_OK;
+  if ((s = check_tokens("q", q, q_stride, n_q_heads, q_dtype))) return s;
+  if (tree && !parents) return fail(PKV_ERR_INVALID_ARG, "null parents");
+  if (!aligned(parents, 4)) return fail(PKV_ERR_INVALID_ARG, "parents not 4-byte aligned");
+  if (!out) return fail(PKV_ERR_INVALID_ARG, "null out");
+  if (!aligned(out, 16) || !aligned(lse, 4)) return fail(PKV_ERR_INVALID_ARG, "out or lse not aligned");
+  if (num_chunks == 0 && (s = default_chunks(&num_chunks))) return s;
+  const size_t need = pkv::chunk_attention_workspace(n_q_heads, a.pool.n_kv, num_chunks);
+  if (!workspace || workspace_bytes < need)
+    return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  if (!aligned(workspace, 256)) return fail(PKV_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  // a row that is computed again reads its query after others are written
+  if (out == q) return fail(PKV_ERR_INVALID_ARG, "out must not be q");
+  a.rows = rows_of(cu_seqlens, seq_lens, block_table, bt_stride, num_rows, total_tokens);
+  if (tree) a.rows.most = PKV_MAX_TREE_TOKENS;
+  a.parents = parents;
+  a.q = static_cast<const uint8_t*>(q);
+  a.q_stride = q_stride;
+  a.n_q = n_q_heads;
+  a.sc = pkv::ScoreArgs{scores->scale, scores->softcap, scores->slopes, scores->prefix_lens};
+  a.out = static_cast<uint8_t*>(out);
+  a.lse = lse;
+  a.workspace = static_cast<uint8_t*>(workspace);
+  a.chunks = num_chunks;
+  const pkv::TileMaps* maps = nullptr;
+  if ((s = pkv::pool_layer_maps(pool, layer, &maps))) return s;
+  const cudaError_t e = pkv::launch_chunk_attention(a, *maps, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, tree ? "tree attention launch" : "chunk attention launch");
+  return PKV_OK;
+}
 
 }  // namespace
 
@@ -197,39 +245,53 @@ pkv_status paged_chunk_attention(const pkv_pool* pool, int layer, const void* q,
                                  const int32_t* seq_lens, int num_rows, int n_q_heads,
                                  const pkv_scores* scores, void* out, float* lse, void* workspace,
                                  size_t workspace_bytes, int num_chunks, void* stream) {
-  pkv::ChunkAttnArgs a;
-  pkv_status s = pkv::pool_layer_view(pool, layer, &a.pool);
+  return chunk_attention(false, pool, layer, q, q_stride, q_dtype, nullptr, cu_seqlens, total_tokens, block_table,
+                         bt_stride, seq_lens, num_rows, n_q_heads, scores, out, lse, workspace, workspace_bytes,
+                         num_chunks, stream);
+}
+
+pkv_status paged_tree_attention(const pkv_pool* pool, int layer, const void* q, long long q_stride,
+                                pkv_kv_dtype q_dtype, const int32_t* parents, const int32_t* cu_seqlens,
+                                int total_tokens, const int32_t* block_table, int bt_stride,
+                                const int32_t* seq_lens, int num_rows, int n_q_heads,
+                                const pkv_scores* scores, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, int num_chunks, void* stream) {
+  return chunk_attention(true, pool, layer, q, q_stride, q_dtype, parents, cu_seqlens, total_tokens, block_table,
+                         bt_stride, seq_lens, num_rows, n_q_heads, scores, out, lse, workspace, workspace_bytes,
+                         num_chunks, stream);
+}
+
+pkv_status kv_tree_commit(const pkv_pool* pool, int first_layer, int num_layers, const int32_t* parents,
+                          const int32_t* leaves, const int32_t* cu_seqlens, int total_tokens,
+                          const int32_t* block_table, int bt_stride, const int32_t* seq_lens,
+                          int num_rows, int32_t* path, int path_stride, int32_t* new_lens,
+                          void* stream) {
+  pkv::CommitArgs a;
+  pkv_status s = pkv::pool_layer_view(pool, first_layer, &a.pool);
   if (s) return s;
-  if ((s = check_group(n_q_heads, a.pool.n_kv))) return s;
-  if ((s = check_q_type(a.pool.dtype, q_dtype))) return s;
+  if (num_layers < 0 || num_layers > pkv::pool_layers(pool) - first_layer)
+    return fail(PKV_ERR_INVALID_ARG, "num_layers %d from layer %d of %d", num_layers, first_layer,
+                pkv::pool_layers(pool));
   if ((s = check_rows(num_rows, total_tokens, cu_seqlens, seq_lens, block_table, bt_stride))) return s;
-  if ((s = check_scores(scores))) return s;
-  if (num_chunks < 0) return fail(PKV_ERR_INVALID_ARG, "num_chunks < 0");
-  if (num_chunks > kMaxChunks) return fail(PKV_ERR_UNSUPPORTED, "num_chunks > %d", kMaxChunks);
-  if (num_rows == 0 || total_tokens == 0) return PKV_OK;
-  if ((s = check_tokens("q", q, q_stride, n_q_heads, q_dtype))) return s;
-  if (!out) return fail(PKV_ERR_INVALID_ARG, "null out");
-  if (!aligned(out, 16) || !aligned(lse, 4)) return fail(PKV_ERR_INVALID_ARG, "out or lse not aligned");
-  if (num_chunks == 0 && (s = default_chunks(&num_chunks))) return s;
-  const size_t need = pkv::chunk_attention_workspace(n_q_heads, a.pool.n_kv, num_chunks);
-  if (!workspace || workspace_bytes < need)
-    return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-  if (!aligned(workspace, 256)) return fail(PKV_ERR_INVALID_ARG, "workspace not 256-byte aligned");
-  // a row that is computed again reads its query after others are written
-  if (out == q) return fail(PKV_ERR_INVALID_ARG, "out must not be q");
+  if (path && path_stride < 1) return fail(PKV_ERR_INVALID_ARG, "path_stride < 1");
+  if (num_rows == 0) return PKV_OK;
+  if (!parents && total_tokens > 0) return fail(PKV_ERR_INVALID_ARG, "null parents");
+  if (!leaves || !new_lens) return fail(PKV_ERR_INVALID_ARG, "null leaves or new_lens");
+  if (!aligned(parents, 4) || !aligned(leaves, 4) || !aligned(path, 4) || !aligned(new_lens, 4))
+    return fail(PKV_ERR_INVALID_ARG, "parents / leaves / path / new_lens not 4-byte aligned");
+  // other CTAs read these while one writes
+  if (new_lens == seq_lens || new_lens == leaves) return fail(PKV_ERR_INVALID_ARG, "new_lens must be an array of its own");
+  a.layers = num_layers;
+  pkv::pool_layer_bytes(pool, &a.data_bytes, &a.scale_bytes);
   a.rows = rows_of(cu_seqlens, seq_lens, block_table, bt_stride, num_rows, total_tokens);
-  a.q = static_cast<const uint8_t*>(q);
-  a.q_stride = q_stride;
-  a.n_q = n_q_heads;
-  a.sc = pkv::ScoreArgs{scores->scale, scores->softcap, scores->slopes, scores->prefix_lens};
-  a.out = static_cast<uint8_t*>(out);
-  a.lse = lse;
-  a.workspace = static_cast<uint8_t*>(workspace);
-  a.chunks = num_chunks;
-  const pkv::TileMaps* maps = nullptr;
-  if ((s = pkv::pool_layer_maps(pool, layer, &maps))) return s;
-  const cudaError_t e = pkv::launch_chunk_attention(a, *maps, as_stream(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+  a.rows.most = PKV_MAX_TREE_TOKENS;
+  a.parents = parents;
+  a.leaves = leaves;
+  a.path = path;
+  a.path_stride = path_stride;
+  a.new_lens = new_lens;
+  const cudaError_t e = pkv::launch_tree_commit(a, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "tree commit launch");
   return PKV_OK;
 }
 
@@ -247,6 +309,7 @@ pkv_status paged_attention_mass(const pkv_pool* pool, int layer, const void* q, 
   if ((s = check_q_type(a.pool.dtype, q_dtype))) return s;
   if ((s = check_rows(num_rows, total_tokens, cu_seqlens, seq_lens, block_table, bt_stride))) return s;
   if ((s = check_scores(scores))) return s;
+  if (a.pool.sinks > 0) return fail(PKV_ERR_UNSUPPORTED, "layer %d has sinks: no attention weights", layer);
   if (last_queries < 0) return fail(PKV_ERR_INVALID_ARG, "last_queries < 0");
   if (mass_stride < 1) return fail(PKV_ERR_INVALID_ARG, "mass_stride < 1");
   if (num_chunks < 0) return fail(PKV_ERR_INVALID_ARG, "num_chunks < 0");

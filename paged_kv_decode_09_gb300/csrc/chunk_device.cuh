@@ -24,7 +24,7 @@ __device__ __forceinline__ RowInfo row_info(const ChunkRows& r, int i, int32_t* 
   x.L = __ldg(r.seq_lens + i);
   const bool valid = x.start >= 0 && end >= x.start && end <= r.total_tokens;
   x.n = valid ? end - x.start : 0;
-  if (!valid || x.L < x.n || static_cast<long long>(x.L) > static_cast<long long>(r.bt_stride) * kPage) {
+  if (!valid || x.L < x.n || x.n > r.most || static_cast<long long>(x.L) > static_cast<long long>(r.bt_stride) * kPage) {
     record_status(status, PKV_DEV_BAD_LENGTH);
     x.L = -1;
   }

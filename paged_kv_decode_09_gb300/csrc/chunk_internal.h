@@ -1,6 +1,7 @@
 // chunk_internal.h — argument blocks and launchers of the long-prompt operators
-// (rope_append.cu, chunk_attention.cu, attention_mass.cu, evict.cu), shared
-// with their C entries (chunk_api.cu).  Not installed.
+// (rope_append.cu, chunk_attention.cuh, attention_mass.cu, evict.cu) and of the
+// calls on drafted trees (chunk_attention.cuh, tree_commit.cu), shared with their
+// C entries (chunk_api.cu).  Not installed.
 #pragma once
 
 #include <cstddef>
@@ -9,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include "pkv_chunk.h"
+#include "pkv_tree.h"
 #include "pkv_internal.h"
 
 namespace pkv {
@@ -23,6 +25,7 @@ struct PoolView {
   int n_kv;
   int dtype;
   int window;
+  int sinks;  // 0 without a window
   int32_t* status;
   unsigned long long test_stall_ns;  // test hook (kv_pool_set_test_stall); 0: off
 };
@@ -37,6 +40,7 @@ struct ChunkRows {
   int bt_stride;
   int num_rows;
   int total_tokens;
+  int most;  // new tokens of a row; rows with more are skipped
 };
 
 struct RopeArgs {
@@ -95,9 +99,32 @@ struct ChunkAttnArgs {
   float* lse;  // or NULL
   uint8_t* workspace;
   int chunks;
+  const int32_t* parents;  // [total_tokens]: the new tokens are trees (paged_tree_attention); or NULL
 };
 size_t chunk_attention_workspace(int n_q, int n_kv, int chunks);
 cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, const TileMaps& maps, cudaStream_t stream);
+// The same where not every token from a query's first on is visible: layers with
+// sinks, and trees (sparse_attention.cu).
+cudaError_t launch_sparse_attention(const ChunkAttnArgs& a, const TileMaps& maps, const CUtensorMap& qmap,
+                                    cudaStream_t stream);
+
+// Accepted paths moved to the front of the drafted slots (tree_commit.cu), over
+// layers first .. of the pool: a layer's arrays lie data_bytes and scale_bytes apart.
+struct CommitArgs {
+  PoolView pool;  // of the first layer
+  int layers;
+  size_t data_bytes, scale_bytes;
+  ChunkRows rows;
+  const int32_t* parents;
+  const int32_t* leaves;
+  int32_t* path;  // or NULL
+  int path_stride;
+  int32_t* new_lens;
+};
+cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t stream);
+// Bytes from a layer's K or V data (or scales) to the next layer's.
+void pool_layer_bytes(const pkv_pool* pool, size_t* data, size_t* scales);
+int pool_layers(const pkv_pool* pool);
 
 // Tensor map of a call's queries (chunk_attention.cu).
 cudaError_t encode_query_map(CUtensorMap* m, bool bf16, const void* q, long long stride, int heads, int group,

@@ -504,7 +504,11 @@ __device__ __forceinline__ void piece_merge(const float* mrg_acc, const float* m
 }
 
 // --------------------------------------------------------------- kernel ----
-template <int DT, int G>
+// SINKS: the layer's first tokens stay visible under its window (kv_pool_set_sinks).
+// A row's units are then the pages of its sinks, from slot 0, and the pages of
+// its window; a page that holds the end of the one and the start of the other
+// is two units, so that a unit's tokens remain one range.
+template <int DT, int G, bool SINKS>
 __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PER_SM
                                             : DT == PKV_KV_F32 ? PKV_F32_CTAS_PER_SM
                                                                : PKV_F16_CTAS_PER_SM)
@@ -549,8 +553,9 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
   // find room as ours exit).
   grid_dependency_wait();
   grid_launch_dependents();
+  const int sinks = SINKS ? a.sinks : 0;
   plan_rows(a.seq_lens, a.num_rows, a.bt_stride, a.window, blockIdx.x == 0 ? a.status : nullptr,
-            lens, row_start);
+            lens, row_start, 1, sinks);
 
   const bool stalled = test_stall(smem_addr(smem + SM::kStall), a.test_stall_ns, ctl, a.status);
   plan_split(row_start, a.num_rows, a.n_kv, gridDim.x, a.aligned_split, split, pc);
@@ -586,9 +591,15 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
       const int npg = row_start[i + 1] - row_start[i];
       const int off = static_cast<int>(x - static_cast<long long>(a.n_kv) * row_start[i]);
       hh = off / npg;
-      const int p = off - hh * npg;  // of the pages the row reads, from window_start / 16
-      int page = __ldg(a.block_table + static_cast<long long>(i) * a.bt_stride +
-                       window_start(lens[i], a.window) / kPage + p);
+      const int p = off - hh * npg;  // of the pages the row reads
+      int entry;
+      if constexpr (SINKS) {
+        const int ws = sink_window_start(lens[i], a.window, sinks), np = sink_pages(ws, sinks);
+        entry = p < np ? p : ws / kPage + p - np;
+      } else {
+        entry = window_start(lens[i], a.window) / kPage + p;
+      }
+      int page = __ldg(a.block_table + static_cast<long long>(i) * a.bt_stride + entry);
       last = (p == npg - 1) ? 1 : 0;
       if (page < 0 || page >= a.num_pages) {
         record_status(a.status, PKV_DEV_BAD_PAGE);
@@ -665,8 +676,10 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
     const long long seg_end = seg_start + npg;
     const long long b = min(seg_end, c_end);
     const int L = lens[i];
-    const int ws = window_start(L, a.window);  // first attended token of the row
-    const int p0 = ws / kPage;                 // its page: the row's unit 0
+    // first attended token of the row behind its sinks
+    const int ws = SINKS ? sink_window_start(L, a.window, sinks) : window_start(L, a.window);
+    const int np = SINKS ? sink_pages(ws, sinks) : 0;  // pages of its sinks: units 0 .. np - 1
+    const int p0 = ws / kPage - np;                    // with rel >= np: the page p0 + rel
     const long long j = static_cast<long long>(i) * a.n_kv + h;
     int k0, k1;
     segment_chunks(sp, i, h, row_start, pc, a.num_rows, a.n_kv, k0, k1);
@@ -699,9 +712,10 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
         continue;
       }
       consumed = u + 1;
-      const int t_page = (p0 + rel) * kPage;  // page's first token
-      const int nvalid = min(kPage, L - t_page);
-      const int tlo = max(0, ws - t_page);
+      const bool sink = SINKS && rel < np;
+      const int t_page = (sink ? rel : p0 + rel) * kPage;  // page's first token
+      const int nvalid = min(kPage, (sink ? sinks : L) - t_page);
+      const int tlo = sink ? 0 : max(0, ws - t_page);
       process_unit<DT, G>(ring + s * TL::kCodes, ring_sc + s * TL::kScales, tlo, nvalid, lane, S);
       if (issued < n_units) issue();
     }
@@ -1013,7 +1027,7 @@ cudaError_t encode_tile_maps(int dtype, void* k_data, void* v_data, long long ti
 
 // The kernel's dynamic shared-memory limit, raised only when a call needs
 // more than any earlier call (per device).
-template <int DT, int G>
+template <int DT, int G, bool SINKS>
 static cudaError_t ensure_smem(size_t smem) {
   static std::atomic<size_t> granted[64];
   int dev = 0;
@@ -1021,7 +1035,7 @@ static cudaError_t ensure_smem(size_t smem) {
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < 64 && granted[dev].load(std::memory_order_relaxed) >= smem)
     return cudaSuccess;
-  e = cudaFuncSetAttribute(paged_decode_kernel<DT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(paged_decode_kernel<DT, G, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem));
   if (e == cudaSuccess && dev >= 0 && dev < 64) {
     size_t cur = granted[dev].load();
@@ -1031,11 +1045,11 @@ static cudaError_t ensure_smem(size_t smem) {
   return e;
 }
 
-template <int DT, int G>
-static cudaError_t launch_decode_t(const DecodeArgs& a, const TileMaps& maps, int chunks,
+template <int DT, int G, bool SINKS>
+static cudaError_t launch_decode_s(const DecodeArgs& a, const TileMaps& maps, int chunks,
                                    cudaStream_t st) {
   const size_t smem = Smem<DT, G>::bytes(a.num_rows);
-  cudaError_t e = ensure_smem<DT, G>(smem);
+  cudaError_t e = ensure_smem<DT, G, SINKS>(smem);
   if (e != cudaSuccess) return e;
   // Programmatic dependent launch: the grid may be scheduled while the
   // previous kernel of the stream finishes; the kernel itself waits for that
@@ -1050,17 +1064,24 @@ static cudaError_t launch_decode_t(const DecodeArgs& a, const TileMaps& maps, in
   attr[0].val.programmaticStreamSerializationAllowed = PKV_PDL;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<DT, G>, a, maps);
+  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<DT, G, SINKS>, a, maps);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
 template <int DT, int G>
+static cudaError_t launch_decode_t(const DecodeArgs& a, const TileMaps& maps, int chunks,
+                                   cudaStream_t st) {
+  return a.sinks > 0 ? launch_decode_s<DT, G, true>(a, maps, chunks, st)
+                     : launch_decode_s<DT, G, false>(a, maps, chunks, st);
+}
+
+template <int DT, int G>
 static cudaError_t occupancy_t(int rows, int* blocks) {
   const size_t smem = Smem<DT, G>::bytes(rows);
-  cudaError_t e = ensure_smem<DT, G>(smem);
+  cudaError_t e = ensure_smem<DT, G, false>(smem);
   if (e != cudaSuccess) return e;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, paged_decode_kernel<DT, G>,
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, paged_decode_kernel<DT, G, false>,
                                                        kThreads, smem);
 }
 

@@ -30,6 +30,7 @@ struct DecodeArgs {
   int n_q;
   float qscale;  // softmax scale * log2(e): scores are kept in base 2
   int window;    // > 0: each row attends to its last `window` tokens
+  int sinks;     // > 0: and to its first `sinks` (single-query kernel)
   int q_len;     // queries (new tokens) per row; q, out [rows][q_len][n_q][128]
   int q0, nq;    // several-query kernel: this pass's queries q0 .. q0 + nq - 1
   int vchunks;   // chunks of the work split (several-query kernels: a CTA may hold 2)
