@@ -74,11 +74,11 @@
 // of their limit.
 //
 // SPARSE kernels.  Under a window, the row's first S tokens (its sinks) stay
-// visible: a tile's blocks are those of the sinks and then those of its window,
-// counted through, and only a block's tokens and pages know of the gap
-// (block_at).  In a tree, a query sees the context before it and, of the row's
-// new tokens, its ancestors: their bits of a group of 32 columns are found by
-// walking up the parents, in blocks that hold new tokens alone.
+// visible: a tile's blocks are made of the pages of the sinks and then of those
+// of its window, counted through (Pages), so that neither leaves a block half
+// empty.  In a tree, a query sees the context before it and, of the row's new
+// tokens, its ancestors: they are found by walking up the parents, once for a
+// block that holds any, while the block's scores are computed.
 #pragma once
 
 #include <atomic>
@@ -180,17 +180,21 @@ struct TileGeom {
   int nb;    // blocks
 };
 
-// SPARSE kernels.  Blocks of the sinks that lie before the block t_lo is in:
-template <int DT>
-__device__ __forceinline__ int sink_blocks(int t_lo, int S) {
-  return t_lo > 0 ? min((S + kBlockTok<DT> - 1) / kBlockTok<DT>, t_lo / kBlockTok<DT>) : 0;
-}
-// and the block that the tile's v-th is.
-template <int DT>
-__device__ __forceinline__ int block_at(int v, int t_lo, int S) {
-  const int sb = sink_blocks<DT>(t_lo, S);
-  return v < sb ? v : v - sb + t_lo / kBlockTok<DT>;
-}
+// SPARSE kernels: the pages a tile reads, counted through.  With sinks before its
+// first other token t_lo (0: none apart) these are the pages of the sinks, sp of
+// them, and those from page sp + gap on.  sp is even, so that a group of 32
+// columns is 32 tokens in a row.
+struct Pages {
+  int sp, gap;
+  __device__ __forceinline__ Pages(int t_lo, int S) {
+    sp = t_lo > 0 ? ((S + kPage - 1) / kPage + 1) & ~1 : 0;
+    gap = max(t_lo / kPage - sp, 0);
+  }
+  __device__ __forceinline__ int page(int v) const { return v < sp ? v : v + gap; }
+  __device__ __forceinline__ int token(int v) const { return v < sp * kPage ? v : v + gap * kPage; }
+  // the n tokens from v on are n in a row
+  __device__ __forceinline__ bool row(int v, int n) const { return gap == 0 || v >= sp * kPage || v + n <= sp * kPage; }
+};
 // The parent of drafted token `node` of the row whose tokens start at `first`.
 __device__ __forceinline__ int parent_of(const ChunkAttnArgs& a, int first, int node) {
   const int p = __ldg(a.parents + first + node);
@@ -206,20 +210,24 @@ struct Sight {
   int lo, C, S, W;
   int first, node, depth;
   __device__ __forceinline__ bool kin(int steps) const { return W == 0 || steps < W || C + depth - steps < S; }
-  // of the tokens c .. c + 31, as bits
-  __device__ __forceinline__ uint32_t word(const ChunkAttnArgs& a, int c) const {
+  // of the context tokens c .. c + 31, as bits
+  __device__ __forceinline__ uint32_t context(int c) const {
     auto below = [](int x) { return x >= 32 ? ~0u : x <= 0 ? 0u : (1u << x) - 1u; };
-    uint32_t bits = below(C - c) & (~below(lo - c) | below(S - c));
-    const int o = c - C;  // drafted token of bit 0
-    if (node >= 0 && o > -32) {
-      int x = node;
+    return below(C - c) & (~below(lo - c) | below(S - c));
+  }
+  // of the drafted tokens among the 32 N from token t on, N words of them
+  template <int N>
+  __device__ __forceinline__ void ancestors(const ChunkAttnArgs& a, int t, uint32_t (&bits)[N]) const {
+    const int o = t - C;
+    int x = o > -32 * N ? node : -1;
 #pragma unroll 1
-      for (int steps = 0; x >= 0 && x >= o; ++steps) {
-        if (x < o + 32 && kin(steps)) bits |= 1u << (x - o);
-        x = parent_of(a, first, x);
-      }
+    for (int steps = 0; x >= 0 && x >= o; ++steps) {
+      const int at = x - o;
+      const uint32_t bit = kin(steps) ? 1u << (at & 31) : 0u;
+#pragma unroll
+      for (int e = 0; e < N; ++e) bits[e] |= at >> 5 == e ? bit : 0u;
+      x = parent_of(a, first, x);
     }
-    return bits;
   }
   __device__ __forceinline__ bool sees(const ChunkAttnArgs& a, int t) const {
     if (t < C) return t >= lo || t < S;
@@ -232,7 +240,6 @@ struct Sight {
   }
 };
 // Query jq of a piece's tile at position P (its tile's first is P0).
-template <int DT>
 __device__ __forceinline__ Sight sight_of(const ChunkAttnArgs& a, int tok, int P0, int L, int F, int jq, int& P) {
   Sight s;
   s.S = a.pool.sinks;
@@ -259,16 +266,13 @@ __device__ __forceinline__ Sight sight_of(const ChunkAttnArgs& a, int tok, int P
   if (s.lo <= s.S) s.lo = 0;
   return s;
 }
-// The same for attend_query, over the tokens of the tile's blocks counted through.
-template <int DT>
+// The same for attend_query, over the tokens of the tile's pages counted through.
 struct SparseSeen {
   static constexpr bool kAll = false;
   const ChunkAttnArgs& a;
   const Sight& s;
-  int t_lo;
-  __device__ __forceinline__ int token(int t) const {
-    return block_at<DT>(t / kBlockTok<DT>, t_lo, s.S) * kBlockTok<DT> + t % kBlockTok<DT>;
-  }
+  Pages pages;
+  __device__ __forceinline__ int token(int t) const { return pages.token(t); }
   __device__ __forceinline__ bool seen(int t) const { return s.sees(a, t); }
 };
 
@@ -291,11 +295,13 @@ struct QueryTiles {
     }
     g.t_lo = seen_from(g.P0, W);
     if (SPARSE && g.t_lo <= S) g.t_lo = 0;
-    g.kb = g.t_lo / kBlockTok<DT>;
-    g.nb = (g.t_hi + kBlockTok<DT> - 1) / kBlockTok<DT> - g.kb;
     if constexpr (SPARSE) {
-      g.nb += sink_blocks<DT>(g.t_lo, S);
+      const int pages = (g.t_hi + kPage - 1) / kPage - Pages(g.t_lo, S).gap;
       g.kb = 0;
+      g.nb = (pages * kPage + kBlockTok<DT> - 1) / kBlockTok<DT>;
+    } else {
+      g.kb = g.t_lo / kBlockTok<DT>;
+      g.nb = (g.t_hi + kBlockTok<DT> - 1) / kBlockTok<DT> - g.kb;
     }
     return g;
   }
@@ -450,9 +456,9 @@ __device__ __noinline__ void mend_rows(const ChunkAttnArgs& a, const uint32_t* n
       float m[4], l[4], acc[4][4];
       if constexpr (SPARSE) {
         int P;
-        const Sight sight = sight_of<DT>(a, d.tok, d.P0, d.L, d.F, j, P);
+        const Sight sight = sight_of(a, d.tok, d.P0, d.L, d.F, j, P);
         attend_query<DT>(a.pool, a.rows, a.sc, d.i, d.h, G, P, q, d.kb * kBlockTok<DT>, (d.kb + d.nb) * kBlockTok<DT>, m,
-                         l, acc, SparseSeen<DT>{a, sight, d.t_lo});
+                         l, acc, SparseSeen{a, sight, Pages(d.t_lo, a.pool.sinks)});
       } else {
         const int P = d.P0 + j;
         const int t0 = max(seen_from(P, a.pool.window), d.kb * kBlockTok<DT>);
@@ -620,29 +626,29 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   // block b of a piece: with a bias from the last one back, where the scores
   // are highest (a steep bias would raise the maximum with every group of 32
   // columns otherwise: 1100 us instead of 474 for a prompt of 8191 tokens)
-  auto block = [&](int kb, int nb, int b, int t_lo) {
-    const int v = GEN == 2 ? kb + nb - 1 - b : kb + b;
-    return SPARSE ? block_at<DT>(v, t_lo, a.pool.sinks) : v;
-  };
-  // pages of block kb that are read
+  auto block = [](int kb, int nb, int b) { return GEN == 2 ? kb + nb - 1 - b : kb + b; };
+  // pages of block kb that are read (SPARSE: counted through, as tokens are until token_of)
   auto pages_in = [&](int kb, int t_lo, int t_hi, int& lo, int& hi) {
     const int first = kb * kPages;
-    lo = max(first, t_lo / kPage);
-    hi = min(first + kPages, (t_hi + kPage - 1) / kPage);
-    if constexpr (SPARSE) {  // with sinks: theirs, and from them on where the window starts in the block too
-      if (t_lo > 0 && kb * N < a.pool.sinks) {
-        lo = first;
-        if (kb != t_lo / N) hi = min(first + kPages, (a.pool.sinks + kPage - 1) / kPage);
-      }
+    hi = (t_hi + kPage - 1) / kPage;
+    if constexpr (SPARSE) {
+      lo = first;
+      hi = min(first + kPages, hi - Pages(t_lo, a.pool.sinks).gap);
+    } else {
+      lo = max(first, t_lo / kPage);
+      hi = min(first + kPages, hi);
     }
   };
   auto pages_of = [&](const Piece& p, int b, int& lo, int& hi) {
-    pages_in(block(p.kb, p.nb, b, p.t_lo), p.t_lo, p.t_hi, lo, hi);
+    pages_in(block(p.kb, p.nb, b), p.t_lo, p.t_hi, lo, hi);
   };
-  // whose table entry is read for page x of a block read from lo on: its own, and for a page between the sinks and
-  // the window, whose entry may be anything, the first's
-  auto entry_of = [&](const Piece& p, int lo, int x) {
-    return SPARSE && x * kPage >= a.pool.sinks && (x + 1) * kPage <= p.t_lo ? lo : x;
+  auto token_of = [&](const Piece& p, int t) { return SPARSE ? Pages(p.t_lo, a.pool.sinks).token(t) : t; };
+  // the table entry of page x of those read: its own, but the first's for a page between the sinks and the window,
+  // whose entry may be anything (its tokens are masked, and zeroed as values)
+  auto entry_of = [&](const Piece& p, int x) {
+    if (!SPARSE) return x;
+    const int page = Pages(p.t_lo, a.pool.sinks).page(x);
+    return page * kPage >= a.pool.sinks && (page + 1) * kPage <= p.t_lo ? 0 : page;
   };
   // whether any query of the tile attends to token t
   auto in_tile = [&](const Piece& p, int t) {
@@ -651,8 +657,14 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   // V blocks that warp 11 sees: with tokens outside [t_lo, t_hi) in their
   // pages (zeroed), or masked for part of the tile (searched)
   auto mended = [&](const Piece& p, int b) {
-    const int t0 = block(p.kb, p.nb, b, p.t_lo) * N;
-    return (t0 < p.full_lo && !(SPARSE && t0 + N <= a.pool.sinks)) || t0 + N > p.full_hi;
+    int t0 = block(p.kb, p.nb, b) * N;
+    if constexpr (SPARSE) {
+      const Pages pages(p.t_lo, a.pool.sinks);
+      if (!pages.row(t0, N)) return true;
+      t0 = pages.token(t0);
+      if (t0 + N <= min(a.pool.sinks, p.full_hi)) return false;
+    }
+    return t0 < p.full_lo || t0 + N > p.full_hi;
   };
 
   if (kQ8 && warp >= 12) {
@@ -669,7 +681,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       if (d.last) break;
       for (int b = 0; b < d.nb && ok; ++b) {
         const bool mend = mended(d, b);
-        const int t0 = block(d.kb, d.nb, b, d.t_lo) * N;
+        const int t0 = block(d.kb, d.nb, b) * N;
 #pragma unroll
         for (int v = 0; v < 2; ++v, ++gs) {
           const int rs = gs % kRaws, s = gs % kS;
@@ -682,8 +694,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
           bool odd = false, large = false;
 #pragma unroll
           for (int e = 0; e < kPages; ++e) {  // token `row` of page e; 0 where no query of the tile attends
-            const int t = t0 + e * kPage + row;
-            const bool in = in_tile(d, t);
+            const bool in = in_tile(d, token_of(d, t0 + e * kPage + row));
             code[e] = *reinterpret_cast<const uint4*>(raw + e * (kPage * kD));
             const __half f = in ? rsc[e * kPage * (kD / kQBlock)] : __float2half_rn(0.0f);
             const unsigned bits = __half_as_ushort(f) & 0x7FFFu;
@@ -794,7 +805,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       auto entry = [&](int b) {
         int l0, h0;
         pages_of(d, b, l0, h0);
-        return lane < h0 - l0 ? __ldg(bt + entry_of(d, l0, l0 + lane)) : 0;
+        return lane < h0 - l0 ? __ldg(bt + entry_of(d, l0 + lane)) : 0;
       };
       int next = entry(0);
       for (int b = 0; b < d.nb; ++b) {
@@ -852,8 +863,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       auto entry = [&](int b) {  // lane e: page e of the block, -1 where it is not read
         int lo, hi;
         pages_of(d, b, lo, hi);
-        const int q = block(d.kb, d.nb, b, d.t_lo) * kPages + lane;
-        return lane < kPages && q >= lo && q < hi ? __ldg(bt + entry_of(d, lo, q)) : -1;
+        const int q = block(d.kb, d.nb, b) * kPages + lane;
+        return lane < kPages && q >= lo && q < hi ? __ldg(bt + entry_of(d, q)) : -1;
       };
       int next = entry(0);
       for (int b = 0; b < d.nb && ok; ++b) {
@@ -861,7 +872,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         if (b + 1 < d.nb) next = entry(b + 1);
         int lo, hi;
         pages_of(d, b, lo, hi);
-        const int q = block(d.kb, d.nb, b, d.t_lo) * kPages + lane;
+        const int q = block(d.kb, d.nb, b) * kPages + lane;
         const bool mine = lane < kPages && q >= lo && q < hi;
         if (mine && (pg < 0 || pg >= a.pool.num_pages)) {
           record_status(a.pool.status, PKV_DEV_BAD_PAGE);
@@ -913,12 +924,12 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         }
         landed ^= 1u << s;
         uint8_t* v = smem + kRing + s * kHalf;
-        const int t0 = block(d.kb, d.nb, b, d.t_lo) * N;
+        const int t0 = block(d.kb, d.nb, b) * N;
         int lo, hi;
         pages_of(d, b, lo, hi);
         // tokens of the pages read that no query of the tile attends to
         for (int t = lo * kPage + lane; t < hi * kPage; t += 32) {
-          if (in_tile(d, t)) continue;
+          if (in_tile(d, token_of(d, t))) continue;
           const int u = t - t0;  // token of the block: page u / 16, group (u / 8) % 2
           uint4* row = reinterpret_cast<uint4*>(v + (u >> 3) * 2048 + (u & 7) * 128);
 #pragma unroll
@@ -1080,7 +1091,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         tc::commit(bar(kBEmpty + s), lead);
         if (b + 1 == nb) tc::commit(bar(kBQEmpty), lead);
         int lo, hi;
-        pages_in(block(kb, nb, b, t_lo), t_lo, t_hi, lo, hi);
+        pages_in(block(kb, nb, b), t_lo, t_hi, lo, hi);
         v.s = (gs + 1) % kS;
         v.lo = lo & (kPages - 1);
         v.n = hi - lo;
@@ -1138,10 +1149,9 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         const int g = d.h * G + r % G;
         int lo = valid ? seen_from(P, a.pool.window) : 0;
         int hi = valid ? seen_to(P, d.L, d.F) : 0x7FFFFFFF;
-        [[maybe_unused]] Sight sight{0, 0x7FFFFFFF, 0, 0, 0, -1, 0};
         if constexpr (SPARSE) {
           if (valid) {
-            sight = sight_of<DT>(a, d.tok, d.P0, d.L, d.F, jq, P);
+            const Sight sight = sight_of(a, d.tok, d.P0, d.L, d.F, jq, P);
             lo = sight.lo;
             hi = sight.C;
           }
@@ -1158,8 +1168,28 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         float l = 0.0f;
         float most = -1.0f;    // a group's sum beyond which its maximum is looked at
         for (int b = !kTurns || two ? 0 : m; b < d.nb; b += every, ++blocks, begun = true) {
-          const int t0 = block(d.kb, d.nb, b, d.t_lo) * N;
-          const bool fast = __all_sync(kFull, (t0 >= lo || (SPARSE && t0 + N <= a.pool.sinks)) && t0 + N <= hi);
+          const int t0 = block(d.kb, d.nb, b) * N;
+          bool fast;
+          [[maybe_unused]] uint32_t see[N / 32];  // what the row sees of the block, where not all rows see all
+          if constexpr (SPARSE) {
+            const Pages pages(d.t_lo, a.pool.sinks);
+            const int t = pages.token(t0);
+            fast = pages.row(t0, N) && __all_sync(kFull, (t >= lo || t + N <= a.pool.sinks) && t + N <= hi);
+            if (__builtin_expect(!fast, 0)) {
+#pragma unroll
+              for (int e = 0; e < N / 32; ++e) see[e] = ~0u;
+              if (valid) {
+                int at;
+                const Sight sight = sight_of(a, d.tok, d.P0, d.L, d.F, jq, at);
+#pragma unroll
+                for (int e = 0; e < N / 32; ++e) see[e] = sight.context(pages.token(t0 + 32 * e));
+                // (the drafted tokens lie behind the gap)
+                if (a.parents) sight.ancestors(a, t0 + pages.gap * kPage, see);
+              }
+            }
+          } else {
+            fast = __all_sync(kFull, t0 >= lo && t0 + N <= hi);
+          }
           const float near = GEN == 1 ? cap.limit(valid, fast) : 0.0f;
           if (!(ok = wait(kBS + m, blocks))) break;
           tc::fence_after();
@@ -1222,7 +1252,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
                 }
               }
               if constexpr (GEN == 2) {
-                const float dist0 = static_cast<float>(t0 + 32 * group - P);  // t - P of the first column
+                const float dist0 = static_cast<float>(token_of(d, t0 + 32 * group) - P);  // t - P of the first column
                 const bool before = behind || dist0 <= -31.0f, after = dist0 >= 0.0f;
                 if (__builtin_expect(__any_sync(kFull, valid && !before && !after), 0)) {  // seen on both sides
 #pragma unroll
@@ -1235,9 +1265,11 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
               }
               if (__builtin_expect(!fast, 0)) {
                 if constexpr (SPARSE) {
-                  const uint32_t see = sight.word(a, t0 + 32 * group);
+                  uint32_t word = see[0];
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) v[e] = see >> e & 1u ? v[e] : kMasked;
+                  for (int e = 1; e < N / 32; ++e) word = group == e ? see[e] : word;
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] = word >> e & 1u ? v[e] : kMasked;
                 } else {
                   const int from = lo - t0 - 32 * group, to = hi - t0 - 32 * group;
 #pragma unroll
