@@ -26,7 +26,7 @@
 // Q, 9 issues the products, 10 copies K and V pages (one tensor copy each)
 // into a ring of five 32 KiB slots, 11 mends V blocks that hold tokens no
 // query of the tile attends to; with q8_0, 10 copies codes and scales into a
-// ring of their own, and 12-15 split them into the ring of slots.  Hand-overs
+// ring of their own, and 12-19 split them into the ring of slots.  Hand-overs
 // by shared-memory barriers:
 //   dfull, dempty[x]  descriptor x of a piece (a tile's blocks in this range)
 //   qfull[m], qempty  Q_m landed; the piece's last scores are computed
@@ -100,8 +100,14 @@ namespace {
 constexpr int kTileRows = 256;   // (query, query head) rows of a tile: 256 / G queries
 template <int DT>
 constexpr int kBlockTok = DT == PKV_KV_Q8_0 ? 64 : 128;  // cached tokens of a block
-template <int DT>
-constexpr int kAttnThreads = DT == PKV_KV_Q8_0 ? 512 : kPlanThreads;
+// Warps that split q8_0: the SPARSE kernel's larger code leaves four of them the
+// slowest of all (q8_0 trees of 32 tokens 139 us, 117 with eight); without it
+// eight take registers and schedulers from the softmax (2048 tokens over 32049
+// 1.37 ms with four, 1.43 with eight).
+template <int DT, bool SPARSE>
+constexpr int kSplitWarps = DT != PKV_KV_Q8_0 ? 0 : SPARSE ? 8 : 4;
+template <int DT, bool SPARSE>
+constexpr int kAttnThreads = kPlanThreads + 32 * kSplitWarps<DT, SPARSE>;
 // How far from a tile's end a boundary moves there, in blocks (chunk_plan): with
 // q8_0's blocks of 64 tokens, from one block away; with blocks of 128, never.
 template <int DT>
@@ -143,8 +149,26 @@ enum : int {
   kBStall,
   kNumBars,
 };
-template <int DT>
-constexpr int kDescReaders = DT == PKV_KV_Q8_0 ? 14 : 11;  // softmax, products, copies, and mending or splitting
+template <int DT, bool SPARSE>  // softmax, products, copies, and mending or splitting
+constexpr int kDescReaders = DT == PKV_KV_Q8_0 ? 10 + kSplitWarps<DT, SPARSE> : 11;
+
+// SPARSE kernels: the pages a tile reads, counted through.  With sinks before its
+// first other token t_lo (0: none apart) these are the pages of the sinks, sp of
+// them, and those from page sp + gap on.  sp is even, so that a group of 32
+// columns is 32 tokens in a row.
+struct Pages {
+  int sp, gap;
+  __device__ __forceinline__ int page(int v) const { return v < sp ? v : v + gap; }
+  __device__ __forceinline__ int token(int v) const { return v < sp * kPage ? v : v + gap * kPage; }
+  // the n tokens from v on are n in a row
+  __device__ __forceinline__ bool row(int v, int n) const { return gap == 0 || v >= sp * kPage || v + n <= sp * kPage; }
+};
+__device__ __forceinline__ Pages pages_from(int t_lo, int S) {
+  Pages p;
+  p.sp = t_lo > 0 ? ((S + kPage - 1) / kPage + 1) & ~1 : 0;
+  p.gap = max(t_lo / kPage - p.sp, 0);
+  return p;
+}
 
 // A piece: blocks kb .. kb + nb - 1 of one tile for KV head h.
 struct Piece {
@@ -152,9 +176,8 @@ struct Piece {
   int full_lo, full_hi;  // [full_lo, full_hi): tokens every query of the tile attends to
   int slot;              // partial slot, -1: the whole tile
   int last;              // no piece: the end
-  int pad;
+  Pages pages;           // SPARSE
 };
-static_assert(sizeof(Piece) == 64, "");
 
 struct Tail {
   uint64_t bars[kNumBars];
@@ -180,21 +203,6 @@ struct TileGeom {
   int nb;    // blocks
 };
 
-// SPARSE kernels: the pages a tile reads, counted through.  With sinks before its
-// first other token t_lo (0: none apart) these are the pages of the sinks, sp of
-// them, and those from page sp + gap on.  sp is even, so that a group of 32
-// columns is 32 tokens in a row.
-struct Pages {
-  int sp, gap;
-  __device__ __forceinline__ Pages(int t_lo, int S) {
-    sp = t_lo > 0 ? ((S + kPage - 1) / kPage + 1) & ~1 : 0;
-    gap = max(t_lo / kPage - sp, 0);
-  }
-  __device__ __forceinline__ int page(int v) const { return v < sp ? v : v + gap; }
-  __device__ __forceinline__ int token(int v) const { return v < sp * kPage ? v : v + gap * kPage; }
-  // the n tokens from v on are n in a row
-  __device__ __forceinline__ bool row(int v, int n) const { return gap == 0 || v >= sp * kPage || v + n <= sp * kPage; }
-};
 // The parent of drafted token `node` of the row whose tokens start at `first`.
 __device__ __forceinline__ int parent_of(const ChunkAttnArgs& a, int first, int node) {
   const int p = __ldg(a.parents + first + node);
@@ -296,7 +304,7 @@ struct QueryTiles {
     g.t_lo = seen_from(g.P0, W);
     if (SPARSE && g.t_lo <= S) g.t_lo = 0;
     if constexpr (SPARSE) {
-      const int pages = (g.t_hi + kPage - 1) / kPage - Pages(g.t_lo, S).gap;
+      const int pages = (g.t_hi + kPage - 1) / kPage - pages_from(g.t_lo, S).gap;
       g.kb = 0;
       g.nb = (pages * kPage + kBlockTok<DT> - 1) / kBlockTok<DT>;
     } else {
@@ -402,7 +410,7 @@ __device__ __forceinline__ Piece piece_of(const Walk<QueryTiles<DT, SPARSE>>& w,
   }
   d.slot = b0 > 0 ? 2 * static_cast<int>(blockIdx.x) : b1 < g.nb ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
   d.last = 0;
-  d.pad = 0;
+  if constexpr (SPARSE) d.pages = pages_from(g.t_lo, w.geo.S);
   return d;
 }
 
@@ -458,7 +466,7 @@ __device__ __noinline__ void mend_rows(const ChunkAttnArgs& a, const uint32_t* n
         int P;
         const Sight sight = sight_of(a, d.tok, d.P0, d.L, d.F, j, P);
         attend_query<DT>(a.pool, a.rows, a.sc, d.i, d.h, G, P, q, d.kb * kBlockTok<DT>, (d.kb + d.nb) * kBlockTok<DT>, m,
-                         l, acc, SparseSeen{a, sight, Pages(d.t_lo, a.pool.sinks)});
+                         l, acc, SparseSeen{a, sight, d.pages});
       } else {
         const int P = d.P0 + j;
         const int t0 = max(seen_from(P, a.pool.window), d.kb * kBlockTok<DT>);
@@ -532,7 +540,7 @@ __device__ __forceinline__ void fill_skipped(const ChunkAttnArgs& a) {
 // GEN: 0 plain scores; 1 capped (at most 1e9); 2 with a distance bias, capped
 // or not, with a scale that is not positive, or a higher cap.
 template <int DT, int GEN, bool SPARSE>
-__global__ void __launch_bounds__(kAttnThreads<DT>, 1)
+__global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkAttnArgs a, const __grid_constant__ TileMaps maps,
                            const __grid_constant__ CUtensorMap qmap) {
   using F = Io<DT>;
@@ -564,9 +572,9 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   if (tid < kNumBars) {
     const int b = tid;
     int count = 1;
-    if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = 4;
+    if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = kSplitWarps<DT, SPARSE>;
     if ((b >= kBP && b < kBO) || b == kBHalf || b == kBJoined) count = 4;
-    if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT>;
+    if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT, SPARSE>;
     mbar_init(bar(b), count);
     fence_mbar_init();
   }
@@ -628,26 +636,26 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   // columns otherwise: 1100 us instead of 474 for a prompt of 8191 tokens)
   auto block = [](int kb, int nb, int b) { return GEN == 2 ? kb + nb - 1 - b : kb + b; };
   // pages of block kb that are read (SPARSE: counted through, as tokens are until token_of)
-  auto pages_in = [&](int kb, int t_lo, int t_hi, int& lo, int& hi) {
+  auto pages_in = [&](int kb, int t_lo, int t_hi, int gap, int& lo, int& hi) {
     const int first = kb * kPages;
     hi = (t_hi + kPage - 1) / kPage;
     if constexpr (SPARSE) {
       lo = first;
-      hi = min(first + kPages, hi - Pages(t_lo, a.pool.sinks).gap);
+      hi = min(first + kPages, hi - gap);
     } else {
       lo = max(first, t_lo / kPage);
       hi = min(first + kPages, hi);
     }
   };
   auto pages_of = [&](const Piece& p, int b, int& lo, int& hi) {
-    pages_in(block(p.kb, p.nb, b), p.t_lo, p.t_hi, lo, hi);
+    pages_in(block(p.kb, p.nb, b), p.t_lo, p.t_hi, SPARSE ? p.pages.gap : 0, lo, hi);
   };
-  auto token_of = [&](const Piece& p, int t) { return SPARSE ? Pages(p.t_lo, a.pool.sinks).token(t) : t; };
+  auto token_of = [&](const Piece& p, int t) { return SPARSE ? p.pages.token(t) : t; };
   // the table entry of page x of those read: its own, but the first's for a page between the sinks and the window,
   // whose entry may be anything (its tokens are masked, and zeroed as values)
   auto entry_of = [&](const Piece& p, int x) {
     if (!SPARSE) return x;
-    const int page = Pages(p.t_lo, a.pool.sinks).page(x);
+    const int page = p.pages.page(x);
     return page * kPage >= a.pool.sinks && (page + 1) * kPage <= p.t_lo ? 0 : page;
   };
   // whether any query of the tile attends to token t
@@ -659,19 +667,21 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   auto mended = [&](const Piece& p, int b) {
     int t0 = block(p.kb, p.nb, b) * N;
     if constexpr (SPARSE) {
-      const Pages pages(p.t_lo, a.pool.sinks);
-      if (!pages.row(t0, N)) return true;
-      t0 = pages.token(t0);
+      if (!p.pages.row(t0, N)) return true;
+      t0 = p.pages.token(t0);
       if (t0 + N <= min(a.pool.sinks, p.full_hi)) return false;
     }
     return t0 < p.full_lo || t0 + N > p.full_hi;
   };
 
   if (kQ8 && warp >= 12) {
-    // 3 x 144 + 80 = 4 x 128 registers a thread, what the launch has
-    if constexpr (kQ8) tc::more_registers<144>();
+    // 3 x 144 + 80 = 4 x 128 registers a thread, or 2 x 136 + 80 + 2 x 64 = 5 x 96: what the launch has
+    if constexpr (SPARSE) tc::fewer_registers<64>();
+    else if constexpr (kQ8) tc::more_registers<144>();
     // ------------------------------ q8_0 keys and values as two f16 parts ----
-    const int row = (tid - 384) >> 3, col = (tid - 384) & 7;  // 8 threads a token, 16 codes each
+    // 8 threads a token, 16 codes each; the warps' first half takes the first half of a block's pages
+    constexpr int kEach = kQ8 ? kPages * 4 / (kQ8 ? kSplitWarps<DT, SPARSE> : 1) : 1;
+    const int row = ((tid - 384) >> 3) & 15, col = (tid - 384) & 7, page0 = ((tid - 384) >> 7) * kEach;
     int gs = 0;
     bool ok = !stalled;
     for (int p = 0; ok; ++p) {
@@ -682,20 +692,27 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       for (int b = 0; b < d.nb && ok; ++b) {
         const bool mend = mended(d, b);
         const int t0 = block(d.kb, d.nb, b) * N;
+        [[maybe_unused]] unsigned ins = ~0u;  // pages whose token `row` some query of the tile attends to
+        if (SPARSE && mend) {
+          ins = 0u;
+#pragma unroll 1
+          for (int e = 0; e < kEach; ++e) ins |= in_tile(d, token_of(d, t0 + (page0 + e) * kPage + row)) ? 1u << e : 0u;
+        }
 #pragma unroll
         for (int v = 0; v < 2; ++v, ++gs) {
           const int rs = gs % kRaws, s = gs % kS;
           if (!(ok = wait(kBRaw + rs, gs / kRaws))) break;
-          const uint8_t* raw = smem + kRaw + rs * kRawBytes + row * kD + ((col ^ (row & 7)) << 4);
+          const uint8_t* raw = smem + kRaw + rs * kRawBytes + (page0 * kPage + row) * kD + ((col ^ (row & 7)) << 4);
           const __half* rsc = reinterpret_cast<const __half*>(smem + kRawScales + rs * kRawScaleBytes) +
-                              row * (kD / kQBlock) + (col >> 1);
-          uint4 code[kPages];
-          __half2 sc[kPages];
+                              (page0 * kPage + row) * (kD / kQBlock) + (col >> 1);
+          uint4 code[kEach];
+          __half2 sc[kEach];
           bool odd = false, large = false;
 #pragma unroll
-          for (int e = 0; e < kPages; ++e) {  // token `row` of page e; 0 where no query of the tile attends
-            const bool in = in_tile(d, token_of(d, t0 + e * kPage + row));
+          for (int e = 0; e < kEach; ++e) {  // token `row` of a page; 0 where no query of the tile attends
             code[e] = *reinterpret_cast<const uint4*>(raw + e * (kPage * kD));
+            const int t = t0 + e * kPage + row;
+            const bool in = SPARSE ? ins >> e & 1u : t >= d.t_lo && t < d.t_hi;
             const __half f = in ? rsc[e * kPage * (kD / kQBlock)] : __float2half_rn(0.0f);
             const unsigned bits = __half_as_ushort(f) & 0x7FFFu;
             odd = odd || bits >= kNotFinite;
@@ -705,11 +722,12 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
           if (gs >= kS && !(ok = wait(kBEmpty + s, gs / kS - 1))) break;
           uint8_t* hi = smem + kRing + s * kHalf;
 #pragma unroll
-          for (int e = 0; e < kPages; ++e) {
+          for (int e = 0; e < kEach; ++e) {
             uint4 h0, l0, h1, l1;
             q8_split8(make_uint2(code[e].x, code[e].y), sc[e], h0, l0);
             q8_split8(make_uint2(code[e].z, code[e].w), sc[e], h1, l1);
-            const uint32_t o0 = tile_vec(kPage * e + row, 2 * col), o1 = tile_vec(kPage * e + row, 2 * col + 1);
+            const int t = (page0 + e) * kPage + row;
+            const uint32_t o0 = tile_vec(t, 2 * col), o1 = tile_vec(t, 2 * col + 1);
             *reinterpret_cast<uint4*>(hi + o0) = h0;
             *reinterpret_cast<uint4*>(hi + o1) = h1;
             *reinterpret_cast<uint4*>(hi + kPart + o0) = l0;
@@ -1042,7 +1060,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
       const Piece& d = tail.piece[x];
       if (tc::uniform(d.last)) break;
       const int nb = tc::uniform(d.nb), t_lo = tc::uniform(d.t_lo), t_hi = tc::uniform(d.t_hi),
-                kb = tc::uniform(d.kb);
+                kb = tc::uniform(d.kb), gap = SPARSE ? tc::uniform(d.pages.gap) : 0;
       const bool two = tc::uniform(d.nq) * G > kTileRows / 2;
       any = true;
       for (int b = 0; b < nb && ok; ++b) {
@@ -1091,7 +1109,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         tc::commit(bar(kBEmpty + s), lead);
         if (b + 1 == nb) tc::commit(bar(kBQEmpty), lead);
         int lo, hi;
-        pages_in(block(kb, nb, b), t_lo, t_hi, lo, hi);
+        pages_in(block(kb, nb, b), t_lo, t_hi, gap, lo, hi);
         v.s = (gs + 1) % kS;
         v.lo = lo & (kPages - 1);
         v.n = hi - lo;
@@ -1119,7 +1137,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   }
   } else {
     // ------------------------------------------------------------ softmax ----
-    if constexpr (kQ8) tc::more_registers<144>();
+    if constexpr (kQ8) tc::more_registers<SPARSE ? 136 : 144>();
     const int m = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t tS = tmem + lanes + kTmemS + 128 * m, tO = tS + (kTmemO - kTmemS);
@@ -1172,7 +1190,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
           bool fast;
           [[maybe_unused]] uint32_t see[N / 32];  // what the row sees of the block, where not all rows see all
           if constexpr (SPARSE) {
-            const Pages pages(d.t_lo, a.pool.sinks);
+            const Pages& pages = d.pages;
             const int t = pages.token(t0);
             fast = pages.row(t0, N) && __all_sync(kFull, (t >= lo || t + N <= a.pool.sinks) && t + N <= hi);
             if (__builtin_expect(!fast, 0)) {
@@ -1550,7 +1568,7 @@ cudaError_t launch_attention_t(const ChunkAttnArgs& a, const TileMaps& maps, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.chunks);
-  cfg.blockDim = dim3(kAttnThreads<DT>);
+  cfg.blockDim = dim3(kAttnThreads<DT, SPARSE>);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
   cfg.attrs = attr;
