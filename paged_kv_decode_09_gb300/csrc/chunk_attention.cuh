@@ -26,7 +26,7 @@
 // Q, 9 issues the products, 10 copies K and V pages (one tensor copy each)
 // into a ring of five 32 KiB slots, 11 mends V blocks that hold tokens no
 // query of the tile attends to; with q8_0, 10 copies codes and scales into a
-// ring of their own, and 12-19 split them into the ring of slots.  Hand-overs
+// ring of their own, and 12-15 (or 12-19) split them into the ring of slots.  Hand-overs
 // by shared-memory barriers:
 //   dfull, dempty[x]  descriptor x of a piece (a tile's blocks in this range)
 //   qfull[m], qempty  Q_m landed; the piece's last scores are computed
@@ -100,10 +100,11 @@ namespace {
 constexpr int kTileRows = 256;   // (query, query head) rows of a tile: 256 / G queries
 template <int DT>
 constexpr int kBlockTok = DT == PKV_KV_Q8_0 ? 64 : 128;  // cached tokens of a block
-// Warps that split q8_0: the SPARSE kernel's larger code leaves four of them the
-// slowest of all (q8_0 trees of 32 tokens 139 us, 117 with eight); without it
-// eight take registers and schedulers from the softmax (2048 tokens over 32049
-// 1.37 ms with four, 1.43 with eight).
+// Warps that split q8_0 blocks.  The SPARSE kernels' larger code left four of
+// them the slowest of all: with eight, four for K and four for V, trees of 32
+// tokens take 119 us instead of 136, and 97 once the halves take turns as well.
+// Without it eight take registers and schedulers from the softmax (2048 tokens
+// over 32049 1.37 ms with four, 1.43 with eight).
 template <int DT, bool SPARSE>
 constexpr int kSplitWarps = DT != PKV_KV_Q8_0 ? 0 : SPARSE ? 8 : 4;
 template <int DT, bool SPARSE>
@@ -549,8 +550,9 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
   constexpr int N = kBlockTok<DT>;                   // tokens of a block
   constexpr int kPages = N / kPage;                  // its pages
   constexpr uint32_t kPart = N * kD * 2;             // bytes of one part of it
-  // The halves take a smaller tile's blocks in turn (q8_0: no registers left)
-  constexpr bool kTurns = !kQ8;
+  // The halves take a smaller tile's blocks in turn (q8_0: with eight warps to
+  // split the codes; with four those set the pace, and nothing is gained)
+  constexpr bool kTurns = !kQ8 || SPARSE;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   Tail& tail = *reinterpret_cast<Tail*>(smem + kTail);
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
   if (tid < kNumBars) {
     const int b = tid;
     int count = 1;
-    if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = kSplitWarps<DT, SPARSE>;
+    if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = 4;
     if ((b >= kBP && b < kBO) || b == kBHalf || b == kBJoined) count = 4;
     if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT, SPARSE>;
     mbar_init(bar(b), count);
@@ -679,9 +681,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
     if constexpr (SPARSE) tc::fewer_registers<64>();
     else if constexpr (kQ8) tc::more_registers<144>();
     // ------------------------------ q8_0 keys and values as two f16 parts ----
-    // 8 threads a token, 16 codes each; the warps' first half takes the first half of a block's pages
-    constexpr int kEach = kQ8 ? kPages * 4 / (kQ8 ? kSplitWarps<DT, SPARSE> : 1) : 1;
-    const int row = ((tid - 384) >> 3) & 15, col = (tid - 384) & 7, page0 = ((tid - 384) >> 7) * kEach;
+    // 8 threads a token, 16 codes each; with eight warps the first four split K blocks, the others V blocks
+    const int row = ((tid - 384) >> 3) & 15, col = (tid - 384) & 7, side = (tid - 384) >> 7;
     int gs = 0;
     bool ok = !stalled;
     for (int p = 0; ok; ++p) {
@@ -696,20 +697,21 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
         if (SPARSE && mend) {
           ins = 0u;
 #pragma unroll 1
-          for (int e = 0; e < kEach; ++e) ins |= in_tile(d, token_of(d, t0 + (page0 + e) * kPage + row)) ? 1u << e : 0u;
+          for (int e = 0; e < kPages; ++e) ins |= in_tile(d, token_of(d, t0 + e * kPage + row)) ? 1u << e : 0u;
         }
 #pragma unroll
-        for (int v = 0; v < 2; ++v, ++gs) {
-          const int rs = gs % kRaws, s = gs % kS;
-          if (!(ok = wait(kBRaw + rs, gs / kRaws))) break;
-          const uint8_t* raw = smem + kRaw + rs * kRawBytes + (page0 * kPage + row) * kD + ((col ^ (row & 7)) << 4);
+        for (int u = 0; u < (SPARSE ? 1 : 2); ++u) {
+          const int v = SPARSE ? side : u, g = gs + v;
+          const int rs = g % kRaws, s = g % kS;
+          if (!(ok = wait(kBRaw + rs, g / kRaws))) break;
+          const uint8_t* raw = smem + kRaw + rs * kRawBytes + row * kD + ((col ^ (row & 7)) << 4);
           const __half* rsc = reinterpret_cast<const __half*>(smem + kRawScales + rs * kRawScaleBytes) +
-                              (page0 * kPage + row) * (kD / kQBlock) + (col >> 1);
-          uint4 code[kEach];
-          __half2 sc[kEach];
+                              row * (kD / kQBlock) + (col >> 1);
+          uint4 code[kPages];
+          __half2 sc[kPages];
           bool odd = false, large = false;
 #pragma unroll
-          for (int e = 0; e < kEach; ++e) {  // token `row` of a page; 0 where no query of the tile attends
+          for (int e = 0; e < kPages; ++e) {  // token `row` of a page; 0 where no query of the tile attends
             code[e] = *reinterpret_cast<const uint4*>(raw + e * (kPage * kD));
             const int t = t0 + e * kPage + row;
             const bool in = SPARSE ? ins >> e & 1u : t >= d.t_lo && t < d.t_hi;
@@ -719,14 +721,14 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
             large = large || (bits >= kLargeScale && bits < kNotFinite);
             sc[e] = __half2half2(f);
           }
-          if (gs >= kS && !(ok = wait(kBEmpty + s, gs / kS - 1))) break;
+          if (g >= kS && !(ok = wait(kBEmpty + s, g / kS - 1))) break;
           uint8_t* hi = smem + kRing + s * kHalf;
 #pragma unroll
-          for (int e = 0; e < kEach; ++e) {
+          for (int e = 0; e < kPages; ++e) {
             uint4 h0, l0, h1, l1;
             q8_split8(make_uint2(code[e].x, code[e].y), sc[e], h0, l0);
             q8_split8(make_uint2(code[e].z, code[e].w), sc[e], h1, l1);
-            const int t = (page0 + e) * kPage + row;
+            const int t = e * kPage + row;
             const uint32_t o0 = tile_vec(t, 2 * col), o1 = tile_vec(t, 2 * col + 1);
             *reinterpret_cast<uint4*>(hi + o0) = h0;
             *reinterpret_cast<uint4*>(hi + o1) = h1;
@@ -744,6 +746,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
             mbar_arrive(bar(kBRawEmpty + rs));
           }
         }
+        gs += 2;
       }
       if (!ok) break;
       __syncwarp();
@@ -1238,7 +1241,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
               // are complete, S was issued after them
               tc::wait_ld();
               if (group > 0 || (kTurns ? begun : b > 0)) {
-                if constexpr (kQ8) rescale_here<DT>(tS, tO, group, b > 0, al);  // no registers for a call
+                if constexpr (kQ8) rescale_here<DT>(tS, tO, group, kTurns ? begun : b > 0, al);  // no registers for a call
                 else rescale<DT>(tS, tO, group, begun, al);
               }
             };
@@ -1404,11 +1407,22 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
 #pragma unroll
             for (int u = 0; u < 32; ++u) o[u] *= f0;
             if (join) {
-              float o1[32];
-              tc::ld32(tO + 128 + 32 * e, o1);
-              tc::wait_ld();
+              if constexpr (kQ8) {  // fewer registers at once
 #pragma unroll
-              for (int u = 0; u < 32; ++u) o[u] = fmaf(f1, o1[u], o[u]);
+                for (int x = 0; x < 32; x += 16) {
+                  uint32_t o1[16];
+                  tc::ld16w(tO + 128 + 32 * e + x, o1);
+                  tc::wait_ld();
+#pragma unroll
+                  for (int u = 0; u < 16; ++u) o[x + u] = fmaf(f1, __uint_as_float(o1[u]), o[x + u]);
+                }
+              } else {
+                float o1[32];
+                tc::ld32(tO + 128 + 32 * e, o1);
+                tc::wait_ld();
+#pragma unroll
+                for (int u = 0; u < 32; ++u) o[u] = fmaf(f1, o1[u], o[u]);
+              }
             }
             if (valid) {
               if (d.slot >= 0) {
