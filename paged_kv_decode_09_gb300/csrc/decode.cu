@@ -469,7 +469,7 @@ __device__ __forceinline__ void process_unit(uint8_t* st, const uint8_t* sc, int
 // states from shared memory: lane l owns dims 4l..4l+3 of every head.  A
 // whole segment is written to the output; otherwise the piece's partial
 // state goes to its workspace slot.
-template <int G>
+template <int G, bool EMPTY>
 __device__ __forceinline__ void piece_merge(const float* mrg_acc, const float* mrg_ml, bool whole,
                                             float* out_seg, float* part_ml, float* part_acc,
                                             long long slot, int lane) {
@@ -478,11 +478,12 @@ __device__ __forceinline__ void piece_merge(const float* mrg_acc, const float* m
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mrg_ml[(w * G + g) * 2]);
+    const float base = EMPTY && M == -INFINITY ? 0.f : M;  // no page in the piece
     float Ls = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(mrg_ml[(w * G + g) * 2] - M);
+      const float f = exp2f(mrg_ml[(w * G + g) * 2] - base);
       Ls = fmaf(f, mrg_ml[(w * G + g) * 2 + 1], Ls);
       const float4 x = *reinterpret_cast<const float4*>(mrg_acc + (w * G + g) * kD + lane * 4);
       A.x = fmaf(f, x.x, A.x);
@@ -504,6 +505,38 @@ __device__ __forceinline__ void piece_merge(const float* mrg_acc, const float* m
 }
 
 // --------------------------------------------------------------- kernel ----
+// What a segment costs a chunk besides its pages (the merge at its end, its
+// partial state, the next queries), in pages.  SINKS kernels count so many units
+// before each segment's pages, which read nothing: chunks that hold many short
+// segments then get fewer pages.  64 rows of 16 to 1018 tokens: 52.7 us without,
+// 30.8 at 8, 29.2 at 12 and 28.9 at 16 in bf16; 43.3, 28.1 at 4, 24.3 at 8 and
+// 25.2 at 12 in q8_0; 55.5, 45.9 at 4 and 47.9 at 8 in f32.  Of 64 rows of 516
+// tokens each, which gain nothing: 34.8, 33.6 at 12 in f16, 27.3, 28.9 at 8 in
+// q8_0, 53.6, 53.5 at 4 in f32.  At most a chunk's share of the pages (small
+// batches would be cut into empty pieces).
+template <int DT>
+constexpr int kSegmentPrice = DT == PKV_KV_Q8_0 ? 8 : DT == PKV_KV_F32 ? 4 : 12;
+
+// `lead` more units before each row with any: row_start counts them for one KV
+// head, as it does the pages.  Every thread of the CTA must call it.
+__device__ __forceinline__ void price_segments(int* row_start, int num_rows, int lead) {
+  __syncthreads();  // row_start[num_rows] is read
+  if (threadIdx.x < 32) {
+    int before = 0, last = 0;  // rows with pages, and row_start as it was, at the group's start
+    for (int base = 0; base < num_rows; base += 32) {
+      const int r = base + static_cast<int>(threadIdx.x);
+      const int end = r < num_rows ? row_start[r + 1] : 0;
+      int start = __shfl_up_sync(kFull, end, 1);
+      if (threadIdx.x == 0) start = last;
+      const unsigned has = __ballot_sync(kFull, r < num_rows && end > start);
+      last = __shfl_sync(kFull, end, 31);
+      if (r < num_rows) row_start[r + 1] = end + lead * (before + __popc(has & ((2u << threadIdx.x) - 1u)));
+      before += __popc(has);
+    }
+  }
+  __syncthreads();
+}
+
 // SINKS: the layer's first tokens stay visible under its window (kv_pool_set_sinks).
 // A row's units are then the pages of its sinks, from slot 0, and the pages of
 // its window; a page that holds the end of the one and the start of the other
@@ -524,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // [0] abort  [1] warps arrived at the current piece end  [2] merge-buffer generation
+  // [3] units before a segment's pages (SINKS)
   volatile int* ctl = reinterpret_cast<volatile int*>(smem + SM::kCtl);
   int* row_start = reinterpret_cast<int*>(smem + SM::kRows);
   int* lens = row_start + a.num_rows + 1;
@@ -556,6 +590,13 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
   const int sinks = SINKS ? a.sinks : 0;
   plan_rows(a.seq_lens, a.num_rows, a.bt_stride, a.window, blockIdx.x == 0 ? a.status : nullptr,
             lens, row_start, 1, sinks);
+  if constexpr (SINKS) {
+    const int price = static_cast<int>(min(static_cast<long long>(kSegmentPrice<DT>),
+                                           static_cast<long long>(row_start[a.num_rows]) * a.n_kv / gridDim.x));
+    if (threadIdx.x == 0) ctl[3] = price;
+    price_segments(row_start, a.num_rows, price);
+  }
+  auto lead = [&]() { return SINKS ? ctl[3] : 0; };  // units before a segment's pages
 
   const bool stalled = test_stall(smem_addr(smem + SM::kStall), a.test_stall_ns, ctl, a.status);
   plan_split(row_start, a.num_rows, a.n_kv, gridDim.x, a.aligned_split, split, pc);
@@ -591,22 +632,22 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
       const int npg = row_start[i + 1] - row_start[i];
       const int off = static_cast<int>(x - static_cast<long long>(a.n_kv) * row_start[i]);
       hh = off / npg;
-      const int p = off - hh * npg;  // of the pages the row reads
+      const int p = off - hh * npg - lead();  // of the pages the row reads
       int entry;
       if constexpr (SINKS) {
         const int ws = sink_window_start(lens[i], a.window, sinks), np = sink_pages(ws, sinks);
-        entry = p < np ? p : ws / kPage + p - np;
+        entry = p < np ? max(p, 0) : ws / kPage + p - np;
       } else {
         entry = window_start(lens[i], a.window) / kPage + p;
       }
       int page = __ldg(a.block_table + static_cast<long long>(i) * a.bt_stride + entry);
-      last = (p == npg - 1) ? 1 : 0;
+      last = (p == npg - 1 - lead()) ? 1 : 0;
       if (page < 0 || page >= a.num_pages) {
         record_status(a.status, PKV_DEV_BAD_PAGE);
         page = 0;
         last = 0;
       }
-      pg = page;
+      pg = SINKS && p < 0 ? -1 : page;
       row = i;
     }
   };
@@ -630,6 +671,12 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
     const int jj = u - batch;
     const int pg = __shfl_sync(kFull, c_pg, jj);
     const int hh = __shfl_sync(kFull, c_h, jj);
+    if (SINKS && pg < 0) {  // nothing to read
+      if (lane == 0) mbar_arrive(bar0 + 8 * static_cast<int>(static_cast<unsigned>(u) % R));
+      __syncwarp();
+      ++issued;
+      return;
+    }
     if (a.k_new != nullptr && __shfl_sync(kFull, c_last, jj)) {
       const int row = __shfl_sync(kFull, c_row, jj);
       append_token<DT>(a, row, hh, pg, (lens[row] - 1) % kPage, lane);  // row's k_new/v_new
@@ -678,8 +725,8 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
     const int L = lens[i];
     // first attended token of the row behind its sinks
     const int ws = SINKS ? sink_window_start(L, a.window, sinks) : window_start(L, a.window);
-    const int np = SINKS ? sink_pages(ws, sinks) : 0;  // pages of its sinks: units 0 .. np - 1
-    const int p0 = ws / kPage - np;                    // with rel >= np: the page p0 + rel
+    const int np = SINKS ? sink_pages(ws, sinks) : 0;  // pages of its sinks, before the window's
+    const int p0 = ws / kPage - np;                    // the row's page rel >= np is page p0 + rel
     const long long j = static_cast<long long>(i) * a.n_kv + h;
     int k0, k1;
     segment_chunks(sp, i, h, row_start, pc, a.num_rows, a.n_kv, k0, k1);
@@ -694,12 +741,12 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
     S.vx = kNoScale;
 
     const int r = static_cast<int>((x - c_begin) % kWarps);
-    // this warp's units of the piece: offsets rel in the segment (ints: a
+    // this warp's units of the piece: pages rel of the segment (ints: a
     // segment has fewer than 2^31 units), u its index among the warp's units
     const long long pos0 = x + ((warp - r + kWarps) % kWarps);
-    const int rel_end = static_cast<int>(b - seg_start);
+    const int rel_end = static_cast<int>(b - seg_start) - lead();
     int u = static_cast<int>((pos0 - first) / kWarps);
-    for (int rel = static_cast<int>(pos0 - seg_start); rel < rel_end; rel += kWarps, ++u) {
+    for (int rel = static_cast<int>(pos0 - seg_start) - lead(); rel < rel_end; rel += kWarps, ++u) {
       const int s = static_cast<int>(static_cast<unsigned>(u) % R);
       bool ok = !aborted && mbar_wait_bounded(bar0 + 8 * s, (static_cast<unsigned>(u) / R) & 1, ctl);
       ok = __all_sync(kFull, ok);
@@ -712,11 +759,13 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
         continue;
       }
       consumed = u + 1;
-      const bool sink = SINKS && rel < np;
-      const int t_page = (sink ? rel : p0 + rel) * kPage;  // page's first token
-      const int nvalid = min(kPage, (sink ? sinks : L) - t_page);
-      const int tlo = sink ? 0 : max(0, ws - t_page);
-      process_unit<DT, G>(ring + s * TL::kCodes, ring_sc + s * TL::kScales, tlo, nvalid, lane, S);
+      if (!SINKS || rel >= 0) {
+        const bool sink = SINKS && rel < np;
+        const int t_page = (sink ? rel : p0 + rel) * kPage;  // page's first token
+        const int nvalid = min(kPage, (sink ? sinks : L) - t_page);
+        const int tlo = sink ? 0 : max(0, ws - t_page);
+        process_unit<DT, G>(ring + s * TL::kCodes, ring_sc + s * TL::kScales, tlo, nvalid, lane, S);
+      }
       if (issued < n_units) issue();
     }
 
@@ -780,11 +829,12 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
         M[g] = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M[g] = fmaxf(M[g], mrg_ml[(w * G + g) * 2]);
+        const float base = SINKS && M[g] == -INFINITY ? 0.f : M[g];  // no page in the piece
         Ls[g] = 0.f;
         A[g] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float f = exp2f(mrg_ml[(w * G + g) * 2] - M[g]);
+          const float f = exp2f(mrg_ml[(w * G + g) * 2] - base);
           Ls[g] = fmaf(f, mrg_ml[(w * G + g) * 2 + 1], Ls[g]);
           A[g] = fmaf(f, mrg_acc[(w * G + g) * kD + d], A[g]);
         }
@@ -854,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
         __threadfence_block();
         const bool live = !ctl[0];
         if (live)
-          piece_merge<G>(mrg_acc, mrg_ml, whole, out_seg, a.part_ml, a.part_acc, k + j, lane);
+          piece_merge<G, SINKS>(mrg_acc, mrg_ml, whole, out_seg, a.part_ml, a.part_acc, k + j, lane);
         __syncwarp();
         if (lane == 0) {  // release the merge buffer for the next piece
           ctl[1] = 0;
