@@ -282,47 +282,46 @@ def kv_append(pool: KVPool, layer: int, k_new, v_new, block_table, seq_lens, str
                            stride, _ptr(seq_lens), rows, _stream(stream)), "kv_append")
 
 
+def _decode(name, pool, layer, q, new, block_table, seq_lens, scale, out, workspace, num_chunks, stream):
+    """paged_decode_attention, and with new = (k_new, v_new) pkv_decode_step."""
+    if not isinstance(seq_lens, torch.Tensor) or not isinstance(block_table, torch.Tensor) or \
+            block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
+        rows, _ = _rows(block_table, seq_lens, pool.device)
+    rows, stride = block_table.shape
+    bt = _array(block_table, torch.int32, "block_table", (rows, stride), pool)
+    lens = _array(seq_lens, torch.int32, "seq_lens", (rows,), pool)
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != HEAD_DIM:
+        _need(q, torch.float32, "q", device=pool.device)
+        raise ValueError("q must be [rows][n_q_heads][128]")
+    qp = _array(q, torch.float32, "q", shape, pool)
+    tokens = [_array(x, torch.float32, n, (rows, pool.n_kv, HEAD_DIM), pool)
+              for x, n in zip(new, ("k_new", "v_new"))]
+    n_q = shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    op = _array(out, torch.float32, "out", shape, pool)
+    if workspace is None:
+        workspace = Workspace(pool, n_q, max(rows, 1), num_chunks)
+    _call(name, pool, stream, pool.handle, layer, qp, *tokens, bt, stride, lens, rows, n_q, scale, op,
+          workspace.tensor.data_ptr(), workspace.nbytes, num_chunks or workspace.num_chunks)
+    return out
+
+
 def paged_decode_attention(pool: KVPool, layer: int, q, block_table, seq_lens, scale: float,
                            out=None, workspace: Workspace | None = None, num_chunks: int = 0,
                            stream=None):
-    rows, stride = _rows(block_table, seq_lens, pool.device)
-    _need(q, torch.float32, "q", device=pool.device)
-    if q.dim() != 3 or q.shape[0] != rows or q.shape[2] != pool.head_dim:
-        raise ValueError("q must be [rows][n_q_heads][128]")
-    n_q = q.shape[1]
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, torch.float32, "out", q.shape, pool.device)
-    if workspace is None:
-        workspace = Workspace(pool, n_q, max(rows, 1), num_chunks)
-    chunks = num_chunks or workspace.num_chunks
-    _check(lib().paged_decode_attention(pool.handle, layer, _ptr(q), _ptr(block_table), stride,
-                                        _ptr(seq_lens), rows, n_q, float(scale), _ptr(out),
-                                        _ptr(workspace.tensor), workspace.nbytes, chunks,
-                                        _stream(stream)), "paged_decode_attention")
-    return out
+    return _decode("paged_decode_attention", pool, layer, q, (), block_table, seq_lens, scale, out, workspace,
+                   num_chunks, stream)
 
 
 def decode_step(pool: KVPool, layer: int, q, k_new, v_new, block_table, seq_lens, scale: float,
                 out=None, workspace: Workspace | None = None, num_chunks: int = 0, stream=None):
     """Append each row's new token, then attend (pkv_decode_step, one launch)."""
-    rows, stride = _rows(block_table, seq_lens, pool.device)
-    _need(q, torch.float32, "q", device=pool.device)
-    shape = (rows, pool.n_kv, pool.head_dim)
-    _need(k_new, torch.float32, "k_new", shape, pool.device)
-    _need(v_new, torch.float32, "v_new", shape, pool.device)
-    n_q = q.shape[1]
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, torch.float32, "out", q.shape, pool.device)
-    if workspace is None:
-        workspace = Workspace(pool, n_q, max(rows, 1), num_chunks)
-    chunks = num_chunks or workspace.num_chunks
-    _check(lib().pkv_decode_step(pool.handle, layer, _ptr(q), _ptr(k_new), _ptr(v_new),
-                                 _ptr(block_table), stride, _ptr(seq_lens), rows, n_q,
-                                 float(scale), _ptr(out), _ptr(workspace.tensor),
-                                 workspace.nbytes, chunks, _stream(stream)), "pkv_decode_step")
-    return out
+    return _decode("pkv_decode_step", pool, layer, q, (k_new, v_new), block_table, seq_lens, scale, out, workspace,
+                   num_chunks, stream)
 
 
 class WorkspaceMQ:

@@ -12,7 +12,15 @@
 //
 // A CTA takes a row and a share of the layers' (KV head, K or V) pairs: it walks
 // the path once, from the parents up to the leaf in shared memory, and looks the
-// pages up once.
+// pages up once, as rows of KV head 0 that every pair adds its own offset to.
+//
+// What bounds it: up to some MB the chain before the first move (the leaf, the
+// parents, the walk, the table, the load, some 3 us); above, DRAM, in pieces of a
+// token of a head (256 bytes; 512 in f32).  A row's 4 to 7 moves leave a warp few
+// loads, so it takes those of several pairs together, but not of a layer or two (8
+// rows of one layer 3.3 us, 4.0 together): 32 rows of 32 layers, 28.8 MB, 11.5 us
+// with a pair at a time, 9.5 so in 1216 CTAs (9.9 in 304, 11.9 in 2048); 192 rows of 16 layers in f32, 286 MB, 51.4
+// us, 5.6 TB/s (63 in 304 CTAs, 55.7 in 608).
 #include <cstdint>
 
 #include "chunk_device.cuh"
@@ -27,9 +35,9 @@ template <int DT>
 __global__ void __launch_bounds__(32 * kWarps) tree_commit_kernel(const __grid_constant__ CommitArgs a) {
   constexpr int kRow = DT == PKV_KV_F32 ? 512 : DT == PKV_KV_Q8_0 ? 128 : 256;  // bytes of a token of a head
   constexpr int kLanes = kRow / 16, kTokens = 32 / kLanes;                      // lanes of a token, tokens of a load
-  __shared__ int parents[PKV_MAX_TREE_TOKENS];  // later the pages of the path's tokens
-  __shared__ int line[PKV_MAX_TREE_TOKENS];     // the path, at the end; later the pages they move to
-  __shared__ int path[PKV_MAX_TREE_TOKENS];
+  __shared__ int parents[PKV_MAX_TREE_TOKENS];
+  __shared__ int line[PKV_MAX_TREE_TOKENS];  // the path, at the end
+  __shared__ longlong2 moves[PKV_MAX_TREE_TOKENS];  // token rows of KV head 0 that move, and where to (-1: not)
   __shared__ int length;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i = blockIdx.x;
   const bool first = blockIdx.y == 0;  // of the row's CTAs: records and reports
@@ -68,56 +76,79 @@ __global__ void __launch_bounds__(32 * kWarps) tree_commit_kernel(const __grid_c
     int x = -1;
     if (d < n) {
       x = line[PKV_MAX_TREE_TOKENS - n + d];
-      path[d] = x;
       if (first && a.path && d < a.path_stride) a.path[static_cast<long long>(i) * a.path_stride + d] = x;
     }
     still += __syncthreads_count(x == d);
   }
   if (first && tid == 0) a.new_lens[i] = C + n;
-  for (int d = still + tid; d < n; d += blockDim.x) {  // line and parents are read: the pages of the moves
-    const int from = __ldg(bt + (C + path[d]) / kPage), to = __ldg(bt + (C + d) / kPage);
+  const int m = n - still;
+  if (m == 0) return;
+  for (int x = tid; x < m; x += blockDim.x) {
+    const int src = C + line[PKV_MAX_TREE_TOKENS - m + x], dst = C + still + x;
+    const int from = __ldg(bt + src / kPage), to = __ldg(bt + dst / kPage);
     const bool ok = from >= 0 && from < a.pool.num_pages && to >= 0 && to < a.pool.num_pages;
     if (!ok) record_status(status, PKV_DEV_BAD_PAGE);
-    parents[d] = ok ? from : -1;
-    line[d] = to;
+    const long long step = static_cast<long long>(a.pool.n_kv) * kPage;
+    moves[x] = make_longlong2(ok ? from * step + src % kPage : -1, ok ? to * step + dst % kPage : -1);
   }
   __syncthreads();
 
-  const int pairs = 2 * a.pool.n_kv, all = a.layers * pairs;
-  for (int u = blockIdx.y * kWarps + warp; u < all; u += gridDim.y * kWarps) {
-    const int layer = u / pairs, pair = u - layer * pairs, h = pair >> 1;
-    uint8_t* data = ((pair & 1) ? a.pool.v_data : a.pool.k_data) + layer * a.data_bytes;
-    auto row_of = [&](int page, int slot) {
-      return (static_cast<long long>(page) * a.pool.n_kv + h) * kPage + slot % kPage;
-    };
-    const int mine = lane / kLanes, vec = lane % kLanes;
-    for (int d0 = still; d0 < n; d0 += kTokens * kInFlight) {
+  // A unit is a layer's KV head and side.  A warp loads kBatch tokens before it
+  // stores any: those of several units where they have few, else a unit's in turn.
+  constexpr int kBatch = kTokens * kInFlight;
+  const int pairs = 2 * a.pool.n_kv, units = a.layers * pairs;
+  const int per = units >= 4 * kWarps ? max(1, kBatch / m) : 1;
+  const int mine = lane / kLanes, vec = lane % kLanes;
+  const int step = gridDim.y * kWarps * per;
+  for (int u0 = (blockIdx.y * kWarps + warp) * per; u0 < units; u0 += step) {
+    const int last = min(u0 + per, units), layer0 = u0 / pairs, pair0 = u0 - layer0 * pairs;
+    for (int d0 = 0; d0 < m; d0 += kBatch) {
       uint4 w[kInFlight];
+      uint8_t* to[kInFlight];
+      int x = d0 + mine, unit = u0, layer = layer0, pair = pair0;  // this lane's move and its unit
 #pragma unroll
-      for (int e = 0; e < kInFlight; ++e) {
-        const int d = d0 + e * kTokens + mine;
-        if (d < n && parents[d] >= 0)
-          w[e] = *reinterpret_cast<const uint4*>(data + row_of(parents[d], C + path[d]) * kRow + 16 * vec);
+      for (int e = 0; e < kInFlight; ++e, x += kTokens) {
+        while (per > 1 && x >= m) {
+          x -= m;
+          ++unit;
+          if (++pair == pairs) {
+            pair = 0;
+            ++layer;
+          }
+        }
+        to[e] = nullptr;
+        if (x < m && unit < last) {
+          const longlong2 mv = moves[x];
+          uint8_t* data = ((pair & 1) ? a.pool.v_data : a.pool.k_data) + layer * a.data_bytes +
+                          (pair >> 1) * (kPage * kRow) + 16 * vec;
+          if (mv.x >= 0) {
+            w[e] = *reinterpret_cast<const uint4*>(data + mv.x * kRow);
+            to[e] = data + mv.y * kRow;
+          }
+        }
       }
       __syncwarp();
 #pragma unroll
-      for (int e = 0; e < kInFlight; ++e) {
-        const int d = d0 + e * kTokens + mine;
-        if (d < n && parents[d] >= 0)
-          *reinterpret_cast<uint4*>(data + row_of(line[d], C + d) * kRow + 16 * vec) = w[e];
-      }
+      for (int e = 0; e < kInFlight; ++e)
+        if (to[e]) *reinterpret_cast<uint4*>(to[e]) = w[e];
       __syncwarp();
     }
     if constexpr (DT == PKV_KV_Q8_0) {  // four f16 scales a token
-      uint8_t* scales = ((pair & 1) ? a.pool.v_scales : a.pool.k_scales) + layer * a.scale_bytes;
-      for (int d0 = still; d0 < n; d0 += 32) {
-        const int d = d0 + lane;
-        const bool ok = d < n && parents[d] >= 0;
-        uint2 w = make_uint2(0u, 0u);
-        if (ok) w = *reinterpret_cast<const uint2*>(scales + row_of(parents[d], C + path[d]) * 8);
-        __syncwarp();
-        if (ok) *reinterpret_cast<uint2*>(scales + row_of(line[d], C + d) * 8) = w;
-        __syncwarp();
+      int layer = layer0, pair = pair0;
+      for (int unit = u0; unit < last; ++unit) {
+        uint8_t* scales = ((pair & 1) ? a.pool.v_scales : a.pool.k_scales) + layer * a.scale_bytes + (pair >> 1) * (kPage * 8);
+        for (int d0 = 0; d0 < m; d0 += 32) {
+          const longlong2 mv = d0 + lane < m ? moves[d0 + lane] : make_longlong2(-1, -1);
+          uint2 w = make_uint2(0u, 0u);
+          if (mv.x >= 0) w = *reinterpret_cast<const uint2*>(scales + mv.x * 8);
+          __syncwarp();
+          if (mv.x >= 0) *reinterpret_cast<uint2*>(scales + mv.y * 8) = w;
+          __syncwarp();
+        }
+        if (++pair == pairs) {
+          pair = 0;
+          ++layer;
+        }
       }
     }
   }
@@ -125,12 +156,15 @@ __global__ void __launch_bounds__(32 * kWarps) tree_commit_kernel(const __grid_c
 
 template <int DT>
 cudaError_t launch(const CommitArgs& a, cudaStream_t st) {
+  // Each CTA walks its row's path and looks its pages up before it moves anything: two waves of four an SM
+  constexpr int kCtas = 2 * 4 * 152;
   const int groups = (a.layers * 2 * a.pool.n_kv + kWarps - 1) / kWarps;
+  const int most = kCtas / a.rows.num_rows + 1;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.rows.num_rows, groups < 1 ? 1 : groups < 65535 ? groups : 65535);
+  cfg.gridDim = dim3(a.rows.num_rows, groups < 1 ? 1 : groups < most ? groups : most);
   cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = st;
   cfg.attrs = attr;
