@@ -156,7 +156,8 @@ pkv_status kv_pool_get_window(const pkv_pool *pool, int layer, int *window);
  * PKV_MAX_SINKS] -> PKV_ERR_INVALID_ARG.  Host-side descriptor state, read when
  * a call is queued.  paged_decode_attention, paged_decode_attention_static,
  * pkv_decode_step, paged_chunk_attention and paged_tree_attention serve layers
- * with sinks; the two-launch form (paged_decode_split), the several-query calls
+ * with sinks; the two-launch form (paged_decode_split; paged_decode_plan and
+ * paged_decode_combine know windows alone), the several-query calls
  * (paged_decode_attention_mq, pkv_decode_step_mq: take paged_chunk_attention) and
  * paged_attention_mass return PKV_ERR_UNSUPPORTED on them. */
 pkv_status kv_pool_set_sinks(pkv_pool *pool, int layer, int sinks);

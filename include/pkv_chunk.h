@@ -84,8 +84,10 @@ pkv_status kv_rope_append(const pkv_pool *pool, int layer, const void *q, long l
  * and the query attends to t in [max(0, P + 1 - W), min(L_i, max(P + 1, F))):
  * causal, but within the row's first F = prefix_lens[i] tokens seen from
  * everywhere (prefix_lens NULL: F = 0), and W the layer's sliding window (0:
- * none).  slopes is fp32 [n_q_heads], prefix_lens int32 [num_rows], both on the
- * device; softcap 0 means none, others are 1e-30 to 1e30. */
+ * none).  On a layer with S sinks (kv_pool_set_sinks; paged_chunk_attention
+ * alone) it attends to t < S below that end as well.  slopes is fp32 [n_q_heads],
+ * prefix_lens int32 [num_rows], both on the device; softcap 0 means none, others
+ * are 1e-30 to 1e30. */
 typedef struct pkv_scores {
     float scale;
     float softcap;

@@ -301,10 +301,10 @@ def _decode(name, pool, layer, q, new, block_table, seq_lens, scale, out, worksp
               for x, n in zip(new, ("k_new", "v_new"))]
     n_q = shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     op = _array(out, torch.float32, "out", shape, pool)
     if workspace is None:
-        workspace = Workspace(pool, n_q, max(rows, 1), num_chunks)
+        workspace = _made(stream, Workspace, pool, n_q, max(rows, 1), num_chunks)
     _call(name, pool, stream, pool.handle, layer, qp, *tokens, bt, stride, lens, rows, n_q, scale, op,
           workspace.tensor.data_ptr(), workspace.nbytes, num_chunks or workspace.num_chunks)
     return out

@@ -280,7 +280,11 @@ pkv_status kv_tree_commit(const pkv_pool* pool, int first_layer, int num_layers,
   if (!aligned(parents, 4) || !aligned(leaves, 4) || !aligned(path, 4) || !aligned(new_lens, 4))
     return fail(PKV_ERR_INVALID_ARG, "parents / leaves / path / new_lens not 4-byte aligned");
   // other CTAs read these while one writes
-  if (new_lens == seq_lens || new_lens == leaves) return fail(PKV_ERR_INVALID_ARG, "new_lens must be an array of its own");
+  for (const int32_t* in : {seq_lens, leaves, parents, cu_seqlens, block_table}) {
+    if (new_lens == in) return fail(PKV_ERR_INVALID_ARG, "new_lens must be an array of its own");
+    if (path && path == in) return fail(PKV_ERR_INVALID_ARG, "path must be an array of its own");
+  }
+  if (new_lens == path) return fail(PKV_ERR_INVALID_ARG, "path must not be new_lens");
   a.layers = num_layers;
   pkv::pool_layer_bytes(pool, &a.data_bytes, &a.scale_bytes);
   a.rows = rows_of(cu_seqlens, seq_lens, block_table, bt_stride, num_rows, total_tokens);

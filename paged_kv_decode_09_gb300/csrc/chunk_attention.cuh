@@ -107,6 +107,17 @@ constexpr int kBlockTok = DT == PKV_KV_Q8_0 ? 64 : 128;  // cached tokens of a b
 // over 32049 1.37 ms with four, 1.43 with eight).
 template <int DT, bool SPARSE>
 constexpr int kSplitWarps = DT != PKV_KV_Q8_0 ? 0 : SPARSE ? 8 : 4;
+// Registers a thread of the q8_0 kernels' roles.  Their sum is what the launch
+// has (4 x 128 and 5 x 96 a thread): the warps that ask for more would wait for
+// ever otherwise, so the launcher compares.
+template <bool SPARSE>
+constexpr int kSoftmaxRegisters = SPARSE ? 136 : 144;
+template <bool SPARSE>
+constexpr int kSplitRegisters = SPARSE ? 64 : 144;
+constexpr int kOtherRegisters = 80;
+template <bool SPARSE>
+constexpr int kRegisterShares = 8 * kSoftmaxRegisters<SPARSE> + 4 * kOtherRegisters +
+                                kSplitWarps<PKV_KV_Q8_0, SPARSE> * kSplitRegisters<SPARSE>;  // of a lane of each warp
 template <int DT, bool SPARSE>
 constexpr int kAttnThreads = kPlanThreads + 32 * kSplitWarps<DT, SPARSE>;
 // How far from a tile's end a boundary moves there, in blocks (chunk_plan): with
@@ -677,9 +688,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
   };
 
   if (kQ8 && warp >= 12) {
-    // 3 x 144 + 80 = 4 x 128 registers a thread, or 2 x 136 + 80 + 2 x 64 = 5 x 96: what the launch has
-    if constexpr (SPARSE) tc::fewer_registers<64>();
-    else if constexpr (kQ8) tc::more_registers<144>();
+    if constexpr (SPARSE) tc::fewer_registers<kSplitRegisters<SPARSE>>();
+    else if constexpr (kQ8) tc::more_registers<kSplitRegisters<SPARSE>>();
     // ------------------------------ q8_0 keys and values as two f16 parts ----
     // 8 threads a token, 16 codes each; with eight warps the first four split K blocks, the others V blocks
     const int row = ((tid - 384) >> 3) & 15, col = (tid - 384) & 7, side = (tid - 384) >> 7;
@@ -754,7 +764,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
     }
     if (warp == 12) fill_skipped(a);
   } else if (warp >= 8) {
-  if constexpr (kQ8) tc::fewer_registers<80>();
+  if constexpr (kQ8) tc::fewer_registers<kOtherRegisters>();
   if (stalled) {
     // test hook: every warp gave up
   } else if (warp == 8) {
@@ -1140,7 +1150,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
   }
   } else {
     // ------------------------------------------------------------ softmax ----
-    if constexpr (kQ8) tc::more_registers<SPARSE ? 136 : 144>();
+    if constexpr (kQ8) tc::more_registers<kSoftmaxRegisters<SPARSE>>();
     const int m = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t tS = tmem + lanes + kTmemS + 128 * m, tO = tS + (kTmemO - kTmemS);
@@ -1572,6 +1582,12 @@ cudaError_t launch_attention_t(const ChunkAttnArgs& a, const TileMaps& maps, con
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !granted[dev].load(std::memory_order_relaxed)) {
+    if constexpr (DT == PKV_KV_Q8_0) {  // see kRegisterShares
+      cudaFuncAttributes f;
+      e = cudaFuncGetAttributes(&f, chunk_attention_kernel<DT, GEN, SPARSE>);
+      if (e != cudaSuccess) return e;
+      if (f.numRegs * kAttnThreads<DT, SPARSE> < 32 * kRegisterShares<SPARSE>) return cudaErrorLaunchOutOfResources;
+    }
     e = cudaFuncSetAttribute(chunk_attention_kernel<DT, GEN, SPARSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;

@@ -448,3 +448,31 @@ def one_row(c, i, n, L):
     r.cu = torch.tensor([0, n])
     r.stored = lambda which, _: c.stored(which, i, L)
     return r
+
+
+@pytest.mark.parametrize("kv", [api.F16, api.Q8_0])
+def test_pages_beyond_32_bits(kv):
+    """Rows in the last pages of a pool whose K alone is more than 4 GiB: the bits of the same rows in a small pool."""
+    rows, n_kv = [(33, 200), (1, 700), (64, 90)], 8
+    c = R.Chunk(kv, n_kv, 4, rows, seed=3)
+    per_page = n_kv * 16 * 128 * (1 if kv == api.Q8_0 else 2)
+    pages = (5 << 30) // per_page
+    big = api.KVPool(1, pages, n_kv, kv, device="cuda")
+    for x, y in zip(arrays(big), arrays(c.pool)):
+        x[0, pages - c.num_pages:] = y[0]
+    bt = torch.where(c.bt >= 0, c.bt + (pages - c.num_pages), c.bt)
+    trees, parents = drafted(c)
+    leaves = torch.tensor([32, 0, 63], dtype=torch.int32, device=c.device)
+    q = c.normal(c.tokens, c.n_q, 128, dtype=R.IO[kv])
+    x = c.normal(3, c.n_q, 128)
+    got = []
+    for pool, table in ((c.pool, c.bt), (big, bt)):
+        pool.set_window(0, 100)
+        pool.set_sinks(0, 5)
+        out = [api.paged_tree_attention(pool, 0, q, parents, c.cu, table, c.lens, SCALE),
+               api.paged_decode_attention(pool, 0, x, table, c.lens, SCALE, num_chunks=1),
+               api.kv_tree_commit(pool, parents, leaves, c.cu, table, c.lens)]
+        assert pool.read_status() == 0
+        got.append(out + [y[0, -c.num_pages:].contiguous().view(torch.uint8) for y in arrays(pool)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)

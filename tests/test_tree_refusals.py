@@ -79,6 +79,8 @@ def commit(pools, kv=api.F16):
     (dict(rows=-1), INVALID), (dict(rows=2049), UNSUPPORTED), (dict(tokens=-1), INVALID), (dict(new=None), INVALID),
     (dict(new=ODD), INVALID), (dict(path=FAKE, path_stride=0), INVALID), (dict(path=ODD), INVALID),
     (dict(new=ctypes.c_void_p((1 << 20) + 8192)), INVALID), (dict(new=ctypes.c_void_p((1 << 20) + 4096)), INVALID),
+    (dict(new=FAKE), INVALID), (dict(path=ctypes.c_void_p((1 << 20) + 8192)), INVALID), (dict(path=FAKE), INVALID),
+    (dict(path=ctypes.c_void_p((1 << 20) + 4096 * 3)), INVALID),
 ])
 def test_commit(lib, pools, changes, status):
     refused(lib, "kv_tree_commit", commit(pools), changes, status)
