@@ -26,7 +26,7 @@
 // Q, 9 issues the products, 10 copies K and V pages (one tensor copy each)
 // into a ring of five 32 KiB slots, 11 mends V blocks that hold tokens no
 // query of the tile attends to; with q8_0, 10 copies codes and scales into a
-// ring of their own, and 12-15 (or 12-19) split them into the ring of slots.  Hand-overs
+// ring of their own, and 12-15 split them into the ring of slots.  Hand-overs
 // by shared-memory barriers:
 //   dfull, dempty[x]  descriptor x of a piece (a tile's blocks in this range)
 //   qfull[m], qempty  Q_m landed; the piece's last scores are computed
@@ -100,26 +100,8 @@ namespace {
 constexpr int kTileRows = 256;   // (query, query head) rows of a tile: 256 / G queries
 template <int DT>
 constexpr int kBlockTok = DT == PKV_KV_Q8_0 ? 64 : 128;  // cached tokens of a block
-// Warps that split q8_0 blocks.  The SPARSE kernels' larger code left four of
-// them the slowest of all: with eight, four for K and four for V, trees of 32
-// tokens take 119 us instead of 136, and 97 once the halves take turns as well.
-// Without it eight take registers and schedulers from the softmax (2048 tokens
-// over 32049 1.37 ms with four, 1.43 with eight).
-template <int DT, bool SPARSE>
-constexpr int kSplitWarps = DT != PKV_KV_Q8_0 ? 0 : SPARSE ? 8 : 4;
-// Registers a thread of the q8_0 kernels' roles.  Their sum is what the launch
-// has (4 x 128 and 5 x 96 a thread): the warps that ask for more would wait for
-// ever otherwise, so the launcher compares.
-template <bool SPARSE>
-constexpr int kSoftmaxRegisters = SPARSE ? 136 : 144;
-template <bool SPARSE>
-constexpr int kSplitRegisters = SPARSE ? 64 : 144;
-constexpr int kOtherRegisters = 80;
-template <bool SPARSE>
-constexpr int kRegisterShares = 8 * kSoftmaxRegisters<SPARSE> + 4 * kOtherRegisters +
-                                kSplitWarps<PKV_KV_Q8_0, SPARSE> * kSplitRegisters<SPARSE>;  // of a lane of each warp
-template <int DT, bool SPARSE>
-constexpr int kAttnThreads = kPlanThreads + 32 * kSplitWarps<DT, SPARSE>;
+template <int DT>
+constexpr int kAttnThreads = DT == PKV_KV_Q8_0 ? 512 : kPlanThreads;
 // How far from a tile's end a boundary moves there, in blocks (chunk_plan): with
 // q8_0's blocks of 64 tokens, from one block away; with blocks of 128, never.
 template <int DT>
@@ -161,8 +143,8 @@ enum : int {
   kBStall,
   kNumBars,
 };
-template <int DT, bool SPARSE>  // softmax, products, copies, and mending or splitting
-constexpr int kDescReaders = DT == PKV_KV_Q8_0 ? 10 + kSplitWarps<DT, SPARSE> : 11;
+template <int DT>
+constexpr int kDescReaders = DT == PKV_KV_Q8_0 ? 14 : 11;  // softmax, products, copies, and mending or splitting
 
 // SPARSE kernels: the pages a tile reads, counted through.  With sinks before its
 // first other token t_lo (0: none apart) these are the pages of the sinks, sp of
@@ -552,7 +534,7 @@ __device__ __forceinline__ void fill_skipped(const ChunkAttnArgs& a) {
 // GEN: 0 plain scores; 1 capped (at most 1e9); 2 with a distance bias, capped
 // or not, with a scale that is not positive, or a higher cap.
 template <int DT, int GEN, bool SPARSE>
-__global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
+__global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkAttnArgs a, const __grid_constant__ TileMaps maps,
                            const __grid_constant__ CUtensorMap qmap) {
   using F = Io<DT>;
@@ -561,9 +543,8 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
   constexpr int N = kBlockTok<DT>;                   // tokens of a block
   constexpr int kPages = N / kPage;                  // its pages
   constexpr uint32_t kPart = N * kD * 2;             // bytes of one part of it
-  // The halves take a smaller tile's blocks in turn (q8_0: with eight warps to
-  // split the codes; with four those set the pace, and nothing is gained)
-  constexpr bool kTurns = !kQ8 || SPARSE;
+  // The halves take a smaller tile's blocks in turn (q8_0: no registers left)
+  constexpr bool kTurns = !kQ8;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   Tail& tail = *reinterpret_cast<Tail*>(smem + kTail);
@@ -587,7 +568,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
     int count = 1;
     if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = 4;
     if ((b >= kBP && b < kBO) || b == kBHalf || b == kBJoined) count = 4;
-    if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT, SPARSE>;
+    if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT>;
     mbar_init(bar(b), count);
     fence_mbar_init();
   }
@@ -688,11 +669,10 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
   };
 
   if (kQ8 && warp >= 12) {
-    if constexpr (SPARSE) tc::fewer_registers<kSplitRegisters<SPARSE>>();
-    else if constexpr (kQ8) tc::more_registers<kSplitRegisters<SPARSE>>();
+    // 3 x 144 + 80 = 4 x 128 registers a thread, what the launch has
+    if constexpr (kQ8) tc::more_registers<144>();
     // ------------------------------ q8_0 keys and values as two f16 parts ----
-    // 8 threads a token, 16 codes each; with eight warps the first four split K blocks, the others V blocks
-    const int row = ((tid - 384) >> 3) & 15, col = (tid - 384) & 7, side = (tid - 384) >> 7;
+    const int row = (tid - 384) >> 3, col = (tid - 384) & 7;  // 8 threads a token, 16 codes each
     int gs = 0;
     bool ok = !stalled;
     for (int p = 0; ok; ++p) {
@@ -710,10 +690,9 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
           for (int e = 0; e < kPages; ++e) ins |= in_tile(d, token_of(d, t0 + e * kPage + row)) ? 1u << e : 0u;
         }
 #pragma unroll
-        for (int u = 0; u < (SPARSE ? 1 : 2); ++u) {
-          const int v = SPARSE ? side : u, g = gs + v;
-          const int rs = g % kRaws, s = g % kS;
-          if (!(ok = wait(kBRaw + rs, g / kRaws))) break;
+        for (int v = 0; v < 2; ++v, ++gs) {
+          const int rs = gs % kRaws, s = gs % kS;
+          if (!(ok = wait(kBRaw + rs, gs / kRaws))) break;
           const uint8_t* raw = smem + kRaw + rs * kRawBytes + row * kD + ((col ^ (row & 7)) << 4);
           const __half* rsc = reinterpret_cast<const __half*>(smem + kRawScales + rs * kRawScaleBytes) +
                               row * (kD / kQBlock) + (col >> 1);
@@ -731,15 +710,14 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
             large = large || (bits >= kLargeScale && bits < kNotFinite);
             sc[e] = __half2half2(f);
           }
-          if (g >= kS && !(ok = wait(kBEmpty + s, g / kS - 1))) break;
+          if (gs >= kS && !(ok = wait(kBEmpty + s, gs / kS - 1))) break;
           uint8_t* hi = smem + kRing + s * kHalf;
 #pragma unroll
           for (int e = 0; e < kPages; ++e) {
             uint4 h0, l0, h1, l1;
             q8_split8(make_uint2(code[e].x, code[e].y), sc[e], h0, l0);
             q8_split8(make_uint2(code[e].z, code[e].w), sc[e], h1, l1);
-            const int t = e * kPage + row;
-            const uint32_t o0 = tile_vec(t, 2 * col), o1 = tile_vec(t, 2 * col + 1);
+            const uint32_t o0 = tile_vec(kPage * e + row, 2 * col), o1 = tile_vec(kPage * e + row, 2 * col + 1);
             *reinterpret_cast<uint4*>(hi + o0) = h0;
             *reinterpret_cast<uint4*>(hi + o1) = h1;
             *reinterpret_cast<uint4*>(hi + kPart + o0) = l0;
@@ -756,7 +734,6 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
             mbar_arrive(bar(kBRawEmpty + rs));
           }
         }
-        gs += 2;
       }
       if (!ok) break;
       __syncwarp();
@@ -764,7 +741,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
     }
     if (warp == 12) fill_skipped(a);
   } else if (warp >= 8) {
-  if constexpr (kQ8) tc::fewer_registers<kOtherRegisters>();
+  if constexpr (kQ8) tc::fewer_registers<80>();
   if (stalled) {
     // test hook: every warp gave up
   } else if (warp == 8) {
@@ -1150,7 +1127,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
   }
   } else {
     // ------------------------------------------------------------ softmax ----
-    if constexpr (kQ8) tc::more_registers<kSoftmaxRegisters<SPARSE>>();
+    if constexpr (kQ8) tc::more_registers<144>();
     const int m = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t tS = tmem + lanes + kTmemS + 128 * m, tO = tS + (kTmemO - kTmemS);
@@ -1186,6 +1163,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
             lo = sight.lo;
             hi = sight.C;
           }
+          __syncwarp();
         }
         float slope2 = 0.0f;
         bool behind = true;
@@ -1217,6 +1195,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
                 // (the drafted tokens lie behind the gap)
                 if (a.parents) sight.ancestors(a, t0 + pages.gap * kPage, see);
               }
+              __syncwarp();  // the loads from tensor memory want the whole warp at once
             }
           } else {
             fast = __all_sync(kFull, t0 >= lo && t0 + N <= hi);
@@ -1251,7 +1230,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
               // are complete, S was issued after them
               tc::wait_ld();
               if (group > 0 || (kTurns ? begun : b > 0)) {
-                if constexpr (kQ8) rescale_here<DT>(tS, tO, group, kTurns ? begun : b > 0, al);  // no registers for a call
+                if constexpr (kQ8) rescale_here<DT>(tS, tO, group, b > 0, al);  // no registers for a call
                 else rescale<DT>(tS, tO, group, begun, al);
               }
             };
@@ -1417,22 +1396,11 @@ __global__ void __launch_bounds__(kAttnThreads<DT, SPARSE>, 1)
 #pragma unroll
             for (int u = 0; u < 32; ++u) o[u] *= f0;
             if (join) {
-              if constexpr (kQ8) {  // fewer registers at once
+              float o1[32];
+              tc::ld32(tO + 128 + 32 * e, o1);
+              tc::wait_ld();
 #pragma unroll
-                for (int x = 0; x < 32; x += 16) {
-                  uint32_t o1[16];
-                  tc::ld16w(tO + 128 + 32 * e + x, o1);
-                  tc::wait_ld();
-#pragma unroll
-                  for (int u = 0; u < 16; ++u) o[x + u] = fmaf(f1, __uint_as_float(o1[u]), o[x + u]);
-                }
-              } else {
-                float o1[32];
-                tc::ld32(tO + 128 + 32 * e, o1);
-                tc::wait_ld();
-#pragma unroll
-                for (int u = 0; u < 32; ++u) o[u] = fmaf(f1, o1[u], o[u]);
-              }
+              for (int u = 0; u < 32; ++u) o[u] = fmaf(f1, o1[u], o[u]);
             }
             if (valid) {
               if (d.slot >= 0) {
@@ -1582,12 +1550,6 @@ cudaError_t launch_attention_t(const ChunkAttnArgs& a, const TileMaps& maps, con
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !granted[dev].load(std::memory_order_relaxed)) {
-    if constexpr (DT == PKV_KV_Q8_0) {  // see kRegisterShares
-      cudaFuncAttributes f;
-      e = cudaFuncGetAttributes(&f, chunk_attention_kernel<DT, GEN, SPARSE>);
-      if (e != cudaSuccess) return e;
-      if (f.numRegs * kAttnThreads<DT, SPARSE> < 32 * kRegisterShares<SPARSE>) return cudaErrorLaunchOutOfResources;
-    }
     e = cudaFuncSetAttribute(chunk_attention_kernel<DT, GEN, SPARSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;
@@ -1598,7 +1560,7 @@ cudaError_t launch_attention_t(const ChunkAttnArgs& a, const TileMaps& maps, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.chunks);
-  cfg.blockDim = dim3(kAttnThreads<DT, SPARSE>);
+  cfg.blockDim = dim3(kAttnThreads<DT>);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
   cfg.attrs = attr;
