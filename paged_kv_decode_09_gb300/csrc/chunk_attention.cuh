@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
   if (tid < kNumBars) {
     const int b = tid;
     int count = 1;
-    if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = 4;
+    if ((b < kBEmpty && kQ8) || (b >= kBRawEmpty && b < kBS)) count = SPARSE ? 2 : 4;
     if ((b >= kBP && b < kBO) || b == kBHalf || b == kBJoined) count = 4;
     if (b >= kBDescEmpty && b < kBDescEmpty + kDescs) count = kDescReaders<DT>;
     mbar_init(bar(b), count);
@@ -672,7 +672,11 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     // 3 x 144 + 80 = 4 x 128 registers a thread, what the launch has
     if constexpr (kQ8) tc::more_registers<144>();
     // ------------------------------ q8_0 keys and values as two f16 parts ----
-    const int row = (tid - 384) >> 3, col = (tid - 384) & 7;  // 8 threads a token, 16 codes each
+    // 8 threads a token, 16 codes each.  SPARSE, whose larger code leaves these warps the slowest of all: two of them
+    // take the K blocks and two the V blocks, so that the waits of the one stand beside the work of the other (trees of
+    // 32 tokens 132 -> 105 us, 2048 tokens with sinks over 32049 258 -> 222).
+    constexpr int kEach = SPARSE ? 2 * kPages : kPages, kRows = SPARSE ? 8 : 16;  // tokens a thread, and how far apart
+    const int row = ((tid - 384) >> 3) & (kRows - 1), col = (tid - 384) & 7, side = (tid - 384) >> 6;
     int gs = 0;
     bool ok = !stalled;
     for (int p = 0; ok; ++p) {
@@ -687,37 +691,38 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         if (SPARSE && mend) {
           ins = 0u;
 #pragma unroll 1
-          for (int e = 0; e < kPages; ++e) ins |= in_tile(d, token_of(d, t0 + e * kPage + row)) ? 1u << e : 0u;
+          for (int e = 0; e < kEach; ++e) ins |= in_tile(d, token_of(d, t0 + e * kRows + row)) ? 1u << e : 0u;
         }
 #pragma unroll
-        for (int v = 0; v < 2; ++v, ++gs) {
-          const int rs = gs % kRaws, s = gs % kS;
-          if (!(ok = wait(kBRaw + rs, gs / kRaws))) break;
+        for (int u = 0; u < (SPARSE ? 1 : 2); ++u) {
+          const int v = SPARSE ? side : u, g = gs + v;
+          const int rs = g % kRaws, s = g % kS;
+          if (!(ok = wait(kBRaw + rs, g / kRaws))) break;
           const uint8_t* raw = smem + kRaw + rs * kRawBytes + row * kD + ((col ^ (row & 7)) << 4);
           const __half* rsc = reinterpret_cast<const __half*>(smem + kRawScales + rs * kRawScaleBytes) +
                               row * (kD / kQBlock) + (col >> 1);
-          uint4 code[kPages];
-          __half2 sc[kPages];
+          uint4 code[kEach];
+          __half2 sc[kEach];
           bool odd = false, large = false;
 #pragma unroll
-          for (int e = 0; e < kPages; ++e) {  // token `row` of a page; 0 where no query of the tile attends
-            code[e] = *reinterpret_cast<const uint4*>(raw + e * (kPage * kD));
-            const int t = t0 + e * kPage + row;
+          for (int e = 0; e < kEach; ++e) {  // a token; 0 where no query of the tile attends
+            code[e] = *reinterpret_cast<const uint4*>(raw + e * (kRows * kD));
+            const int t = t0 + e * kRows + row;
             const bool in = SPARSE ? ins >> e & 1u : t >= d.t_lo && t < d.t_hi;
-            const __half f = in ? rsc[e * kPage * (kD / kQBlock)] : __float2half_rn(0.0f);
+            const __half f = in ? rsc[e * kRows * (kD / kQBlock)] : __float2half_rn(0.0f);
             const unsigned bits = __half_as_ushort(f) & 0x7FFFu;
             odd = odd || bits >= kNotFinite;
             large = large || (bits >= kLargeScale && bits < kNotFinite);
             sc[e] = __half2half2(f);
           }
-          if (gs >= kS && !(ok = wait(kBEmpty + s, gs / kS - 1))) break;
+          if (g >= kS && !(ok = wait(kBEmpty + s, g / kS - 1))) break;
           uint8_t* hi = smem + kRing + s * kHalf;
 #pragma unroll
-          for (int e = 0; e < kPages; ++e) {
+          for (int e = 0; e < kEach; ++e) {
             uint4 h0, l0, h1, l1;
             q8_split8(make_uint2(code[e].x, code[e].y), sc[e], h0, l0);
             q8_split8(make_uint2(code[e].z, code[e].w), sc[e], h1, l1);
-            const uint32_t o0 = tile_vec(kPage * e + row, 2 * col), o1 = tile_vec(kPage * e + row, 2 * col + 1);
+            const uint32_t o0 = tile_vec(kRows * e + row, 2 * col), o1 = tile_vec(kRows * e + row, 2 * col + 1);
             *reinterpret_cast<uint4*>(hi + o0) = h0;
             *reinterpret_cast<uint4*>(hi + o1) = h1;
             *reinterpret_cast<uint4*>(hi + kPart + o0) = l0;
@@ -734,6 +739,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
             mbar_arrive(bar(kBRawEmpty + rs));
           }
         }
+        gs += 2;
       }
       if (!ok) break;
       __syncwarp();
