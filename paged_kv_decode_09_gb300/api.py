@@ -171,6 +171,7 @@ class KVPool:
         self.device = torch.device(device)
         if self.device.index is None:
             self.device = torch.device(self.device.type, torch.cuda.current_device())
+        self.index = self.device.index
         shape = (num_layers, num_pages, n_kv_heads, PAGE, head_dim)
         sshape = (num_layers, num_pages, n_kv_heads, PAGE, head_dim // Q8_BLOCK)
         if tensors is None:
@@ -441,6 +442,7 @@ def paged_decode_combine(seq_lens, n_q_heads: int, n_kv_heads: int, bt_stride: i
 # The kernels behind these calls take a few microseconds for a decode step, so their arguments are looked at
 # with few attribute reads; what does not fit is looked at again by _need, for its message.
 _KIND = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+_Tensor, _int32 = torch.Tensor, torch.int32
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
@@ -451,10 +453,21 @@ class _Scores(ctypes.Structure):  # pkv_scores
 
 def _array(t, dtype, name, shape, pool):
     """The address of a contiguous tensor of this dtype and shape on the pool's device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and
-            t.get_device() == pool.device.index):
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and
+            t.get_device() == pool.index):
         _need(t, dtype, name, shape, pool.device)
     return t.data_ptr()
+
+
+def _row_ints(pool, rows, *named):
+    """The addresses of int32 arrays [rows], given as tensor, name, tensor, name .."""
+    shape, index, out = (rows,), pool.index, []
+    for t, name in zip(named[::2], named[1::2]):
+        if not (isinstance(t, _Tensor) and t.dtype is _int32 and t.shape == shape and t.is_contiguous() and
+                t.get_device() == index):
+            _need(t, _int32, name, shape, pool.device)
+        out.append(t.data_ptr())
+    return out
 
 
 def _optional(t, dtype, name, shape, pool):
@@ -474,7 +487,7 @@ def _token_array(t, name, tokens, heads, dtype, pool):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != pool.device.index:
+    if t.get_device() != pool.index:
         raise ValueError(f"{name} is on {t.device}, expected {pool.device}")
     shape = t.shape
     if len(shape) != 3 or shape[2] != HEAD_DIM or (tokens is not None and shape[0] != tokens) or \
@@ -498,7 +511,7 @@ def _made(stream, make, *args, **kw):
 def _call(name, pool, stream, *args):
     """The C entry `name` on the pool's device and the given stream, or its current one: launches go to the
     current device."""
-    index = pool.device.index
+    index = pool.index
     raw = _raw_stream(index) if stream is None else stream.cuda_stream
     fn = getattr(_lib, name)
     if _current_device() == index:
@@ -588,7 +601,7 @@ class WorkspaceMass:
 
 
 def _scratch(workspace, pool):
-    if workspace.tensor.get_device() != pool.device.index:
+    if workspace.tensor.get_device() != pool.index:
         raise ValueError(f"workspace is on {workspace.tensor.device}, expected {pool.device}")
     return workspace.tensor.data_ptr(), workspace.nbytes, workspace.num_chunks
 
@@ -654,16 +667,15 @@ def kv_tree_commit(pool: KVPool, parents, leaves, cu_seqlens, block_table, seq_l
     tokens = parents.shape[0]
     if path is not None and (not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[0] != rows):
         raise ValueError("path must be a tensor [rows][stride]")
-    lens = _array(seq_lens, torch.int32, "seq_lens", (rows,), pool)
     if new_lens is None:
         new_lens = _made(stream, torch.empty_like, seq_lens)
+    lens, new, leaf = _row_ints(pool, rows, seq_lens, "seq_lens", new_lens, "new_lens", leaves, "leaves")
     _call("kv_tree_commit", pool, stream, pool.handle, first_layer,
           pool.num_layers - first_layer if num_layers is None else num_layers,
-          _array(parents, torch.int32, "parents", (tokens,), pool),
-          _array(leaves, torch.int32, "leaves", (rows,), pool),
+          _array(parents, torch.int32, "parents", (tokens,), pool), leaf,
           _array(cu_seqlens, torch.int32, "cu_seqlens", (rows + 1,), pool), tokens, bt, stride, lens, rows,
           None if path is None else _array(path, torch.int32, "path", path.shape, pool),
-          1 if path is None else path.shape[1], _array(new_lens, torch.int32, "new_lens", (rows,), pool))
+          1 if path is None else path.shape[1], new)
     return new_lens
 
 

@@ -517,22 +517,46 @@ __device__ __forceinline__ void piece_merge(const float* mrg_acc, const float* m
 template <int DT>
 constexpr int kSegmentPrice = DT == PKV_KV_Q8_0 ? 8 : DT == PKV_KV_F32 ? 4 : 12;
 
-// `lead` more units before each row with any: row_start counts them for one KV
-// head, as it does the pages.  Every thread of the CTA must call it.
-__device__ __forceinline__ void price_segments(int* row_start, int num_rows, int lead) {
-  __syncthreads();  // row_start[num_rows] is read
+// The start of a row's window behind S sinks, its first tokens, which stay
+// visible: 0 where the window reaches them, so that the row attends to all of [0,
+// L); else it attends to [0, S) and [sink_window_start, L).
+__device__ __forceinline__ int sink_window_start(int L, int window, int sinks) {
+  const int ws = window_start(L, window);
+  return ws > sinks ? ws : 0;
+}
+// Pages of the sinks of a row whose window starts at ws (0 where it has none apart).
+__device__ __forceinline__ int sink_pages(int ws, int sinks) { return ws > 0 ? (sinks + kPage - 1) / kPage : 0; }
+
+// plan_rows for a layer with sinks: row_start counts the pages of each row's sinks
+// and window, and before them the segment's price, which *price receives.
+__device__ __forceinline__ void plan_sink_rows(const DecodeArgs& a, int most, int32_t* status, int* lens,
+                                               int* row_start, volatile int* price) {
+  plan_rows(a.seq_lens, a.num_rows, a.bt_stride, 0, status, lens, row_start);  // lengths; all pages
   if (threadIdx.x < 32) {
-    int before = 0, last = 0;  // rows with pages, and row_start as it was, at the group's start
-    for (int base = 0; base < num_rows; base += 32) {
-      const int r = base + static_cast<int>(threadIdx.x);
-      const int end = r < num_rows ? row_start[r + 1] : 0;
-      int start = __shfl_up_sync(kFull, end, 1);
-      if (threadIdx.x == 0) start = last;
-      const unsigned has = __ballot_sync(kFull, r < num_rows && end > start);
-      last = __shfl_sync(kFull, end, 31);
-      if (r < num_rows) row_start[r + 1] = end + lead * (before + __popc(has & ((2u << threadIdx.x) - 1u)));
-      before += __popc(has);
+    const int lane = threadIdx.x;
+    auto pages = [&](int r) {
+      const int L = r < a.num_rows ? lens[r] : 0, ws = sink_window_start(L, a.window, a.sinks);
+      return (L + kPage - 1) / kPage - ws / kPage + sink_pages(ws, a.sinks);
+    };
+    long long all = 0;
+    for (int r = lane; r < a.num_rows; r += 32) all += pages(r);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
+    const int lead = static_cast<int>(min(static_cast<long long>(most), all * a.n_kv / gridDim.x));
+    int carry = 0;
+    for (int base = 0; base < a.num_rows; base += 32) {
+      const int r = base + lane;
+      int v = pages(r);
+      v += v > 0 ? lead : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += u;
+      }
+      if (r < a.num_rows) row_start[r + 1] = carry + v;
+      carry += __shfl_sync(kFull, v, 31);
     }
+    if (lane == 0) *price = lead;
   }
   __syncthreads();
 }
@@ -588,13 +612,11 @@ __global__ void __launch_bounds__(kThreads, DT == PKV_KV_Q8_0   ? PKV_Q8_CTAS_PE
   grid_dependency_wait();
   grid_launch_dependents();
   const int sinks = SINKS ? a.sinks : 0;
-  plan_rows(a.seq_lens, a.num_rows, a.bt_stride, a.window, blockIdx.x == 0 ? a.status : nullptr,
-            lens, row_start, 1, sinks);
   if constexpr (SINKS) {
-    const int price = static_cast<int>(min(static_cast<long long>(kSegmentPrice<DT>),
-                                           static_cast<long long>(row_start[a.num_rows]) * a.n_kv / gridDim.x));
-    if (threadIdx.x == 0) ctl[3] = price;
-    price_segments(row_start, a.num_rows, price);
+    plan_sink_rows(a, kSegmentPrice<DT>, blockIdx.x == 0 ? a.status : nullptr, lens, row_start, ctl + 3);
+  } else {
+    plan_rows(a.seq_lens, a.num_rows, a.bt_stride, a.window, blockIdx.x == 0 ? a.status : nullptr,
+              lens, row_start);
   }
   auto lead = [&]() { return SINKS ? ctl[3] : 0; };  // units before a segment's pages
 

@@ -266,27 +266,17 @@ __device__ __forceinline__ int window_start(int L, int window) {
   return window > 0 && L > window ? L - window : 0;
 }
 
-// The same behind S sinks, the row's first tokens, which stay visible: 0 where
-// the window reaches them, so that the row attends to all of [0, L); else the
-// row attends to [0, S) and [sink_window_start, L).
-__device__ __forceinline__ int sink_window_start(int L, int window, int sinks) {
-  const int ws = window_start(L, window);
-  return ws > sinks ? ws : 0;
-}
-// Pages of the sinks of a row whose window starts at ws (0 where it has none apart).
-__device__ __forceinline__ int sink_pages(int ws, int sinks) { return ws > 0 ? (sinks + kPage - 1) / kPage : 0; }
-
 // The per-CTA plan: validated lengths and the exclusive prefix sum of the
 // pages each row reads, in shared memory.  lens[i] is seq_lens[i] clamped to
 // [0, 16 * bt_stride] (a clamp records PKV_DEV_BAD_LENGTH); a row reads the
 // pages holding tokens [window_start, L), block-table entries
 // window_start / 16 onwards; row_start has num_rows + 1 entries.  Rows
 // shorter than min_len (the queries of a several-query step) read nothing
-// and record PKV_DEV_BAD_LENGTH.  With sinks a row reads their pages too.  Warp
-// 0 scans; every thread of the CTA must call it.
+// and record PKV_DEV_BAD_LENGTH.  Warp 0 scans; every thread of the CTA must
+// call it.
 __device__ __forceinline__ void plan_rows(const int32_t* __restrict__ seq_lens, int num_rows,
                                           int bt_stride, int window, int32_t* status, int* lens,
-                                          int* row_start, int min_len = 1, int sinks = 0) {
+                                          int* row_start, int min_len = 1) {
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int carry = 0;
@@ -308,8 +298,7 @@ __device__ __forceinline__ void plan_rows(const int32_t* __restrict__ seq_lens, 
         L = 0;
         lens[r] = 0;
       }
-      const int ws = sink_window_start(L, window, sinks);
-      int v = L > 0 ? (L + kPage - 1) / kPage - ws / kPage + sink_pages(ws, sinks) : 0;
+      int v = L > 0 ? (L + kPage - 1) / kPage - window_start(L, window) / kPage : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(kFull, v, o);
