@@ -697,6 +697,10 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
         for (int u = 0; u < (SPARSE ? 1 : 2); ++u) {
           const int v = SPARSE ? side : u, g = gs + v;
           const int rs = g % kRaws, s = g % kS;
+          // With an odd ring its stages go to K and V in turn: the stage's copy before this one is the other warps' to
+          // wait for, and until it has landed the parity of this one's is that of the copy before it.  So those warps'
+          // release of the stage comes first.
+          if (SPARSE && g >= kRaws && !(ok = wait(kBRawEmpty + rs, g / kRaws - 1))) break;
           if (!(ok = wait(kBRaw + rs, g / kRaws))) break;
           const uint8_t* raw = smem + kRaw + rs * kRawBytes + row * kD + ((col ^ (row & 7)) << 4);
           const __half* rsc = reinterpret_cast<const __half*>(smem + kRawScales + rs * kRawScaleBytes) +

@@ -199,6 +199,36 @@ def test_two_calls_at_once():
         assert torch.equal(o, out) and torch.equal(z, lse)
 
 
+@pytest.mark.parametrize("kv", TYPES)
+def test_many_calls_back_to_back(kv):
+    """Thousands of calls that nothing waits between, on three sets of inputs in turn: the bits of the first, and no wait
+    that gave up."""
+    sets = []
+    for seed in range(3):
+        c = R.Chunk(kv, 8, 4, [(128, 9000 + 500 * seed), (7, 4000), (30, 2500 + seed)], seed=seed)
+        c.pool.set_window(0, 1500)
+        c.pool.set_sinks(0, 40)
+        trees, parents = drafted(c)
+        q = c.normal(c.tokens, c.n_q, 128, dtype=R.IO[kv])
+        sets.append((c, parents, q, api.WorkspaceChunk(c.pool, c.n_q), torch.zeros_like(q), torch.zeros_like(q)))
+
+    def calls(tree, chunk):
+        for (c, parents, q, ws, _, _), a, b in zip(sets, tree, chunk):
+            api.paged_tree_attention(c.pool, 0, q, parents, c.cu, c.bt, c.lens, SCALE, out=a, workspace=ws)
+            api.paged_chunk_attention(c.pool, 0, q, c.cu, c.bt, c.lens, SCALE, out=b, workspace=ws)
+
+    first = [torch.empty_like(x[2]) for x in sets], [torch.empty_like(x[2]) for x in sets]
+    calls(*first)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for _ in range(100):
+            calls([x[4] for x in sets], [x[5] for x in sets])
+        torch.cuda.synchronize()
+        for x, a, b in zip(sets, *first):
+            assert torch.equal(x[4], a) and torch.equal(x[5], b)
+            assert x[0].pool.read_status() == 0
+
+
 def test_nothing_to_do_and_bad_pages():
     c = R.Chunk(api.F16, 2, 2, [(0, 5), (0, 0)], seed=1)
     assert api.paged_tree_attention(c.pool, 0, torch.empty(0, 4, 128, dtype=torch.float16, device=c.device),
