@@ -306,8 +306,9 @@ def _decode(name, pool, layer, q, new, block_table, seq_lens, scale, out, worksp
     op = _array(out, torch.float32, "out", shape, pool)
     if workspace is None:
         workspace = _made(stream, Workspace, pool, n_q, max(rows, 1), num_chunks)
-    _call(name, pool, stream, pool.handle, layer, qp, *tokens, bt, stride, lens, rows, n_q, scale, op,
-          workspace.tensor.data_ptr(), workspace.nbytes, num_chunks or workspace.num_chunks)
+    ws, nbytes, chunks = _scratch(workspace, pool)
+    _call(name, pool, stream, pool.handle, layer, qp, *tokens, bt, stride, lens, rows, n_q, float(scale), op, ws, nbytes,
+          num_chunks or chunks)
     return out
 
 

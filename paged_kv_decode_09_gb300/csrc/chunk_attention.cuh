@@ -78,7 +78,11 @@
 // of its window, counted through (Pages), so that neither leaves a block half
 // empty.  In a tree, a query sees the context before it and, of the row's new
 // tokens, its ancestors: they are found by walking up the parents, once for a
-// block that holds any, while the block's scores are computed.
+// block that holds any, while the block's scores are computed.  Trees of 64
+// tokens in 8 rows of 1K to 6K, bf16: 43.4 us (a causal chunk of those sizes
+// 42.6), 670 TFLOP/s, 39 of them this kernel's; a prompt of 8191 tokens under a
+// window of 2048 with 4 sinks 205.6 us, 1170 TFLOP/s, of which the merge of 152
+// split tiles takes 12.
 #pragma once
 
 #include <atomic>
@@ -674,7 +678,7 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
     // ------------------------------ q8_0 keys and values as two f16 parts ----
     // 8 threads a token, 16 codes each.  SPARSE, whose larger code leaves these warps the slowest of all: two of them
     // take the K blocks and two the V blocks, so that the waits of the one stand beside the work of the other (trees of
-    // 32 tokens 132 -> 105 us, 2048 tokens with sinks over 32049 258 -> 222).
+    // 32 tokens 132 -> 106 us, 2048 tokens with sinks over 32049 258 -> 226).
     constexpr int kEach = SPARSE ? 2 * kPages : kPages, kRows = SPARSE ? 8 : 16;  // tokens a thread, and how far apart
     const int row = ((tid - 384) >> 3) & (kRows - 1), col = (tid - 384) & 7, side = (tid - 384) >> 6;
     int gs = 0;
