@@ -1,5 +1,6 @@
 """Layers whose first tokens stay visible under their window (kv_pool_set_sinks), on the GPU against the 64-bit
 definition: the single-token step, the fused append, and chunk attention."""
+import ctypes
 import math
 
 import pytest
@@ -188,6 +189,20 @@ def test_no_window_no_effect():
             set_layer(c, window, sinks)
             assert torch.equal(plain, api.paged_decode_attention(c.pool, 0, q, c.bt, c.lens, SCALE, num_chunks=1))
             T.check(c, q, api.paged_decode_attention(c.pool, 0, q, c.bt, c.lens, SCALE), None, SCALE)
+
+
+def test_step_without_a_workspace():
+    """The entry point with scratch of the library's own serves sinks as well."""
+    c = R.Chunk(api.Q8_0, 2, 4, [(1, L) for L in (700, 40, 3, 1500)], seed=3)
+    set_layer(c, 200, 33)
+    q = c.normal(4, c.n_q, 128)
+    out = torch.zeros_like(q)
+    fn = api.lib().paged_decode_attention_static
+    fn.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                   ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]
+    assert fn(c.pool.handle, 0, q.data_ptr(), c.bt.data_ptr(), c.bt.shape[1], c.lens.data_ptr(), 4, c.n_q, SCALE,
+              out.data_ptr(), 0, torch.cuda.current_stream().cuda_stream) == 0
+    check_rows(c, q, out, window=200, sinks=33)
 
 
 def test_calls_that_refuse_sinks():
