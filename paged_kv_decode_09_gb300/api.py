@@ -294,7 +294,7 @@ def _decode(name, pool, layer, q, new, block_table, seq_lens, scale, out, worksp
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     shape = q.shape
-    if len(shape) != 3 or shape[0] != rows or shape[2] != HEAD_DIM:
+    if len(shape) != 3 or shape[2] != HEAD_DIM or (shape[0] != rows and not (new and shape[0] > rows)):
         _need(q, torch.float32, "q", device=pool.device)
         raise ValueError("q must be [rows][n_q_heads][128]")
     qp = _array(q, torch.float32, "q", shape, pool)
@@ -321,7 +321,8 @@ def paged_decode_attention(pool: KVPool, layer: int, q, block_table, seq_lens, s
 
 def decode_step(pool: KVPool, layer: int, q, k_new, v_new, block_table, seq_lens, scale: float,
                 out=None, workspace: Workspace | None = None, num_chunks: int = 0, stream=None):
-    """Append each row's new token, then attend (pkv_decode_step, one launch)."""
+    """Append each row's new token, then attend (pkv_decode_step, one launch).  q may have more rows than the
+    block table: the first ones are its, and the rows of out, which is like q, behind them are left as they are."""
     return _decode("pkv_decode_step", pool, layer, q, (k_new, v_new), block_table, seq_lens, scale, out, workspace,
                    num_chunks, stream)
 
