@@ -77,11 +77,14 @@
 // visible: a tile's blocks are made of the pages of the sinks and then of those
 // of its window, counted through (Pages), so that neither leaves a block half
 // empty.  In a tree, a query sees the context before it and, of the row's new
-// tokens, its ancestors: they are found by walking up the parents, once for a
-// block that holds any, while the block's scores are computed.  Trees of 64
-// tokens in 8 rows of 1K to 6K, bf16: 43.4 us (a causal chunk of those sizes
+// tokens, its ancestors: they are found by walking up the parents from the query,
+// for a block that holds any, while the block's scores are computed.  Under a
+// window a piece's start walks to the root as well, for the query's depth (a
+// chain of 1000 tokens over 3000, window 1500: 824 us, 2103 with that walk for
+// every masked block; without a window 675, its causal chunk 50).  Trees of 64
+// tokens in 8 rows of 1K to 6K, bf16: 43.3 us (a causal chunk of those sizes
 // 42.6), 670 TFLOP/s, 39 of them this kernel's; a prompt of 8191 tokens under a
-// window of 2048 with 4 sinks 205.6 us, 1170 TFLOP/s, of which the merge of 152
+// window of 2048 with 4 sinks 205.2 us, 1170 TFLOP/s, of which the merge of 152
 // split tiles takes 12.
 #pragma once
 
@@ -1202,8 +1205,10 @@ __global__ void __launch_bounds__(kAttnThreads<DT>, 1)
 #pragma unroll
               for (int e = 0; e < N / 32; ++e) see[e] = ~0u;
               if (valid) {
-                int at;
-                const Sight sight = sight_of(a, d.tok, d.P0, d.L, d.F, jq, at);
+                // The depth was walked at the piece's start, and lo = P + 1 - W holds it.  A query whose lo is 0 sees
+                // everything before it: what its window leaves out are sinks.
+                const int W = lo > 0 ? a.pool.window : 0;
+                const Sight sight{lo, hi, a.pool.sinks, W, d.tok - d.F, a.parents ? d.F + jq : -1, lo + W - 1 - d.P0};
 #pragma unroll
                 for (int e = 0; e < N / 32; ++e) see[e] = sight.context(pages.token(t0 + 32 * e));
                 // (the drafted tokens lie behind the gap)
