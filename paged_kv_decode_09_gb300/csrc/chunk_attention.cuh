@@ -357,14 +357,15 @@ struct Io {
   // (the largest, 2^(8 + 7), is still below f16's 65504); bf16 has the range.
   [[maybe_unused]] static constexpr float kShift = DT == PKV_KV_BF16 ? 0.0f : 7.0f;
   [[maybe_unused]] static constexpr float kScale = DT == PKV_KV_BF16 ? 1.0f : 128.0f;
-  // two packed values times f
+  // Two packed values times f.  A maximum raised by 25 or more is a factor that f16 holds as 0, though the weights, up
+  // to 2^15, leave something: their product is made in fp32.
   static __device__ __forceinline__ uint32_t scale(uint32_t w, float f) {
     if constexpr (kType == PKV_KV_BF16) {
       const __nv_bfloat162 h = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(f));
       return *reinterpret_cast<const uint32_t*>(&h);
     } else {
-      const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(f));
-      return *reinterpret_cast<const uint32_t*>(&h);
+      const float2 x = values(w);
+      return pack(x.x * f, x.y * f);
     }
   }
   static __device__ __forceinline__ float2 values(uint32_t w) {
