@@ -60,8 +60,9 @@ pkv_status paged_tree_attention(const pkv_pool *pool, int layer, const void *q, 
  *             value records PKV_DEV_BAD_TREE and stands for -1
  *   path      int32 [num_rows][path_stride] or NULL: receives path_d at [i][d], d <
  *             min(a, path_stride); the other entries are left as they are
- *   new_lens  int32 [num_rows]; not seq_lens or leaves.  A skipped row receives its
- *             seq_lens[i]
+ *   new_lens  int32 [num_rows].  A skipped row receives its seq_lens[i]
+ * path and new_lens are arrays of their own, none of the inputs.  Of the parents,
+ * those of the accepted token and its ancestors are looked at.
  * Block-table entries outside the pool record PKV_DEV_BAD_PAGE; the tokens
  * concerned are not moved.  A page behind C_i that two rows of the call share
  * must not be in a path's way.  Every type of pool.  One launch. */

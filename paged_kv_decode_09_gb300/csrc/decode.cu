@@ -512,8 +512,14 @@ __device__ __forceinline__ void piece_merge(const float* mrg_acc, const float* m
 // 30.8 at 8, 29.2 at 12 and 28.9 at 16 in bf16; 43.3, 28.1 at 4, 24.3 at 8 and
 // 25.2 at 12 in q8_0; 55.5, 45.9 at 4 and 47.9 at 8 in f32.  Of 64 rows of 516
 // tokens each, which gain nothing: 34.8, 33.6 at 12 in f16, 27.3, 28.9 at 8 in
-// q8_0, 53.6, 53.5 at 4 in f32.  At most a chunk's share of the pages (small
-// batches would be cut into empty pieces).
+// q8_0, 53.6, 53.5 at 4 in f32; of 32 rows under a window of 4096: 91.1, 90.5 in
+// f16, 60.9, 60.4 in q8_0, 163.5, 163.8 in f32 (in q8_0 the code for it costs
+// more than the cuts do: 58.5 without it).
+// At most a chunk's share of the pages: small batches would be cut into empty
+// pieces, and a merge counts on it.  Under the uniform split a chunk is at least
+// as long as a price then, so that of a segment's pieces only the first may hold
+// no page, and the second holds one: merge_segment_warp takes two pieces at a time
+// and has no guard for a pair whose maxima are both -inf.
 template <int DT>
 constexpr int kSegmentPrice = DT == PKV_KV_Q8_0 ? 8 : DT == PKV_KV_F32 ? 4 : 12;
 

@@ -18,9 +18,11 @@
 // parents, the walk, the table, the load, some 3 us); above, DRAM, in pieces of a
 // token of a head (256 bytes; 512 in f32).  A row's 4 to 7 moves leave a warp few
 // loads, so it takes those of several pairs together, but not of a layer or two (8
-// rows of one layer 3.3 us, 4.0 together): 32 rows of 32 layers, 28.8 MB, 11.5 us
-// with a pair at a time, 9.5 so in 1216 CTAs (9.9 in 304, 11.9 in 2048); 192 rows of 16 layers in f32, 286 MB, 51.4
-// us, 5.6 TB/s (63 in 304 CTAs, 55.7 in 608).
+// rows of one layer 3.3 us, 4.0 together): 32 rows of 32 layers, 28.8 MB, 9.5 us
+// in 1216 CTAs (9.9 in 304, 11.9 in 2048), with a pair at a time 10.7 (9.8 in 304,
+// 13.6 in 2048); 192 rows of 16 layers in f32, 286 MB, 51.4 us, 5.6 TB/s (63 in
+// 304 CTAs, 55.7 in 608).  In q8_0, 15.3 MB of the former rows, 13.3 us: the scales
+// of a warp's pairs go one pair after the other, a trip to memory each.
 #include <cstdint>
 
 #include "chunk_device.cuh"
